@@ -61,6 +61,10 @@ typedef enum {
                                   > max_context_len: sequence b's output rows are zeros */
 #define PA_DEV_BAD_SLOT 4u     /* slot >= num_blocks * block_size: that token is not written */
 #define PA_DEV_BAD_PAIR 8u     /* src or dst outside [0, num_blocks): that pair is skipped */
+#define PA_DEV_BAD_POS 32u     /* position outside [0, max_positions): that token is skipped */
+#define PA_DEV_BAD_SCALE 64u   /* a block scale that is no power of two in [2^-100, 2^120]: the
+                                  block's tokens are left out of the softmax, or its head's new
+                                  rows are not written */
 #define PA_DEV_TIMEOUT 16u     /* a pipeline wait inside a tensor-core kernel gave up
                                   (bounded at 1 s): outputs of that launch are unspecified */
 
@@ -437,6 +441,133 @@ const char* pa_status_string(int status);
 int pa_decode_plan(int dtype, int B, int Hq, int Hkv, int D, int block_size,
                    int max_context_len, int partition_size, int* kernel, int* num_partitions,
                    int* partition_tokens);
+
+/*
+ * Rotary append: pa_reshape_and_cache_kv with the rotary position embedding
+ * applied on the way, so that no separate pass reads and writes q and k.
+ *
+ * pa_rope_and_cache_kv -- for each token t with slot s = slot_mapping[t] and
+ * position p = positions[t], over pairs (x_a, x_b) of the first rot_dim elements
+ * of each query and key head:
+ *   x_a' = x_a cos_sin[p][i] - x_b cos_sin[p][rot_dim / 2 + i]
+ *   x_b' = x_b cos_sin[p][i] + x_a cos_sin[p][rot_dim / 2 + i]
+ * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved, i <
+ * rot_dim / 2; the elements behind rot_dim are kept. In fp32, each product and
+ * sum rounded to nearest (no fused multiply-add). Rotated query heads go to
+ * query_out, rotated key heads and the value heads to the pools.
+ * query, query_out  [T, Hq, D] of src_dtype (PA_F32, PA_F16 or PA_BF16);
+ *               query_out may be query itself (rotated in place), otherwise
+ *               the two do not overlap. Hq = 0 with NULL: keys only;
+ * key, value    [T, Hkv, D] of src_dtype;
+ * *_stride      elements from one token to the next (>= heads * D, a multiple
+ *               of 16 bytes; a token's heads are dense), so the arrays may be
+ *               slices of one fused projection;
+ * positions     [T] int64; a position outside [0, max_positions) sets
+ *               PA_DEV_BAD_POS and skips the token (nothing of it is written);
+ * cos_sin       [max_positions, rot_dim] float: rot_dim / 2 cosines, then
+ *               rot_dim / 2 sines per position;
+ * rot_dim       a multiple of 16, at most D;
+ * key_cache, k_dtype, k_scale, value_cache, v_dtype, v_scale
+ *               as pa_reshape_and_cache_kv (an FP8 pool gets the rotated
+ *               fp32 value over its scale, rounded once);
+ * slot_mapping  [T] int64; a negative slot (padding) skips the token, its
+ *               query row included; a slot past the pool sets PA_DEV_BAD_SLOT
+ *               and skips it too. Two tokens on one slot: as
+ *               pa_reshape_and_cache.
+ */
+int pa_rope_and_cache_kv(void* query_out, int64_t query_out_stride, const void* query,
+                         int64_t query_stride, const void* key, int64_t key_stride,
+                         const void* value, int64_t value_stride, int src_dtype,
+                         const int64_t* positions, const float* cos_sin, int max_positions,
+                         int rot_dim, int interleaved, void* key_cache, int k_dtype, float k_scale,
+                         void* value_cache, int v_dtype, float v_scale,
+                         const int64_t* slot_mapping, int T, int Hq, int Hkv, int D,
+                         int block_size, int num_blocks, uint32_t* err_flag, void* stream);
+
+/*
+ * Block-scaled 8-bit cache: pools of E4M3 codes with one scale per physical
+ * block and KV head and pool, so no calibrated pool-wide scale is needed:
+ *   K_b[i][h] = value(code) * k_scales[block][h],  V_b[i][h] likewise,
+ *   key_cache, value_cache  [num_blocks, block_size, Hkv, D] uint8 codes;
+ *   k_scales, v_scales      [num_blocks, Hkv] float, each a power of two 2^e
+ *                           with -100 <= e <= 120 (of blocks in use).
+ * A power of two costs an E4M3 code nothing (its grid is relative) and makes
+ * every division by a scale exact.
+ *
+ * pa_rope_and_cache_blk8 -- pa_rope_and_cache_kv into such pools. Per block,
+ * head and pool, with need = the smallest 2^e (e >= -100) such that amax <=
+ * 448 * 2^e over the finite elements of the call's rows of the block:
+ *  - a call that writes the block's offset 0 starts the block: its scale
+ *    becomes need, whatever it was, and rows that the call does not write are
+ *    left as they are (they hold no token);
+ *  - otherwise the scale becomes max(old, need), and when that grows it the
+ *    rows the call does not write are rounded to the new scale.
+ *  A row's code is the fp32 (rotated) value over the scale, rounded to nearest
+ *  even, saturating (infinities become +-448, NaN 0x7F).
+ * Tokens of one block must be consecutive in slot_mapping (as a sequence's
+ * tokens are; padding between them ends the run); the same block named again
+ * after another one, or one slot named twice, is a caller error: which rows
+ * and scale land is unspecified.
+ * cos_sin NULL (with positions NULL and Hq = 0): no rotation, the rows as they
+ * are. A block whose scale is no valid power of two and whose offset 0 is not
+ * written sets PA_DEV_BAD_SCALE and keeps its rows.
+ */
+int pa_rope_and_cache_blk8(void* query_out, int64_t query_out_stride, const void* query,
+                           int64_t query_stride, const void* key, int64_t key_stride,
+                           const void* value, int64_t value_stride, int src_dtype,
+                           const int64_t* positions, const float* cos_sin, int max_positions,
+                           int rot_dim, int interleaved, void* key_cache, void* value_cache,
+                           float* k_scales, float* v_scales, const int64_t* slot_mapping, int T,
+                           int Hq, int Hkv, int D, int block_size, int num_blocks,
+                           uint32_t* err_flag, void* stream);
+
+/*
+ * pa_copy_scales -- the scales of copied blocks: for each pair p, row
+ * block_mapping[p][0] of both source arrays to row block_mapping[p][1] of the
+ * destination ones, beside pa_copy_blocks (the same arrays as source and
+ * destination) or pa_swap_blocks (the other pool's scales, device memory or
+ * page-locked host memory) of the codes. Pairs, ids and errors as there.
+ */
+int pa_copy_scales(float* dst_k_scales, float* dst_v_scales, const float* src_k_scales,
+                   const float* src_v_scales, const int64_t* block_mapping, int num_pairs, int Hkv,
+                   int src_blocks, int dst_blocks, uint32_t* err_flag, void* stream);
+
+/*
+ * pa_decode_window_kv -- pa_decode_kv over a sliding window and a few first
+ * tokens: sequence b's query attends the tokens
+ *   t < context_lens[b]  with  t >= context_lens[b] - window  or  t < num_sinks.
+ * window        >= 1; num_sinks >= 0. Blocks that hold none of these tokens,
+ *               and their table entries, are not read (a cache may have freed
+ *               them). context_lens still counts every token.
+ * workspace     device scratch of at least pa_window_workspace_size(...) bytes,
+ *               256-byte aligned, or NULL when that size is 0; its contents do
+ *               not matter before or after.
+ * Other arguments, types, shapes and errors as pa_decode_kv.
+ */
+size_t pa_window_workspace_size(int B, int Hq, int Hkv, int D, int max_context_len, int window,
+                                int num_sinks);
+int pa_decode_window_kv(void* out, int out_dtype, const void* query, int q_dtype,
+                        const void* key_cache, int k_dtype, float k_scale, const void* value_cache,
+                        int v_dtype, float v_scale, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens, int B, int Hq, int Hkv,
+                        int D, int block_size, int num_blocks, float scale, int window,
+                        int num_sinks, int max_context_len, void* workspace,
+                        size_t workspace_bytes, uint32_t* err_flag, void* stream);
+
+/*
+ * pa_decode_blk8 -- decode attention over the block-scaled 8-bit cache, of all
+ * tokens (window 0) or of a window and first tokens as above (window >= 1).
+ * query         [B, Hq, D] of q_dtype (PA_F32, PA_F16 or PA_BF16); out of
+ *               PA_F32 or q_dtype. A block with an invalid scale sets
+ *               PA_DEV_BAD_SCALE and is left out of the softmax.
+ * Other arguments, the workspace and errors as pa_decode_window_kv.
+ */
+int pa_decode_blk8(void* out, int out_dtype, const void* query, int q_dtype, const void* key_cache,
+                   const void* value_cache, const float* k_scales, const float* v_scales,
+                   const int32_t* block_tables, int max_blocks_per_seq,
+                   const int32_t* context_lens, int B, int Hq, int Hkv, int D, int block_size,
+                   int num_blocks, float scale, int window, int num_sinks, int max_context_len,
+                   void* workspace, size_t workspace_bytes, uint32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }

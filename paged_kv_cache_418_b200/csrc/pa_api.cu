@@ -23,17 +23,6 @@ namespace {
 
 constexpr int kDefaultPartition = 512;
 
-bool supported_shape(int Hq, int Hkv, int D, int bs) {
-  if (Hkv <= 0 || Hq <= 0 || Hq % Hkv) return false;
-  const int G = Hq / Hkv;
-  return (D == 64 || D == 128) && (bs == 16 || bs == 32) &&
-         (G == 1 || G == 2 || G == 4 || G == 8 || G == 16);
-}
-
-int esize_of(int dtype) { return dtype == PA_F32 ? 4 : (dtype == PA_FP8_E4M3 ? 1 : 2); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Upper bound of the prefix partitions of a shared-prefix decode (one per tile).
 int max_prefix_slots(int max_shared_blocks, int block_size) {
   return (max_shared_blocks * block_size + kPrefixTile - 1) / kPrefixTile;
@@ -192,18 +181,6 @@ int pa_decode_plan(int dtype, int B, int Hq, int Hkv, int D, int block_size, int
 }  // extern "C"
 
 namespace {
-
-bool scale_ok(float x) { return std::isfinite(x) && x > 0.f; }
-
-// Pool element types a decode takes for a query of q_dtype: both the query's
-// type; both FP8; or, for a 16-bit query, one FP8 pool and one of its type.
-bool pool_types_ok(int q_dtype, int k_dtype, int v_dtype) {
-  const bool kf = k_dtype == PA_FP8_E4M3, vf = v_dtype == PA_FP8_E4M3;
-  if (!kf && k_dtype != q_dtype) return false;
-  if (!vf && v_dtype != q_dtype) return false;
-  if (kf != vf && q_dtype == PA_F32) return false;
-  return true;
-}
 
 // Shared body of the decode entry points. q_dtype: query element type;
 // k_dtype / v_dtype: pool element types (q_dtype, or PA_FP8_E4M3 read times

@@ -121,6 +121,28 @@ __device__ __forceinline__ void flag_error(uint32_t* err_flag, uint32_t bit) {
   if (err_flag) atomicOr(err_flag, bit);
 }
 
+// Scales of the block-scaled 8-bit cache: 2^e with e in [kMinScaleExp,
+// kMaxScaleExp]. Every finite fp32 magnitude over 2^-100 * 448 fits one, and
+// 2^-e is a normal fp32 number, so dividing by a scale is exact.
+constexpr int kMinScaleExp = -100, kMaxScaleExp = 120;
+
+// Smallest scale with top / scale <= 448 (= 1.75 * 2^8, E4M3's largest value).
+__device__ __forceinline__ float block_scale_for(float top) {
+  const uint32_t b = __float_as_uint(top);
+  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(kMinScaleExp, min(kMaxScaleExp, e));
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+__device__ __forceinline__ bool block_scale_ok(float s) {
+  const uint32_t b = __float_as_uint(s);
+  return (b & 0x807fffffu) == 0u && b >= ((uint32_t)(kMinScaleExp + 127) << 23) &&
+         b <= ((uint32_t)(kMaxScaleExp + 127) << 23);
+}
+// log2 of a valid scale.
+__device__ __forceinline__ int block_scale_log2(float s) {
+  return (int)(__float_as_uint(s) >> 23) - 127;
+}
+
 // Programmatic dependent launch. Every kernel of the library lets the next
 // kernel in its stream be scheduled as soon as all of its own CTAs are running
 // (pdl_trigger), and touches global memory only after the previous kernel has

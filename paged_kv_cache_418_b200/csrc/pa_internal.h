@@ -4,9 +4,35 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "pa_common.cuh"
 
 namespace pa {
+
+// Host checks shared by the entry points.
+inline bool supported_shape(int Hq, int Hkv, int D, int bs) {
+  if (Hkv <= 0 || Hq <= 0 || Hq % Hkv) return false;
+  const int G = Hq / Hkv;
+  return (D == 64 || D == 128) && (bs == 16 || bs == 32) &&
+         (G == 1 || G == 2 || G == 4 || G == 8 || G == 16);
+}
+
+inline int esize_of(int dtype) { return dtype == PA_F32 ? 4 : (dtype == PA_FP8_E4M3 ? 1 : 2); }
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool scale_ok(float x) { return std::isfinite(x) && x > 0.f; }
+
+// Pool element types a decode takes for a query of q_dtype: both the query's
+// type; both FP8; or, for a 16-bit query, one FP8 pool and one of its type.
+inline bool pool_types_ok(int q_dtype, int k_dtype, int v_dtype) {
+  const bool kf = k_dtype == PA_FP8_E4M3, vf = v_dtype == PA_FP8_E4M3;
+  if (!kf && k_dtype != q_dtype) return false;
+  if (!vf && v_dtype != q_dtype) return false;
+  if (kf != vf && q_dtype == PA_F32) return false;
+  return true;
+}
 
 // Everything a decode launch needs, resolved by the host layer.
 struct DecodeArgs {
@@ -133,6 +159,63 @@ int launch_reshape_and_cache_kv(const void* key, const void* value, int src_dtyp
                                 int v_fp8, float v_scale, const int64_t* slot_mapping, int T,
                                 int Hkv, int D, int block_size, int num_blocks,
                                 uint32_t* err_flag, cudaStream_t stream);
+// Append with the rotary embedding on the way (rope_cache.cu). Strides are
+// elements between tokens; heads of a token are dense.
+struct RopeArgs {
+  void* query_out;              // NULL with Hq = 0
+  const void* query;
+  const void* key;
+  const void* value;
+  long long qo_stride, q_stride, k_stride, v_stride;
+  const int64_t* positions;     // [T]; NULL without a rotation (blk8 only)
+  const float* cos_sin;         // [max_pos][rot]: rot / 2 cosines, then rot / 2 sines
+  int max_pos, rot, interleaved;
+  void* key_cache;
+  void* value_cache;
+  int k_fp8, v_fp8;             // per-pool scales (rope_and_cache_kernel)
+  float k_scale, v_scale;
+  float* k_scales;              // [num_blocks][Hkv] (blk8)
+  float* v_scales;
+  const int64_t* slot_mapping;  // [T]
+  int T, Hq, Hkv, D, bs, num_blocks;
+  uint32_t* err_flag;
+};
+int launch_rope_and_cache(const RopeArgs& a, int src_dtype, bool blk8, cudaStream_t stream);
+int launch_copy_scales(float* dst_k, float* dst_v, const float* src_k, const float* src_v,
+                       const int64_t* block_mapping, int num_pairs, int Hkv, int src_blocks,
+                       int dst_blocks, uint32_t* err_flag, cudaStream_t stream);
+
+// Decode over a window and first tokens, and over the block-scaled cache
+// (decode_window.cu).
+struct WinArgs {
+  void* out;
+  int out_dtype;
+  const void* q;
+  int q_dtype;
+  const void* k_cache;
+  const void* v_cache;
+  int k_dtype, v_dtype;
+  const float* k_scales;        // [num_blocks][Hkv] of the block-scaled cache, else NULL
+  const float* v_scales;
+  const int32_t* block_tables;
+  int max_blocks;
+  const int32_t* context_lens;
+  int B, Hq, Hkv, D, bs, num_blocks;
+  float scale_log2;             // softmax scale * log2(e) (* the K pool's scale)
+  float v_scale;                // value of one V unit (per-pool scale; 1 otherwise)
+  int window, sinks;            // window 0: every token
+  int max_context_len;
+  int P, ptiles;                // parts per (sequence, KV head chunk), 16-token tiles per part
+  float* ws_acc;                // [B][P][Hq][D]
+  float* ws_m;                  // [B][P][Hq]
+  float* ws_l;
+  uint32_t* err_flag;
+};
+// Parts and tiles per part of a windowed decode; its scratch.
+void plan_window(WinArgs& a);
+size_t window_scratch_bytes(int B, int Hq, int D, int P);
+int launch_decode_window(const WinArgs& a, cudaStream_t stream);
+
 int launch_swap_blocks(void* dst_key, void* dst_value, const void* src_key,
                        const void* src_value, int esize, const int64_t* block_mapping,
                        int num_pairs, int Hkv, int D, int block_size, int src_blocks,

@@ -22,6 +22,7 @@ from . import _build
 PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2, 3
 PA_OK = 0
 PA_DEV_BAD_BLOCK_ID, PA_DEV_BAD_CTX, PA_DEV_BAD_SLOT, PA_DEV_BAD_PAIR = 1, 2, 4, 8
+PA_DEV_BAD_POS, PA_DEV_BAD_SCALE = 32, 64
 _TORCH_TO_PA = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
                 torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3}
 
@@ -76,6 +77,23 @@ def _load() -> ctypes.CDLL:
     lib.pa_prefill_kv.argtypes = [P, I, P, I, P, I, F, P, I, F, P, I, P, P, I, I, I, I, I, I, I, I,
                                   F, I, P, P]
     lib.pa_prefill_kv.restype = I
+    L = ctypes.c_int64
+    lib.pa_rope_and_cache_kv.argtypes = [P, L, P, L, P, L, P, L, I, P, P, I, I, I, P, I, F, P, I, F,
+                                         P, I, I, I, I, I, I, P, P]
+    lib.pa_rope_and_cache_kv.restype = I
+    lib.pa_rope_and_cache_blk8.argtypes = [P, L, P, L, P, L, P, L, I, P, P, I, I, I, P, P, P, P,
+                                           P, I, I, I, I, I, I, P, P]
+    lib.pa_rope_and_cache_blk8.restype = I
+    lib.pa_copy_scales.argtypes = [P, P, P, P, P, I, I, I, I, P, P]
+    lib.pa_copy_scales.restype = I
+    lib.pa_window_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.pa_window_workspace_size.restype = S
+    lib.pa_decode_window_kv.argtypes = [P, I, P, I, P, I, F, P, I, F, P, I, P, I, I, I, I, I, I, F,
+                                        I, I, I, P, S, P, P]
+    lib.pa_decode_window_kv.restype = I
+    lib.pa_decode_blk8.argtypes = [P, I, P, I, P, P, P, P, P, I, P, I, I, I, I, I, I, F, I, I, I,
+                                   P, S, P, P]
+    lib.pa_decode_blk8.restype = I
     return lib
 
 
@@ -453,3 +471,161 @@ def workspace_for(query: torch.Tensor, key_cache: torch.Tensor, max_context_len:
     B, Hq, D = query.shape
     n = pa_workspace_size(B, Hq, key_cache.shape[2], D, max_context_len, partition_size)
     return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=query.device)
+
+
+def _token_stride(t: torch.Tensor, fn: str) -> int:
+    """Elements between tokens of a [T,H,D] tensor whose heads are dense (a slice of a
+    fused projection is; a transposed or expanded view is refused)."""
+    if t.dim() != 3 or (t.shape[1] > 0 and t.stride(2) != 1) or \
+            (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise PAError(fn, 2)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def check_block_runs(slot_mapping: torch.Tensor, block_size: int,
+                     fn: str = "pa_rope_and_cache_blk8") -> None:
+    """ValueError if the tokens of one block are not consecutive in slot_mapping."""
+    s = slot_mapping.detach().to("cpu", torch.int64).reshape(-1)
+    block = torch.where(s >= 0, torch.div(s, block_size, rounding_mode="floor"),
+                        torch.full_like(s, -1))
+    new = torch.ones_like(block, dtype=torch.bool)
+    new[1:] = block[1:] != block[:-1]
+    runs = block[new]
+    runs = runs[runs >= 0]
+    if torch.unique(runs).numel() != runs.numel():
+        raise ValueError(f"{fn}: the tokens of one block are not consecutive in slot_mapping")
+
+
+def pa_rope_and_cache_kv(query_out: Optional[torch.Tensor], query: Optional[torch.Tensor],
+                         key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                         cos_sin: torch.Tensor, key_cache: torch.Tensor,
+                         value_cache: torch.Tensor, k_scale: float, v_scale: float,
+                         slot_mapping: torch.Tensor, interleaved: bool = False,
+                         err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rotate query [T,Hq,D] into query_out and key [T,Hkv,D] into the K pool at positions
+    [T] (int64) with the table cos_sin [max_positions, rot_dim], and write value to the V
+    pool, at slot_mapping [T] (see pa_rope_and_cache_kv in include/pa.h). query_out may be
+    query; query None: keys only. The tensors may be slices of one projection."""
+    fn = "pa_rope_and_cache_kv"
+    if DEBUG:
+        check_slot_mapping(slot_mapping, fn)
+    num_blocks, block_size, Hkv, D = key_cache.shape
+    Hq = 0 if query is None else query.shape[1]
+    with _on_device_of(key_cache):
+        rc = LIB.pa_rope_and_cache_kv(
+            _ptr(query_out), 0 if query is None else _token_stride(query_out, fn), _ptr(query),
+            0 if query is None else _token_stride(query, fn), _ptr(key), _token_stride(key, fn),
+            _ptr(value), _token_stride(value, fn), pa_dtype(key), _ptr(positions), _ptr(cos_sin),
+            cos_sin.shape[0], cos_sin.shape[1], int(interleaved), _ptr(key_cache),
+            pa_dtype(key_cache), float(k_scale), _ptr(value_cache), pa_dtype(value_cache),
+            float(v_scale), _ptr(slot_mapping), slot_mapping.shape[0], Hq, Hkv, D, block_size,
+            num_blocks, _ptr(err_flag), _stream(stream))
+    if rc:
+        raise PAError(fn, rc)
+
+
+def pa_rope_and_cache_blk8(query_out: Optional[torch.Tensor], query: Optional[torch.Tensor],
+                           key: torch.Tensor, value: torch.Tensor,
+                           positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                           key_cache: torch.Tensor, value_cache: torch.Tensor,
+                           k_scales: torch.Tensor, v_scales: torch.Tensor,
+                           slot_mapping: torch.Tensor, interleaved: bool = False,
+                           err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_rope_and_cache_kv into pools of E4M3 codes with one power-of-two scale per block
+    and KV head, k_scales / v_scales [num_blocks, Hkv] (see pa_rope_and_cache_blk8 in
+    include/pa.h). cos_sin None (with query and positions None): no rotation."""
+    fn = "pa_rope_and_cache_blk8"
+    num_blocks, block_size, Hkv, D = key_cache.shape
+    if DEBUG:
+        check_slot_mapping(slot_mapping, fn)
+        check_block_runs(slot_mapping, block_size, fn)
+    Hq = 0 if query is None else query.shape[1]
+    with _on_device_of(key_cache):
+        rc = LIB.pa_rope_and_cache_blk8(
+            _ptr(query_out), 0 if query is None else _token_stride(query_out, fn), _ptr(query),
+            0 if query is None else _token_stride(query, fn), _ptr(key), _token_stride(key, fn),
+            _ptr(value), _token_stride(value, fn), pa_dtype(key), _ptr(positions), _ptr(cos_sin),
+            0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
+            int(interleaved), _ptr(key_cache), _ptr(value_cache), _ptr(k_scales), _ptr(v_scales),
+            _ptr(slot_mapping), slot_mapping.shape[0], Hq, Hkv, D, block_size, num_blocks,
+            _ptr(err_flag), _stream(stream))
+    if rc:
+        raise PAError(fn, rc)
+
+
+def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
+                   src_k_scales: torch.Tensor, src_v_scales: torch.Tensor,
+                   block_mapping: torch.Tensor, err_flag: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Copy the block scales [num_blocks, Hkv] of each (src, dst) row of block_mapping, beside
+    pa_copy_blocks or pa_swap_blocks of the codes."""
+    if DEBUG:
+        check_block_mapping(block_mapping, "pa_copy_scales",
+                            same_pool=dst_k_scales.data_ptr() == src_k_scales.data_ptr())
+    src_blocks, Hkv = src_k_scales.shape
+    with _on_device_of(dst_k_scales, src_k_scales):
+        rc = LIB.pa_copy_scales(_ptr(dst_k_scales), _ptr(dst_v_scales), _ptr(src_k_scales),
+                                _ptr(src_v_scales), _ptr(block_mapping), block_mapping.shape[0],
+                                Hkv, src_blocks, dst_k_scales.shape[0], _ptr(err_flag),
+                                _stream(stream))
+    if rc:
+        raise PAError("pa_copy_scales", rc)
+
+
+def pa_window_workspace_size(B: int, Hq: int, Hkv: int, D: int, max_context_len: int,
+                             window: int = 0, num_sinks: int = 0) -> int:
+    return int(LIB.pa_window_workspace_size(B, Hq, Hkv, D, max_context_len, window, num_sinks))
+
+
+def window_workspace_for(query: torch.Tensor, key_cache: torch.Tensor, max_context_len: int,
+                         window: int = 0, num_sinks: int = 0) -> Optional[torch.Tensor]:
+    """A device byte tensor big enough for pa_decode_window_kv or pa_decode_blk8, or None."""
+    B, Hq, D = query.shape
+    n = pa_window_workspace_size(B, Hq, key_cache.shape[2], D, max_context_len, window, num_sinks)
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=query.device)
+
+
+def pa_decode_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                        value_cache: torch.Tensor, k_scale: float, v_scale: float,
+                        block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                        window: int, num_sinks: int, max_context_len: int,
+                        workspace: Optional[torch.Tensor] = None,
+                        err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_decode_kv over the last `window` tokens and the first `num_sinks` ones (see
+    pa_decode_window_kv in include/pa.h)."""
+    B, Hq, D = query.shape
+    num_blocks, block_size, Hkv, _ = key_cache.shape
+    with _on_device_of(query):
+        rc = LIB.pa_decode_window_kv(
+            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
+            pa_dtype(key_cache), float(k_scale), _ptr(value_cache), pa_dtype(value_cache),
+            float(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, Hq,
+            Hkv, D, block_size, num_blocks, float(scale), int(window), int(num_sinks),
+            int(max_context_len), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _ptr(err_flag), _stream(stream))
+    if rc:
+        raise PAError("pa_decode_window_kv", rc)
+
+
+def pa_decode_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                   value_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                   max_context_len: int, window: int = 0, num_sinks: int = 0,
+                   workspace: Optional[torch.Tensor] = None,
+                   err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Decode attention over pools of E4M3 codes with one power-of-two scale per block and KV
+    head, k_scales / v_scales [num_blocks, Hkv]; window 0: every token (see pa_decode_blk8 in
+    include/pa.h)."""
+    B, Hq, D = query.shape
+    num_blocks, block_size, Hkv, _ = key_cache.shape
+    with _on_device_of(query):
+        rc = LIB.pa_decode_blk8(
+            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
+            _ptr(value_cache), _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
+            block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, block_size, num_blocks,
+            float(scale), int(window), int(num_sinks), int(max_context_len), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _ptr(err_flag), _stream(stream))
+    if rc:
+        raise PAError("pa_decode_blk8", rc)

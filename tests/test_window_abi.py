@@ -1,0 +1,180 @@
+"""Host-side checks of the rotary append, the windowed attention and the block-scaled cache:
+documented refusals before any launch, workspace sizes, random arguments that never crash, the
+binding's stride and debug checks. CPU only (nothing here launches a kernel)."""
+
+import ctypes
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from paged_kv_cache_418_b200 import ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NAN, INF = float("nan"), float("inf")
+
+ROPE = dict(qo=16, qos=1024, q=16, qs=1024, k=16, ks=256, v=16, vs=256, dt=2, pos=16, cs=16, mp=64, rot=128,
+            il=0, kc=16, kdt=2, ksc=1.0, vc=16, vdt=2, vsc=1.0, sm=16, T=0, Hq=8, Hkv=2, D=128, bs=16,
+            nb=4, err=None, stream=None)
+BLK = {k: v for k, v in ROPE.items() if k not in ("kdt", "ksc", "vdt", "vsc")}
+_o = list(BLK)
+_o.insert(_o.index("sm"), "vscs")
+_o.insert(_o.index("vscs"), "kscs")
+BLK = {k: BLK.get(k, 16) for k in _o}
+DEC = dict(out=16, odt=0, q=16, qdt=2, kc=16, kdt=2, ksc=1.0, vc=16, vdt=2, vsc=1.0, bt=16, mb=8, cl=16, B=2,
+           Hq=8, Hkv=2, D=128, bs=16, nb=4, scale=0.1, window=5, sinks=1, mc=64, ws=None, wsb=0, err=None,
+           stream=None)
+DEC8 = dict(out=16, odt=0, q=16, qdt=2, kc=16, vc=16, kscs=16, vscs=16, bt=16, mb=8, cl=16, B=2, Hq=8, Hkv=2,
+            D=128, bs=16, nb=4, scale=0.1, window=0, sinks=0, mc=64, ws=None, wsb=0, err=None, stream=None)
+
+
+def call(fn, base, **kw):
+    args = dict(base)
+    for k in kw:
+        assert k in args, k
+    args.update(kw)
+    return getattr(ops.LIB, fn)(*args.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 0), (dict(T=-1), 2), (dict(dt=3), 3), (dict(kdt=1), 3), (dict(vdt=0), 3), (dict(D=96), 4),
+    (dict(bs=8), 4), (dict(rot=0), 2), (dict(rot=24), 2), (dict(rot=144), 2), (dict(kdt=3, ksc=0.0), 2),
+    (dict(vdt=3, vsc=NAN), 2), (dict(ks=255), 2), (dict(ks=260), 2), (dict(vs=128), 2), (dict(qs=1000), 2),
+    (dict(qos=1028), 2), (dict(Hkv=0), 2), (dict(Hq=-1), 2), (dict(mp=-1), 2), (dict(Hkv=65536, ks=1 << 24, vs=1 << 24), 4),
+    (dict(T=1, k=None), 1), (dict(T=1, q=None), 1), (dict(T=1, qo=None), 1), (dict(T=1, pos=None), 1),
+    (dict(T=1, cs=None), 1), (dict(T=1, sm=None), 1), (dict(T=1, kc=24), 7), (dict(T=1, q=24), 7),
+    (dict(T=1, cs=20), 7), (dict(T=1, qs=1 << 62), 2)])
+def test_rope_kv_refusals(kw, status):
+    assert call("pa_rope_and_cache_kv", ROPE, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 0), (dict(T=1, kscs=None), 1), (dict(T=1, vscs=None), 1), (dict(dt=3), 3), (dict(D=32), 4),
+    (dict(T=1, cs=None), 1), (dict(T=1, cs=None, pos=None), 1), (dict(T=1, cs=None, Hq=0), 1),
+    (dict(rot=8), 2), (dict(ks=100), 2), (dict(T=1, vc=8), 7)])
+def test_rope_blk8_refusals(kw, status):
+    assert call("pa_rope_and_cache_blk8", BLK, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 0), (dict(window=0), 2), (dict(window=-1), 2), (dict(sinks=-1), 2), (dict(qdt=3), 3),
+    (dict(kdt=1), 3), (dict(kdt=3, ksc=0.0), 2), (dict(vdt=3, vsc=INF), 2), (dict(qdt=0, kdt=0, vdt=3), 3),
+    (dict(odt=1), 3), (dict(D=80), 4), (dict(bs=64), 4), (dict(Hq=6), 4), (dict(Hq=7), 4), (dict(scale=NAN), 2),
+    (dict(mb=0), 2), (dict(mc=-1), 2), (dict(B=65536), 4), (dict(q=None), 1), (dict(cl=None), 1),
+    (dict(out=8), 7), (dict(B=1, Hq=1, Hkv=1, mc=100000, window=90000, mb=9000), 5),
+    (dict(B=1, Hq=1, Hkv=1, mc=100000, window=90000, mb=9000, ws=257, wsb=1 << 40), 5)])
+def test_decode_window_refusals(kw, status):
+    assert call("pa_decode_window_kv", DEC, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 0), (dict(window=-1), 2), (dict(kscs=None), 1), (dict(vscs=None), 1), (dict(qdt=4), 3),
+    (dict(odt=2, qdt=1), 3), (dict(D=256), 4), (dict(kc=17), 7)])
+def test_decode_blk8_refusals(kw, status):
+    assert call("pa_decode_blk8", DEC8, **kw) == status
+
+
+def test_copy_scales_refusals():
+    f = ops.LIB.pa_copy_scales
+    assert f(None, None, None, None, None, 0, 8, 4, 4, None, None) == 0
+    assert f(16, 16, 16, 16, 16, -1, 8, 4, 4, None, None) == 2
+    assert f(16, 16, 16, 16, 16, 1, 0, 4, 4, None, None) == 2
+    assert f(16, None, 16, 16, 16, 1, 8, 4, 4, None, None) == 1
+
+
+def test_workspace_size():
+    n = ops.pa_window_workspace_size
+    assert n(0, 8, 2, 128, 100) == 0 and n(1, 7, 2, 128, 100) == 0 and n(1, 8, 2, 128, 100, -1) == 0
+    assert n(1, 8, 2, 128, 16) == 0                               # one tile: nothing to join
+    assert n(1, 8, 2, 128, 100000) > 0
+    # a window bounds it, whatever the context
+    assert n(1, 8, 2, 128, 10 ** 9, 512, 4) == n(1, 8, 2, 128, 10 ** 6, 512, 4)
+    for B in (1, 3, 64, 1000, 65535):
+        for mc in (1, 1000, 100000, 2 ** 31 - 1):
+            assert n(B, 64, 8, 128, mc) <= 64 << 20 or B > 1000
+
+
+def test_binding_refuses_views_whose_heads_are_not_dense():
+    kc = torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16)
+    x = torch.zeros(3, 8, 128, dtype=torch.bfloat16)
+    cs = torch.zeros(8, 128)
+    i = torch.zeros(3, dtype=torch.int64)
+    for bad in (torch.zeros(3, 128, 2, dtype=torch.bfloat16).transpose(1, 2),
+                torch.zeros(3, 4, 128, dtype=torch.bfloat16)[:, ::2], torch.zeros(3, 256, dtype=torch.bfloat16)):
+        with pytest.raises(ops.PAError):
+            ops.pa_rope_and_cache_kv(x, x, bad, kc[0, :3], i, cs, kc, kc, 1.0, 1.0, i)
+
+
+def test_debug_check_of_block_runs():
+    ops.check_block_runs(torch.tensor([3, 4, -1, 16, 17, -1, 40]), 16)
+    with pytest.raises(ValueError, match="consecutive"):
+        ops.check_block_runs(torch.tensor([3, 16, 4]), 16)
+    with pytest.raises(ValueError, match="consecutive"):
+        ops.check_block_runs(torch.tensor([3, -1, 4]), 16)
+    kc = torch.zeros(4, 16, 2, 128, dtype=torch.uint8)
+    x = torch.zeros(3, 2, 128)
+    s = torch.zeros(4, 2)
+    was = ops.DEBUG
+    ops.set_debug(True)
+    try:
+        with pytest.raises(ValueError):
+            ops.pa_rope_and_cache_blk8(None, None, x, x, None, None, kc, kc, s, s, torch.tensor([3, 16, 4]))
+        with pytest.raises(ValueError):
+            ops.pa_rope_and_cache_kv(x, x, x, x, torch.zeros(3).long(), torch.zeros(4, 128), kc, kc, 1.0, 1.0,
+                                     torch.tensor([3, 3, 4]))
+        with pytest.raises(ValueError):
+            ops.pa_copy_scales(s, s, s, s, torch.tensor([[0, 1], [1, 2]]))
+    finally:
+        ops.set_debug(was)
+
+
+CHILD = r'''
+import ctypes, random, sys
+sys.path.insert(0, "tests")
+import test_window_abi as M
+from paged_kv_cache_418_b200 import ops
+rng = random.Random(99)
+ptrs = [None, 16, 0x1000, 0x1001, 0x1008, 0x7f0000000000, 0x7f0000000004]
+ints = [-7, -1, 0, 1, 2, 3, 4, 5, 8, 16, 24, 32, 64, 96, 128, 512, 4096, 1 << 20, 1 << 30, (1 << 31) - 1]
+longs = ints + [1 << 40, (1 << 62), -(1 << 62)]
+floats = [float("nan"), float("inf"), -1.0, 0.0, 0.088, 1.0]
+sizes = [0, 1, 255, 1 << 20, 1 << 40]
+def pick(t):
+    if t is ctypes.c_void_p: return rng.choice(ptrs)
+    if t is ctypes.c_float: return rng.choice(floats)
+    if t is ctypes.c_size_t: return rng.choice(sizes)
+    if t is ctypes.c_int64: return rng.choice(longs)
+    return rng.choice(ints)
+A = 0x10000
+base = {"pa_rope_and_cache_kv": dict(M.ROPE, T=4), "pa_rope_and_cache_blk8": dict(M.BLK, T=4),
+        "pa_decode_window_kv": dict(M.DEC, ws=A, wsb=1 << 30), "pa_decode_blk8": dict(M.DEC8, ws=A, wsb=1 << 30)}
+base.update(getattr(M, "MORE", {}))
+for name, kw in base.items():
+    fn = getattr(ops.LIB, name)
+    b = [A if v == 16 and t is ctypes.c_void_p else v for v, t in zip(kw.values(), fn.argtypes)]
+    assert len(b) == len(fn.argtypes) == len(kw), name
+    r = fn(*b)
+    if r != 6:                                   # every host check passed, the launch cannot
+        print("BASE", name, r); sys.exit(1)
+    for _ in range(3000):
+        args = list(b)
+        for i in rng.sample(range(len(args)), rng.choice([1, 1, 2, 3])):
+            args[i] = pick(fn.argtypes[i])
+        r = fn(*args)
+        if not 0 <= r <= 7:
+            print("BAD", name, r, args); sys.exit(1)
+fn = ops.LIB.pa_window_workspace_size
+for _ in range(3000):
+    fn(*[pick(t) for t in fn.argtypes])
+print("OK")
+'''
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host-only check; run where no GPU is visible")
+def test_random_arguments_never_crash_the_host_side():
+    r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, cwd=ROOT, timeout=600,
+                       env=dict(os.environ, CUDA_VISIBLE_DEVICES="", PYTHONPATH=ROOT))
+    assert r.returncode == 0, (r.returncode, r.stdout[-2000:], r.stderr[-2000:])
+    assert r.stdout.strip().endswith("OK"), r.stdout
