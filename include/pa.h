@@ -569,6 +569,34 @@ int pa_decode_blk8(void* out, int out_dtype, const void* query, int q_dtype, con
                    int num_blocks, float scale, int window, int num_sinks, int max_context_len,
                    void* workspace, size_t workspace_bytes, uint32_t* err_flag, void* stream);
 
+/*
+ * pa_prefill_window_kv -- pa_prefill_kv over a sliding window and a few first
+ * tokens: the new token at position p attends the keys
+ *   t <= p  with  t > p - window  or  t < num_sinks
+ * (window >= 1, num_sinks >= 0). Blocks that none of the call's queries attends,
+ * and their table entries, are not read. Positions, types, shapes and errors as
+ * pa_prefill_kv. As there, the query rows of up to 128 / G neighbouring tokens
+ * are one matrix operand: an infinite or NaN V element of a token that one of
+ * them attends may reach the others' rows.
+ *
+ * pa_prefill_blk8 -- the same over the block-scaled 8-bit cache (scales and
+ * their errors as pa_decode_blk8); window 0: every earlier token.
+ */
+int pa_prefill_window_kv(void* out, int out_dtype, const void* query, int q_dtype,
+                         const void* key_cache, int k_dtype, float k_scale, const void* value_cache,
+                         int v_dtype, float v_scale, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens,
+                         const int32_t* query_start, int B, int T, int max_query_len, int Hq,
+                         int Hkv, int D, int block_size, int num_blocks, float scale, int window,
+                         int num_sinks, int max_context_len, uint32_t* err_flag, void* stream);
+int pa_prefill_blk8(void* out, int out_dtype, const void* query, int q_dtype, const void* key_cache,
+                    const void* value_cache, const float* k_scales, const float* v_scales,
+                    const int32_t* block_tables, int max_blocks_per_seq,
+                    const int32_t* context_lens, const int32_t* query_start, int B, int T,
+                    int max_query_len, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                    float scale, int window, int num_sinks, int max_context_len,
+                    uint32_t* err_flag, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

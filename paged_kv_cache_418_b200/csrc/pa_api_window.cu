@@ -96,6 +96,52 @@ int decode_window_impl(void* out, int out_dtype, const void* query, int q_dtype,
   return launch_decode_window(a, static_cast<cudaStream_t>(stream));
 }
 
+// Shared body of the windowed and block-scaled prefills.
+int prefill_window_impl(void* out, int out_dtype, const void* query, int q_dtype,
+                        const void* key_cache, int k_dtype, float k_scale, const void* value_cache,
+                        int v_dtype, float v_scale, bool blk8, const float* k_scales,
+                        const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                        const int32_t* context_lens, const int32_t* query_start, int B, int T,
+                        int max_query_len, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                        float scale, int window, int num_sinks, int max_context_len,
+                        uint32_t* err_flag, void* stream) {
+  if (q_dtype < PA_F32 || q_dtype > PA_BF16) return PA_ERR_DTYPE;
+  if (out_dtype != PA_F32 && out_dtype != q_dtype) return PA_ERR_DTYPE;
+  const bool k8 = k_dtype == PA_FP8_E4M3, v8 = v_dtype == PA_FP8_E4M3;
+  if ((!k8 && k_dtype != q_dtype) || (!v8 && v_dtype != q_dtype)) return PA_ERR_DTYPE;
+  if (B < 0 || T < 0 || max_query_len < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || block_size <= 0 ||
+      num_blocks < 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
+      window < (blk8 ? 0 : 1) || num_sinks < 0)
+    return PA_ERR_SHAPE;
+  if (!supported_shape(Hq, Hkv, D, block_size) ||
+      !prefill_fa_supported(q_dtype, Hq, Hkv, D, block_size))
+    return PA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale)) return PA_ERR_SHAPE;
+  if (!blk8 && ((k8 && !scale_ok(k_scale)) || (v8 && !scale_ok(v_scale)))) return PA_ERR_SHAPE;
+  if (B == 0 || T == 0 || max_query_len == 0) return PA_OK;
+  if (!out || !query || !key_cache || !value_cache || !block_tables || !context_lens || !query_start)
+    return PA_ERR_NULL;
+  if (blk8 && (!k_scales || !v_scales)) return PA_ERR_NULL;
+  if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
+    return PA_ERR_ALIGN;
+  PrefillLaunch p{};
+  p.out = out; p.out_dtype = out_dtype; p.q = query;
+  p.k_cache = key_cache; p.v_cache = value_cache; p.dtype = q_dtype;
+  p.k_dtype = k_dtype; p.v_dtype = v_dtype;
+  p.v_scale = v8 && !blk8 ? v_scale : 1.f;
+  p.block_tables = block_tables; p.max_blocks = max_blocks_per_seq;
+  p.context_lens = context_lens; p.query_start = query_start;
+  p.B = B; p.T = T; p.max_query_len = max_query_len; p.Hq = Hq; p.Hkv = Hkv; p.bs = block_size;
+  p.num_blocks = num_blocks;
+  p.scale_log2 = scale * kLog2e * (k8 && !blk8 ? k_scale : 1.f);
+  p.max_context_len = max_context_len;
+  p.err_flag = err_flag;
+  p.window = window; p.sinks = num_sinks;
+  p.k_scales = blk8 ? k_scales : nullptr;
+  p.v_scales = blk8 ? v_scales : nullptr;
+  return launch_prefill_window(p, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -196,6 +242,34 @@ int pa_decode_blk8(void* out, int out_dtype, const void* query, int q_dtype, con
                             max_blocks_per_seq, context_lens, B, Hq, Hkv, D, block_size,
                             num_blocks, scale, window, num_sinks, max_context_len, workspace,
                             workspace_bytes, err_flag, stream);
+}
+
+int pa_prefill_window_kv(void* out, int out_dtype, const void* query, int q_dtype,
+                         const void* key_cache, int k_dtype, float k_scale, const void* value_cache,
+                         int v_dtype, float v_scale, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens,
+                         const int32_t* query_start, int B, int T, int max_query_len, int Hq,
+                         int Hkv, int D, int block_size, int num_blocks, float scale, int window,
+                         int num_sinks, int max_context_len, uint32_t* err_flag, void* stream) {
+  return prefill_window_impl(out, out_dtype, query, q_dtype, key_cache, k_dtype, k_scale,
+                             value_cache, v_dtype, v_scale, false, nullptr, nullptr, block_tables,
+                             max_blocks_per_seq, context_lens, query_start, B, T, max_query_len, Hq,
+                             Hkv, D, block_size, num_blocks, scale, window, num_sinks,
+                             max_context_len, err_flag, stream);
+}
+
+int pa_prefill_blk8(void* out, int out_dtype, const void* query, int q_dtype, const void* key_cache,
+                    const void* value_cache, const float* k_scales, const float* v_scales,
+                    const int32_t* block_tables, int max_blocks_per_seq,
+                    const int32_t* context_lens, const int32_t* query_start, int B, int T,
+                    int max_query_len, int Hq, int Hkv, int D, int block_size, int num_blocks,
+                    float scale, int window, int num_sinks, int max_context_len,
+                    uint32_t* err_flag, void* stream) {
+  return prefill_window_impl(out, out_dtype, query, q_dtype, key_cache, PA_FP8_E4M3, 1.f,
+                             value_cache, PA_FP8_E4M3, 1.f, true, k_scales, v_scales, block_tables,
+                             max_blocks_per_seq, context_lens, query_start, B, T, max_query_len, Hq,
+                             Hkv, D, block_size, num_blocks, scale, window, num_sinks,
+                             max_context_len, err_flag, stream);
 }
 
 }  // extern "C"

@@ -135,7 +135,13 @@ struct PrefillLaunch {
   float scale_log2;
   int max_context_len;
   uint32_t* err_flag;
+  // launch_prefill_window only
+  int window, sinks;            // window 0: every token
+  const float* k_scales;        // block-scaled cache: [num_blocks][Hkv], else NULL
+  const float* v_scales;
 };
+// Windowed and block-scaled paged prefill (prefill_window.cu).
+int launch_prefill_window(const PrefillLaunch& p, cudaStream_t stream);
 int launch_prefill_tc(const PrefillLaunch& p, cudaStream_t stream);
 // Paged prefill with the query rows on the MMA's M (prefill_tc.cu).
 bool prefill_fa_supported(int dtype, int Hq, int Hkv, int D, int bs);

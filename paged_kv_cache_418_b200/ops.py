@@ -94,6 +94,12 @@ def _load() -> ctypes.CDLL:
     lib.pa_decode_blk8.argtypes = [P, I, P, I, P, P, P, P, P, I, P, I, I, I, I, I, I, F, I, I, I,
                                    P, S, P, P]
     lib.pa_decode_blk8.restype = I
+    lib.pa_prefill_window_kv.argtypes = [P, I, P, I, P, I, F, P, I, F, P, I, P, P, I, I, I, I, I, I,
+                                         I, I, F, I, I, I, P, P]
+    lib.pa_prefill_window_kv.restype = I
+    lib.pa_prefill_blk8.argtypes = [P, I, P, I, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, F,
+                                    I, I, I, P, P]
+    lib.pa_prefill_blk8.restype = I
     return lib
 
 
@@ -629,3 +635,48 @@ def pa_decode_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tens
             _ptr(err_flag), _stream(stream))
     if rc:
         raise PAError("pa_decode_blk8", rc)
+
+
+def pa_prefill_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                         value_cache: torch.Tensor, k_scale: float, v_scale: float,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor,
+                         query_start: torch.Tensor, max_query_len: int, scale: float, window: int,
+                         num_sinks: int, max_context_len: int,
+                         err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_prefill_kv over the last `window` tokens up to each query's and the first
+    `num_sinks` ones (see pa_prefill_window_kv in include/pa.h)."""
+    T, Hq, D = query.shape
+    num_blocks, block_size, Hkv, _ = key_cache.shape
+    B = query_start.shape[0] - 1
+    with _on_device_of(query):
+        rc = LIB.pa_prefill_window_kv(
+            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
+            pa_dtype(key_cache), float(k_scale), _ptr(value_cache), pa_dtype(value_cache),
+            float(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+            _ptr(query_start), B, T, int(max_query_len), Hq, Hkv, D, block_size, num_blocks,
+            float(scale), int(window), int(num_sinks), int(max_context_len), _ptr(err_flag),
+            _stream(stream))
+    if rc:
+        raise PAError("pa_prefill_window_kv", rc)
+
+
+def pa_prefill_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                    value_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor,
+                    query_start: torch.Tensor, max_query_len: int, scale: float,
+                    max_context_len: int, window: int = 0, num_sinks: int = 0,
+                    err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Paged prefill over the block-scaled 8-bit cache; window 0: every earlier token (see
+    pa_prefill_blk8 in include/pa.h)."""
+    T, Hq, D = query.shape
+    num_blocks, block_size, Hkv, _ = key_cache.shape
+    B = query_start.shape[0] - 1
+    with _on_device_of(query):
+        rc = LIB.pa_prefill_blk8(
+            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
+            _ptr(value_cache), _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
+            block_tables.shape[1], _ptr(context_lens), _ptr(query_start), B, T,
+            int(max_query_len), Hq, Hkv, D, block_size, num_blocks, float(scale), int(window),
+            int(num_sinks), int(max_context_len), _ptr(err_flag), _stream(stream))
+    if rc:
+        raise PAError("pa_prefill_blk8", rc)

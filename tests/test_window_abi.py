@@ -29,6 +29,16 @@ DEC = dict(out=16, odt=0, q=16, qdt=2, kc=16, kdt=2, ksc=1.0, vc=16, vdt=2, vsc=
 DEC8 = dict(out=16, odt=0, q=16, qdt=2, kc=16, vc=16, kscs=16, vscs=16, bt=16, mb=8, cl=16, B=2, Hq=8, Hkv=2,
             D=128, bs=16, nb=4, scale=0.1, window=0, sinks=0, mc=64, ws=None, wsb=0, err=None, stream=None)
 
+PRE = dict(out=16, odt=0, q=16, qdt=2, kc=16, kdt=2, ksc=1.0, vc=16, vdt=2, vsc=1.0, bt=16, mb=8, cl=16, qst=16,
+           B=2, T=9, mq=5, Hq=8, Hkv=2, D=128, bs=16, nb=4, scale=0.1, window=5, sinks=1, mc=64, err=None,
+           stream=None)
+PRE8 = {k: v for k, v in PRE.items() if k not in ("kdt", "ksc", "vdt", "vsc")}
+_o = list(PRE8)
+_o[_o.index("bt"):_o.index("bt")] = ["kscs", "vscs"]
+PRE8 = {k: PRE8.get(k, 16) for k in _o}
+PRE8["window"] = PRE8["sinks"] = 0
+MORE = {"pa_prefill_window_kv": PRE, "pa_prefill_blk8": PRE8}
+
 
 def call(fn, base, **kw):
     args = dict(base)
@@ -74,6 +84,21 @@ def test_decode_window_refusals(kw, status):
     (dict(odt=2, qdt=1), 3), (dict(D=256), 4), (dict(kc=17), 7)])
 def test_decode_blk8_refusals(kw, status):
     assert call("pa_decode_blk8", DEC8, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 0), (dict(T=0), 0), (dict(mq=0), 0), (dict(window=0), 2), (dict(sinks=-2), 2), (dict(qdt=0, kdt=0, vdt=0), 4),
+    (dict(D=64), 4), (dict(kdt=1), 3), (dict(kdt=3, ksc=-1.0), 2), (dict(odt=1), 3), (dict(scale=INF), 2),
+    (dict(qst=None), 1), (dict(q=8), 7), (dict(T=-1), 2)])
+def test_prefill_window_refusals(kw, status):
+    assert call("pa_prefill_window_kv", PRE, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 0), (dict(window=-1), 2), (dict(kscs=None), 1), (dict(vscs=None), 1), (dict(D=64), 4),
+    (dict(qdt=0), 4), (dict(qdt=5), 3)])
+def test_prefill_blk8_refusals(kw, status):
+    assert call("pa_prefill_blk8", PRE8, **kw) == status
 
 
 def test_copy_scales_refusals():
