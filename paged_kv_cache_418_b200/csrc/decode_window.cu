@@ -1,5 +1,6 @@
 // decode_window.cu -- decode attention over part of a sequence's tokens (a
-// sliding window and a few first tokens) and over the block-scaled 8-bit cache.
+// sliding window and a few first tokens) and over the block-scaled 8-bit cache,
+// 16- and 8-bit pools.
 //
 // A sequence of ctx tokens whose last one is the query's attends the tokens
 //   t < ctx  with  t >= ctx - window  or  t < sinks     (window 0: every t < ctx).
@@ -10,11 +11,22 @@
 //
 // The work per visible (token, KV head) is 2 D bytes-per-element of K and V
 // against 4 D flops per query head: with up to 16 query heads per KV head it is
-// bound by HBM, so the kernel is built around bytes in flight. Every warp owns a
-// ring of tiles in shared memory that it fills with 16-byte asynchronous copies
-// (no registers held, no barrier with the other warps) and takes its tiles from
-// it. The products are warp-level m16n8k16 MMAs whose operands the warp reads
-// from its tile in the order the instruction wants:
+// bound by HBM, so the kernel is built around bytes in flight. One CTA per SM:
+// a producer warp and eight consumer warps around a ring of 192 KB. A step of the
+// ring holds, for a group of HG = 8, 4, 2 or 1 neighbouring KV heads, 8 / HG
+// sub-tiles of 16 or 32 tokens, so that every consumer warp has one (head,
+// sub-tile): TMA brings 16 tokens of all the group's heads in one box (4-32 KB;
+// boxes of one head are bound by TMA issue), 128-byte swizzled. With HG = 8
+// each warp owns a head's whole softmax and never meets the others.
+//
+// Work split. A unit is (sequence, group of HG KV heads, chunk of up to 8 query
+// heads); the CTAs take equal shares of the units' costs (window_common.cuh). A
+// unit inside one share is written to the output; a cut one leaves one piece per
+// CTA (slot 2c + 1 where the unit starts, 2c in the CTAs after it) that the merge
+// kernel joins in the order of the CTAs. No CTA waits for another.
+//
+// The products are warp-level m16n8k16 MMAs whose operands the warp reads from
+// its tile in the order the instruction wants:
 //   S[16 x 8 keys]  = Q . K^T : A = the query heads in rows 0-7, what their
 //     rounding to 16 bits lost in rows 8-15 (an 8-bit pool meets queries of any
 //     type at ~22 bits), B = K rows as they lie, the dims permuted alike on both
@@ -22,7 +34,15 @@
 //   O[16 x 8 dims] += P . V : rows 0-7 the weights, rows 8-15 what their rounding
 //     to 16 bits lost, so the MMA rows that 8 heads leave empty carry the second
 //     half of the precision and the two halves are added at the end.
-// 8-bit codes are widened to f16 (exactly) between shared memory and the MMA.
+// 8-bit codes are widened to f16 (exactly) between shared memory and the MMA. The
+// 8 keys of a score product are tokens 0 4 2 6 5 1 7 3 of their tile: in that order
+// both the K reads (4 chunks of 2 rows) and the V reads (2 chunks of 4 rows) of
+// eight lanes fall on different banks under the 128-byte swizzle.
+// (Warp-level MMAs rather than tcgen05: at 4-16 flops per byte the tensor work is a
+// few percent of either pipe, and they take the weights from the registers the
+// softmax leaves them in, while a tcgen05 tile pays a round trip of scores and
+// weights through tensor memory and, for 8-bit V, a widened copy of the tile in
+// shared memory.)
 //
 // Block-scaled pools: K's power of two multiplies the scores of its block's
 // tokens. V's would have to multiply the weights before they are rounded to
@@ -30,401 +50,189 @@
 // running maximum is taken over log2 of the whole contribution, s' = s + log2(vs)
 // (an exact integer): weights w = 2^(s' - m') are normalised to the largest
 // contribution, and the exp-sum counts w 2^-log2(vs).
-#include <math_constants.h>
+//
+// Every pipeline wait is bounded (1 s): one that gives up sets PA_DEV_TIMEOUT,
+// raises the CTA's abort flag, and the producer waits for its copies in flight.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
-#include <cfloat>
-
-#include "pa_internal.h"
+#include "tc_ptx.cuh"
+#include "window_common.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTok = 16;                        // tokens per tile
-constexpr int kHeads = 8;                       // query heads per CTA
-constexpr float kMove = 8.f;                    // the reference maximum moves when passed by 2^8:
-                                                // weights stay under 2^8, far inside f16
+using namespace tc;
 
-struct Span {
-  int lo, sk, ctx;    // visible: t < ctx and (t >= lo or t < sk)
-  int n0, w0, n;      // virtual tile v < n: tile v (v < n0) or v - n0 + w0
-  __device__ __forceinline__ int tile(int v) const { return v < n0 ? v : v - n0 + w0; }
-  __device__ __forceinline__ bool sees(int t) const { return t < ctx && (t >= lo || t < sk); }
-  // every token of the tile that starts at t0
-  __device__ __forceinline__ bool whole(int t0) const {
-    return t0 + kTok <= ctx && (t0 >= lo || t0 + kTok <= sk);
-  }
+constexpr int kCons = 8;                        // consumer warps
+constexpr int kThreads = (kCons + 1) * 32;
+constexpr int kRing = 192 * 1024;
+constexpr int kHeads = 8;                       // query heads of a KV head per unit
+constexpr int kMaxSub = 16;                     // (box, head) pairs of a step
+
+// Token of key n of an 8-key score product.
+__device__ __forceinline__ int tok_of(int n) { return (int)((0x37156240u >> (4 * n)) & 7u); }
+
+// What the consumers of a step need of it: per box its first token (-1: not there),
+// per (box, head) the scales.
+struct Meta {
+  int t0[kMaxSub];
+  float ks[kMaxSub];
+  int lvs[kMaxSub];                             // log2 of the V scale; kNoScale: skip the box
 };
+constexpr int kNoScale = 1 << 20;
 
-__device__ __forceinline__ Span span_of(int ctx, int window, int sinks) {
-  Span s;
-  s.ctx = ctx;
-  s.lo = window > 0 ? max(0, ctx - window) : 0;
-  s.sk = min(sinks, s.lo);
-  s.w0 = s.lo / kTok;
-  s.n0 = min((s.sk + kTok - 1) / kTok, s.w0);
-  s.n = s.n0 + (ctx + kTok - 1) / kTok - s.w0;
-  return s;
-}
-
-__device__ __forceinline__ bool bad_context(const WinArgs& a, int ctx) {
-  return ctx < 0 || ctx > (long long)a.max_blocks * a.bs || ctx > a.max_context_len;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 16 bytes from global to shared memory, zeros when !take (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(take ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-
-template <bool BF>
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if (BF)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// x0, x1 as packed 16-bit values and what their rounding lost, the same way.
-template <bool BF>
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  if (BF) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-    const float2 f = __bfloat1622float2(h);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    const __half2 h = __floats2half2_rn(x0, x1);
-    const float2 f = __half22float2(h);
-    const __half2 r = __floats2half2_rn(x0 - f.x, x1 - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&r);
-  }
-}
-
-// Two E4M3 codes (the low 16 bits) as packed f16, exactly.
-__device__ __forceinline__ uint32_t widen2(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-
-__device__ __forceinline__ float load_q1(const void* q, size_t i, int dtype) {
-  if (dtype == PA_F32) return static_cast<const float*>(q)[i];
-  if (dtype == PA_F16) return __half2float(static_cast<const __half*>(q)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
-}
-
-constexpr int esize(int dt) { return dt == PA_F32 ? 4 : dt == PA_FP8_E4M3 ? 1 : 2; }
-
-// The tile's shared-memory layout: K rows then V rows, 16-byte chunks swizzled
-// within a row so that the reads below touch every bank once per eight lanes
-// (K: lanes read 4 adjacent chunks of 2 rows; V: 2 adjacent chunks of 4 rows
-// two apart; fp32: one chunk of 8 rows).
-template <int DT, int D> struct Rows {
-  static constexpr int ROWB = D * esize(DT);
-  static constexpr int CPR = ROWB / 16;         // chunks per row
-  static constexpr int BYTES = kTok * ROWB;
-  static __device__ __forceinline__ uint32_t k_at(int row, int c) {
-    const int sw = DT == PA_F32 ? (row & 7) : CPR >= 8 ? ((row & 1) << 2) : 0;
-    return (uint32_t)(row * ROWB + ((c ^ sw) << 4));
-  }
-  static __device__ __forceinline__ uint32_t v_at(int row, int c) {
-    const int sw = CPR >= 8 ? (row & 7) : ((row >> 1) & 3);
-    return (uint32_t)(row * ROWB + ((c ^ sw) << 4));
-  }
-};
-
-// Tiles a warp keeps in its ring: 24 KB of bytes in flight per warp (two CTAs of
-// four warps per SM), at least two.
-constexpr int stages_for(int tile_bytes) {
-  const int n = 24 * 1024 / tile_bytes;
-  return n < 2 ? 2 : n > 8 ? 8 : n;
-}
-
-// Copies of one tile of one KV head into a ring stage.
-template <int KT, int VT, int D>
-__device__ __forceinline__ void issue_tile(const WinArgs& a, uint32_t stage, const Span& sp, int t0,
-                                           int id, int in_block, int h, int lane) {
-  using RK = Rows<KT, D>;
-  using RV = Rows<VT, D>;
-  const bool ok = id >= 0;
-  const size_t row0 = ((size_t)(ok ? id : 0) * a.bs + in_block) * a.Hkv + h;
-  const char* kp = static_cast<const char*>(a.k_cache) + (ok ? row0 * RK::ROWB : 0);
-  const char* vp = static_cast<const char*>(a.v_cache) + (ok ? row0 * RV::ROWB : 0);
-#pragma unroll
-  for (int i = 0; i < RK::CPR / 2; ++i) {
-    const int x = i * 32 + lane, row = x / RK::CPR, c = x % RK::CPR;
-    const bool take = ok && sp.sees(t0 + row);
-    copy16(stage + RK::k_at(row, c), take ? kp + (size_t)row * a.Hkv * RK::ROWB + c * 16 : kp, take);
-  }
-#pragma unroll
-  for (int i = 0; i < RV::CPR / 2; ++i) {
-    const int x = i * 32 + lane, row = x / RV::CPR, c = x % RV::CPR;
-    const bool take = ok && sp.sees(t0 + row);
-    copy16(stage + RK::BYTES + RV::v_at(row, c), take ? vp + (size_t)row * a.Hkv * RV::ROWB + c * 16 : vp,
-           take);
-  }
-}
-
-// What a warp knows of its next 32 tiles, one per lane: the block (-1: bad) and,
-// for block-scaled pools, its scales.
-struct Ahead {
-  int id;
-  float ks;        // K scale
-  int lvs;         // log2 of the V scale
-};
-template <bool BSC>
-__device__ __forceinline__ Ahead look_up(const WinArgs& a, const int32_t* table, const Span& sp, int v,
-                                         int v_end, int h) {
-  Ahead x{-1, 1.f, 0};
-  if (v < v_end) {
-    x.id = __ldg(table + sp.tile(v) * kTok / a.bs);
-    if (x.id < 0 || x.id >= a.num_blocks) {
-      flag_error(a.err_flag, PA_DEV_BAD_BLOCK_ID);
-      x.id = -1;
-    } else if (BSC) {
-      const float ks = __ldg(a.k_scales + (size_t)x.id * a.Hkv + h);
-      const float vs = __ldg(a.v_scales + (size_t)x.id * a.Hkv + h);
-      if (!block_scale_ok(ks) || !block_scale_ok(vs)) {
-        flag_error(a.err_flag, PA_DEV_BAD_SCALE);
-        x.id = -1;
-      } else {
-        x.ks = ks;
-        x.lvs = block_scale_log2(vs);
-      }
-    }
-  }
-  return x;
-}
-
-// The CTA's warps' (m, l, acc) for gc heads joined and written: the output, or a
-// part for the merge.
-template <int D, int HEADS>
-__device__ __forceinline__ void finish(const WinArgs& a, const float* sm_acc, const float* sm_m,
-                                       const float* sm_l, int gc, int b, int hq0, int part, bool last) {
-  for (int i = threadIdx.x; i < gc * D; i += kWarps * 32) {
-    const int g = i / D, d = i - g * D;
-    float M = -FLT_MAX, L = 0.f, O = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * HEADS + g]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float c = ex2(sm_m[w * HEADS + g] - M);
-      L = fmaf(sm_l[w * HEADS + g], c, L);
-      O = fmaf(sm_acc[(w * HEADS + g) * D + d], c, O);
-    }
-    if (last) {
-      store_out(a.out, ((size_t)b * a.Hq + hq0 + g) * D + d, L == 0.f ? 0.f : O / L * a.v_scale,
-                a.out_dtype);
-    } else {
-      const size_t slot = ((size_t)b * a.P + part) * a.Hq + hq0 + g;
-      a.ws_acc[slot * D + d] = O;
-      if (d == 0) { a.ws_m[slot] = M; a.ws_l[slot] = L; }
-    }
-  }
-}
-
-// Zero rows of a sequence with nothing to attend or a bad length (part 0 writes them).
-template <int D>
-__device__ __forceinline__ void zero_rows(const WinArgs& a, int gc, int b, int hq0) {
-  for (int i = threadIdx.x; i < gc * D; i += kWarps * 32)
-    store_out(a.out, ((size_t)b * a.Hq + hq0) * D + i, 0.f, a.out_dtype);
-}
-
-}  // namespace
-
-// KT, VT: pool element types. BSC: both pools hold codes with one scale per
-// block and KV head. CTA = (part, KV head and chunk of 8 query heads, sequence),
-// four warps that take the part's tiles in turn.
 template <int KT, int VT, int D, bool BSC>
-__global__ void __launch_bounds__(kWarps * 32)
-decode_window_kernel(const WinArgs a) {
-  using RK = Rows<KT, D>;
-  using RV = Rows<VT, D>;
-  constexpr bool KBF = KT == PA_BF16, VBF = VT == PA_BF16;
-  constexpr bool K8 = KT == PA_FP8_E4M3, V8 = VT == PA_FP8_E4M3;
-  constexpr int STAGE = RK::BYTES + RV::BYTES;
-  constexpr int NST = stages_for(STAGE);
-  constexpr int KS = D / 16;                    // k-steps of the score product
-  constexpr int NT = D / 8;                     // 8-wide dim tiles of the output product
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sm_q[kHeads * D];
-  __shared__ float sm_f[kHeads];                // score factor of each head
-  __shared__ float sm_m[kWarps * kHeads], sm_l[kWarps * kHeads];
-  static_assert(kWarps * kHeads * D * 4 <= kWarps * NST * STAGE, "the joined sums reuse the rings");
-  pdl_trigger();
-  pdl_wait();
+struct Core {
+  static constexpr bool KBF = KT == PA_BF16, VBF = VT == PA_BF16;
+  static constexpr bool K8 = KT == PA_FP8_E4M3, V8 = VT == PA_FP8_E4M3;
+  static constexpr int EK = esize(KT), EV = esize(VT);
+  static constexpr int TW = D * (EK + EV) <= 256 ? 2 : 1;       // 16-token boxes of a warp per step
+  static constexpr int LBK = D * EK < 128 ? D * EK : 128;       // bytes of a line of a K row
+  static constexpr int LBV = D * EV < 128 ? D * EV : 128;
+  static constexpr int KBYTES = kCons * TW * kTok * D * EK, VBYTES = kCons * TW * kTok * D * EV;
+  static constexpr int STAGE = KBYTES + VBYTES;
+  static constexpr int NST = kRing / STAGE;
+  static constexpr int KS = D / 16;             // k-steps of the score product
+  static constexpr int NT = D / 8;              // 8-wide dim tiles of the output product
+  static constexpr int RUN = K8 ? 16 : 8;       // dims of a lane's run of a K row
+  static constexpr int EPV = V8 && D == 128 ? 16 : 8;   // dims of a lane's run of a V row
+  static constexpr int NS = 2 * NT;             // output values per lane: slot e * NT + j
+  static_assert(NST >= 3 && kRing % STAGE == 0, "ring");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int G = a.Hq / a.Hkv;
-  const int chunks = (G + kHeads - 1) / kHeads;
-  const int h = blockIdx.y / chunks, chunk = blockIdx.y - h * chunks;
-  const int b = blockIdx.z, part = blockIdx.x;
-  const int hq0 = h * G + chunk * kHeads, gc = min(kHeads, G - chunk * kHeads);
-
-  const int ctx = a.context_lens[b];
-  if (bad_context(a, ctx) || ctx == 0) {
-    if (part == 0) {
-      if (ctx != 0 && threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err_flag, PA_DEV_BAD_CTX);
-      zero_rows<D>(a, gc, b, hq0);
-    }
-    return;
-  }
-  const Span sp = span_of(ctx, a.window, a.sinks);
-  const int v0 = part * a.ptiles;
-  if (v0 >= sp.n) return;
-  const int v1 = min(sp.n, v0 + a.ptiles);
-
-  const int32_t* table = a.block_tables + (size_t)b * a.max_blocks;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (NST * STAGE);
-  const int mine = (v1 - v0 - warp + kWarps - 1) / kWarps;     // tiles of this warp (<= 0: none)
-  Ahead now = look_up<BSC>(a, table, sp, v0 + warp + kWarps * lane, v1, h);
-  Ahead next = now;
-  // stage k % NST <- the warp's tile k (tiles 0-31 of the current batch are in
-  // `now`, those of the next one in `next`)
-  auto issue = [&](int k, const Ahead& from) {
-    const int id = __shfl_sync(0xffffffffu, from.id, k & 31);
-    const int t0 = sp.tile(v0 + warp + kWarps * k) * kTok;
-    issue_tile<KT, VT, D>(a, ring + (k % NST) * STAGE, sp, t0, id, t0 & (a.bs - 1), h, lane);
-  };
-#pragma unroll
-  for (int k = 0; k < NST - 1; ++k) {
-    if (k < mine) issue(k, now);
-    copy_commit();
-  }
-
-  // the query heads in fp32; an 8-bit K pool takes them scaled by a power of two
-  // that puts the head's largest element into [2^14, 2^15)
-  for (int r = warp; r < kHeads; r += kWarps) {
-    float x[D / 32];
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      x[e] = r < gc ? load_q1(a.q, ((size_t)b * a.Hq + hq0 + r) * D + e * 32 + lane, a.q_dtype) : 0.f;
-      top = fmaxf(top, fabsf(x[e]));
-    }
-    float factor = a.scale_log2;
-    if (K8) {
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      const int e = (int)(bits >> 23) - 127;                // exponent of the largest element
-      if (e >= -100 && e < 127) {
-        const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);   // 2^(14 - e)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) x[i] *= up;
-        factor = a.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) sm_q[r * D + e * 32 + lane] = x[e];
-    if (lane == 0) sm_f[r] = factor;
-  }
-  __syncthreads();
-  // A operand of the score product: k-step 2 i + j (16-bit K) or 4 i + j (codes)
-  // takes 4 elements of the 8 or 16 of a lane's run
   uint32_t qa[KS][4];
-  constexpr int RUN = K8 ? 16 : 8;
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) {
-    const int i = ks / (RUN / 4), j = ks % (RUN / 4);
-    const float* x = sm_q + g * D + i * 4 * RUN + t * RUN + 4 * j;
-    split2<KBF>(x[0], x[1], qa[ks][0], qa[ks][1]);
-    split2<KBF>(x[2], x[3], qa[ks][2], qa[ks][3]);
-  }
-  const float factor = sm_f[g];
-
-  float m = -FLT_MAX, l = 0.f;
+  float factor, m, l;
   float o[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  // offsets of this lane's operands in a head's box
+  uint32_t kx;                                  // K: key tok_of(g), chunk t (chunk 4 + t: ^ 64)
+  uint32_t vx[2];                               // V: tokens of keys 2 t and 2 t + 1, run g
 
-  for (int k = 0; k < mine; ++k) {
-    // batches of 32 tiles: the next one's blocks are looked up before its first
-    // tile is issued, NST - 1 tiles ahead
-    const int ki = k + NST - 1;
-    if ((ki & 31) == 0 || k == 0) {
-      const int base = (ki & ~31);
-      next = base == 0 ? now : look_up<BSC>(a, table, sp, v0 + warp + kWarps * (base + lane), v1, h);
-    }
-    __syncwarp();                               // every lane has read the stage's last tile
-    if (ki < mine) issue(ki, next);
-    copy_commit();
-    copy_wait<NST - 1>();
-    __syncwarp();
-    if ((k & 31) == 0 && k > 0) now = next;
-    const int id = __shfl_sync(0xffffffffu, now.id, k & 31);
-    const float ks_b = BSC ? __shfl_sync(0xffffffffu, now.ks, k & 31) : 1.f;
-    const int lvs = BSC ? __shfl_sync(0xffffffffu, now.lvs, k & 31) : 0;
-    if (id < 0) continue;
-    const int t0 = sp.tile(v0 + warp + kWarps * k) * kTok;
-    const uint32_t kst = ring + (k % NST) * STAGE, vst = kst + RK::BYTES;
+  static __device__ __forceinline__ int dim_of(int s, int lane) {
+    const int e = s / NT, j = s % NT;
+    return (j / EPV) * (8 * EPV) + (2 * (lane & 3) + e) * EPV + j % EPV;
+  }
+  // 16-byte chunk c of token row r within a line of LB bytes, as TMA swizzles it
+  template <int LB> static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return (uint32_t)(r * LB + ((LB == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+  }
+  __device__ __forceinline__ void init(int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    kx = at<LBK>(tok_of(g), t);
+    for (int i = 0; i < 2; ++i)
+      vx[i] = LBV == 128 ? at<LBV>(tok_of(2 * t + i), g) : at<LBV>(tok_of(2 * t + i), g >> 1) + 8 * (g & 1);
+  }
 
-    // ---- scores: two 8-key products
-    float c[2][4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+  // the unit's query heads [gc][D]; an 8-bit K pool takes each scaled by a power
+  // of two that puts its largest element into [2^14, 2^15)
+  __device__ __forceinline__ void start(const WinArgs& a, size_t q0, int gc, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float x[D / 4];
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < D / (4 * RUN); ++i) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint4 w = lds16(kst + RK::k_at(8 * nt + g, 4 * i + t));
-        if (K8) {
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma<false>(c[nt], qa[4 * i + j], widen2(ww[j]), widen2(ww[j] >> 16));
+      for (int c = 0; c < RUN / 8; ++c) {
+        float* f = x + i * RUN + c * 8;
+        if (g < gc) {
+          const size_t p = q0 + (size_t)g * D + i * 4 * RUN + t * RUN + c * 8;
+          if (a.q_dtype == PA_F32) {
+            widen16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + p), f);
+            widen16<float>(*reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + p + 4), f + 4);
+          } else if (a.q_dtype == PA_F16) {
+            widen16<__half>(*reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + p), f);
+          } else {
+            widen16<__nv_bfloat16>(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + p), f);
+          }
         } else {
-          mma<KBF>(c[nt], qa[2 * i], w.x, w.y);
-          mma<KBF>(c[nt], qa[2 * i + 1], w.z, w.w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = 0.f;
         }
       }
     }
-    // ---- online softmax of head g over keys 8 nt + 2 t + {0, 1}
-    const float f = BSC ? factor * ks_b : factor;
-    float s[2][2];
+    factor = a.scale_log2;
+    if (K8) {
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+      for (int k = 0; k < D / 4; ++k) top = fmaxf(top, fabsf(x[k]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = (int)(__float_as_uint(top) >> 23) - 127;    // exponent of the largest element
+      if (e >= -100 && e < 127) {
+        const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);   // 2^(14 - e)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[nt][e] = (c[nt][e] + c[nt][e + 2]) * f;
-        if (BSC) s[nt][e] += (float)lvs;
+        for (int k = 0; k < D / 4; ++k) x[k] *= up;
+        factor = a.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
       }
-    if (!sp.whole(t0)) {
+    }
+    // k-step 2 i + j (16-bit K) or 4 i + j (codes): 4 elements of the lane's run i
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      split2<KBF>(x[4 * ks], x[4 * ks + 1], qa[ks][0], qa[ks][1]);
+      split2<KBF>(x[4 * ks + 2], x[4 * ks + 3], qa[ks][2], qa[ks][3]);
+    }
+    m = -FLT_MAX;
+    l = 0.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  }
+
+  // TW boxes of the warp's head. kb, vb: the head's part of box 0 in the stage,
+  // kbox, vbox: from box to box, khalf, vhalf: from a row's first line to its second.
+  __device__ __forceinline__ void step(uint32_t kb, uint32_t vb, uint32_t kbox, uint32_t vbox,
+                                       uint32_t khalf, uint32_t vhalf, const Span& sp, const int* t0,
+                                       const float* ks, const int* lvs, int lane) {
+    const int t = lane & 3;
+    // ---- scores: two 8-key products per box
+    float s[TW][2][2];
+#pragma unroll
+    for (int w = 0; w < TW; ++w) {
+      float c[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / (4 * RUN); ++i) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const uint4 v = lds16(kb + w * kbox + (LBK == 128 ? (i >> 1) * khalf : 0) + 8 * nt * LBK +
+                                ((i & 1) ? kx ^ 64u : kx));
+          if (K8) {
+            const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma<false>(c[nt], qa[(4 * i + j) % KS], widen2(ww[j]), widen2(ww[j] >> 16));
+          } else {
+            mma<KBF>(c[nt], qa[(2 * i) % KS], v.x, v.y);
+            mma<KBF>(c[nt], qa[(2 * i + 1) % KS], v.z, v.w);
+          }
+        }
+      }
+      // head g over the tokens of keys 8 nt + 2 t + {0, 1}
+      const float f = BSC ? factor * ks[w] : factor;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!sp.sees(t0 + 8 * nt + 2 * t + e)) s[nt][e] = -CUDART_INF_F;
+        for (int e = 0; e < 2; ++e) {
+          s[w][nt][e] = (c[nt][e] + c[nt][e + 2]) * f;
+          if (BSC) s[w][nt][e] += (float)lvs[w];
+        }
     }
-    float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+    bool whole[TW];
+#pragma unroll
+    for (int w = 0; w < TW; ++w) {
+      whole[w] = t0[w] >= 0 && sp.whole(t0[w]);
+      if (!whole[w]) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (t0[w] < 0 || !sp.sees(t0[w] + 8 * nt + tok_of(2 * t + e))) s[w][nt][e] = -CUDART_INF_F;
+      }
+    }
+    // ---- online softmax
+    float mx = -CUDART_INF_F;
+#pragma unroll
+    for (int w = 0; w < TW; ++w)
+      mx = fmaxf(mx, fmaxf(fmaxf(s[w][0][0], s[w][0][1]), fmaxf(s[w][1][0], s[w][1][1])));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     if (__any_sync(0xffffffffu, mx > m + kMove)) {
@@ -437,265 +245,410 @@ decode_window_kernel(const WinArgs a) {
         o[j][0] *= alpha; o[j][1] *= alpha; o[j][2] *= alpha; o[j][3] *= alpha;
       }
     }
-    float p[2][2], sum = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int w = 0; w < TW; ++w) {
+      float p[2][2], sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        p[nt][e] = ex2(s[nt][e] - m);
-        sum += p[nt][e];
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          p[nt][e] = ex2(s[w][nt][e] - m);
+          sum += p[nt][e];
+        }
+      if (BSC) l = fmaf(sum, __uint_as_float((uint32_t)(127 - lvs[w]) << 23), l);
+      else l += sum;
+      uint32_t pw[4];
+      split2<VBF>(p[0][0], p[0][1], pw[0], pw[1]);
+      split2<VBF>(p[1][0], p[1][1], pw[2], pw[3]);
+      // ---- O += P . V: the lane's tokens are those of keys 2 t, 2 t + 1 and 8 + them
+      if (t0[w] < 0) continue;                  // what lies in the stage may be anything
+      uint32_t keep = 15u;                      // which of the four to take: V rows that are not
+      if (!whole[w]) {                          // visible may hold NaN, their weights are 0
+        keep = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          keep |= sp.sees(t0[w] + 8 * (i >> 1) + tok_of(2 * t + (i & 1))) ? 1u << i : 0u;
       }
-    if (BSC) l = fmaf(sum, __uint_as_float((uint32_t)(127 - lvs) << 23), l);
-    else l += sum;
-    uint32_t pa_[4];
-    split2<VBF>(p[0][0], p[0][1], pa_[0], pa_[1]);
-    split2<VBF>(p[1][0], p[1][1], pa_[2], pa_[3]);
-
-    // ---- O += P . V: the lane's tokens are 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-    if constexpr (V8 && D == 64) {
-      uint2 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-        w[i] = lds8(vst + RV::v_at(row, g >> 1) + 8 * (g & 1));
-      }
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint32_t r0 = q ? w[0].y : w[0].x, r1 = q ? w[1].y : w[1].x;
-        const uint32_t r2 = q ? w[2].y : w[2].x, r3 = q ? w[3].y : w[3].x;
-        const uint32_t x0 = __byte_perm(r0, r1, 0x5140), x1 = __byte_perm(r0, r1, 0x7362);
-        const uint32_t y0 = __byte_perm(r2, r3, 0x5140), y1 = __byte_perm(r2, r3, 0x7362);
-        mma<false>(o[4 * q], pa_, widen2(x0), widen2(y0));
-        mma<false>(o[4 * q + 1], pa_, widen2(x0 >> 16), widen2(y0 >> 16));
-        mma<false>(o[4 * q + 2], pa_, widen2(x1), widen2(y1));
-        mma<false>(o[4 * q + 3], pa_, widen2(x1 >> 16), widen2(y1 >> 16));
-      }
-    } else {
-#pragma unroll
-      for (int cg = 0; cg < RV::CPR / 8; ++cg) {
-        uint4 w[4];
+      const uint32_t base = vb + w * vbox;
+      if constexpr (V8 && D == 64) {
+        uint2 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-          w[i] = lds16(vst + RV::v_at(row, 8 * cg + g));
+          v[i] = lds8(base + 8 * (i >> 1) * LBV + vx[i & 1]);
+          if (!((keep >> i) & 1u)) v[i] = make_uint2(0, 0);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t r0 = (&w[0].x)[q], r1 = (&w[1].x)[q], r2 = (&w[2].x)[q], r3 = (&w[3].x)[q];
-          if (V8) {
-            const uint32_t x0 = __byte_perm(r0, r1, 0x5140), x1 = __byte_perm(r0, r1, 0x7362);
-            const uint32_t y0 = __byte_perm(r2, r3, 0x5140), y1 = __byte_perm(r2, r3, 0x7362);
-            mma<false>(o[4 * q], pa_, widen2(x0), widen2(y0));
-            mma<false>(o[4 * q + 1], pa_, widen2(x0 >> 16), widen2(y0 >> 16));
-            mma<false>(o[4 * q + 2], pa_, widen2(x1), widen2(y1));
-            mma<false>(o[4 * q + 3], pa_, widen2(x1 >> 16), widen2(y1 >> 16));
-          } else {
-            mma<VBF>(o[8 * cg + 2 * q], pa_, __byte_perm(r0, r1, 0x5410), __byte_perm(r2, r3, 0x5410));
-            mma<VBF>(o[8 * cg + 2 * q + 1], pa_, __byte_perm(r0, r1, 0x7632),
-                     __byte_perm(r2, r3, 0x7632));
+        for (int q = 0; q < 2; ++q)
+          codes(q, pw, q ? v[0].y : v[0].x, q ? v[1].y : v[1].x, q ? v[2].y : v[2].x, q ? v[3].y : v[3].x);
+      } else {
+#pragma unroll
+        for (int cg = 0; cg < D * EV / LBV; ++cg) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = lds16(base + cg * vhalf + 8 * (i >> 1) * LBV + vx[i & 1]);
+            if (!((keep >> i) & 1u)) v[i] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t r0 = (&v[0].x)[q], r1 = (&v[1].x)[q], r2 = (&v[2].x)[q], r3 = (&v[3].x)[q];
+            if (V8) {
+              codes(q, pw, r0, r1, r2, r3);
+            } else {
+              mma<VBF>(o[(8 * cg + 2 * q) % NT], pw, __byte_perm(r0, r1, 0x5410), __byte_perm(r2, r3, 0x5410));
+              mma<VBF>(o[(8 * cg + 2 * q + 1) % NT], pw, __byte_perm(r0, r1, 0x7632),
+                       __byte_perm(r2, r3, 0x7632));
+            }
           }
         }
       }
     }
   }
-  copy_wait<0>();
-  __syncthreads();                              // the rings are free
-
-  // ---- join the warps
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
-  if (t == 0) { sm_m[warp * kHeads + g] = m; sm_l[warp * kHeads + g] = l; }
-  float* sm_acc = reinterpret_cast<float*>(smem);
-  constexpr int EPV = V8 && D == 128 ? 16 : 8;  // dims of a lane's run of a V row
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int d = (j / EPV) * (8 * EPV) + 2 * t * EPV + j % EPV;
-    sm_acc[(warp * kHeads + g) * D + d] = o[j][0] + o[j][2];
-    sm_acc[(warp * kHeads + g) * D + d + EPV] = o[j][1] + o[j][3];
+  // four dims' products from four codes of each of the lane's tokens
+  __device__ __forceinline__ void codes(int q, const uint32_t* pw, uint32_t r0, uint32_t r1, uint32_t r2,
+                                        uint32_t r3) {
+    const uint32_t x0 = __byte_perm(r0, r1, 0x5140), x1 = __byte_perm(r0, r1, 0x7362);
+    const uint32_t y0 = __byte_perm(r2, r3, 0x5140), y1 = __byte_perm(r2, r3, 0x7362);
+    mma<false>(o[(4 * q) % NT], pw, widen2(x0), widen2(y0));
+    mma<false>(o[(4 * q + 1) % NT], pw, widen2(x0 >> 16), widen2(y0 >> 16));
+    mma<false>(o[(4 * q + 2) % NT], pw, widen2(x1), widen2(y1));
+    mma<false>(o[(4 * q + 3) % NT], pw, widen2(x1 >> 16), widen2(y1 >> 16));
   }
-  __syncthreads();
-  finish<D, kHeads>(a, sm_acc, sm_m, sm_l, gc, b, hq0, part, sp.n <= a.ptiles);
+  __device__ __forceinline__ float value(int s) const {
+    const int e = s / NT, j = s % NT;
+    return o[j][e] + o[j][e + 2];
+  }
+};
+
+// n consecutive values to out[i ..]: 8 to a 16-bit output or 4 to an fp32 one at once.
+__device__ __forceinline__ void store8_out(void* out, size_t i, const float* f, int dt) {
+  if (dt == PA_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + i);
+    p[0] = make_float4(f[0], f[1], f[2], f[3]);
+    p[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (dt == PA_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
-// fp32 pools: the same walk and ring, products on the CUDA cores (4 query heads
-// per CTA). Scores: lane = (token, half of the dims); output: a lane owns D / 32
-// dims of every head.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32)
-decode_window_f32_kernel(const WinArgs a) {
-  using R = Rows<PA_F32, D>;
-  constexpr int HC = 4;
-  constexpr int STAGE = 2 * R::BYTES;
-  constexpr int NST = stages_for(STAGE);
-  constexpr int PER = D / 32;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float sm_q[HC * D];
-  __shared__ float sm_m[kWarps * HC], sm_l[kWarps * HC];
+constexpr int kMaxStages = 6;
+template <class C> constexpr int join_bytes() { return kCons * C::NS * 32 * 4; }
+// ring | sums to join (groups of fewer than 8 heads) | metadata, barriers
+template <class C> constexpr int smem_bytes() {
+  return 1024 + kRing + join_bytes<C>() + C::NST * (int)sizeof(Meta) + 2 * kMaxStages * 8 + 16;
+}
+
+}  // namespace
+
+template <int KT, int VT, int D, bool BSC>
+__global__ void __launch_bounds__(kThreads, 1)
+decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV) {
+  using C = Core<KT, VT, D, BSC>;
+  constexpr int NST = C::NST, TW = C::TW;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* sm_join = reinterpret_cast<float*>(smem + kRing);
+  Meta* meta = reinterpret_cast<Meta*>(smem + kRing + join_bytes<C>());
+  const uint32_t sring = smem_addr(smem);
+  const uint32_t bars = smem_addr(meta + NST);
+  auto full = [&](int s) { return bars + 16u * (uint32_t)s; };
+  auto empty = [&](int s) { return bars + 16u * (uint32_t)s + 8u; };
+  __shared__ uint32_t sm_abort;
+  __shared__ float sm_m[kCons][kHeads], sm_l[kCons][kHeads];
+  volatile uint32_t* abort_flag = &sm_abort;
   pdl_trigger();
-  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kCons);
+    }
+    sm_abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+
   const int G = a.Hq / a.Hkv;
-  const int chunks = (G + HC - 1) / HC;
-  const int h = blockIdx.y / chunks, chunk = blockIdx.y - h * chunks;
-  const int b = blockIdx.z, part = blockIdx.x;
-  const int hq0 = h * G + chunk * HC, gc = min(HC, G - chunk * HC);
-  const int ctx = a.context_lens[b];
-  if (bad_context(a, ctx) || ctx == 0) {
-    if (part == 0) {
-      if (ctx != 0 && threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err_flag, PA_DEV_BAD_CTX);
-      zero_rows<D>(a, gc, b, hq0);
+  const int hg = a.hg, nsub = kCons / hg, nbox = nsub * TW;
+  const int chunks = (G + kHeads - 1) / kHeads;
+  const int ny = a.Hkv / hg * chunks;
+  const int cta = blockIdx.x;
+  Share w = find_share<kThreads>(a, ny, nbox, cta, gridDim.x);    // (its barriers publish the inits)
+  if (cta >= w.shares) return;
+  const int units = a.B * ny;
+  const uint32_t kboxb = (uint32_t)(hg * kTok * D * C::EK), vboxb = (uint32_t)(hg * kTok * D * C::EV);
+
+  if (warp == kCons) {
+    // ------------------------------------------------------------ producer
+    int seq = 0;
+    bool stop = false;
+    while (!stop && w.p0 < units && w.base0 < w.hi) {
+      const Batch u = next_batch(a, w, ny, nbox, cta, lane);
+      for (int i = 0; i < u.count && !stop; ++i) {
+        const int s0 = __shfl_sync(0xffffffffu, u.s0, i), s1 = __shfl_sync(0xffffffffu, u.s1, i);
+        if (s0 >= s1) continue;
+        const int b = __shfl_sync(0xffffffffu, u.b, i);
+        const int h0 = __shfl_sync(0xffffffffu, u.y, i) / chunks * hg;
+        const Span sp = span_of(a, __shfl_sync(0xffffffffu, u.ctx, i));
+        const int32_t* table = a.block_tables + (size_t)b * a.max_blocks;
+        // this lane's box of step k: its id, two steps ahead; then its scales (lane =
+        // (box, head)), one ahead
+        auto fetch = [&](int k) {
+          const int v = k * nbox + lane;
+          return lane < nbox && k < s1 && v < sp.n ? __ldg(table + sp.tile(v) * kTok / a.bs) : -1;
+        };
+        float ks_n = 1.f, vs_n = 1.f;
+        auto fetch_scales = [&](int id) {
+          if (BSC) {
+            const int bid = __shfl_sync(0xffffffffu, id, lane / hg);
+            if (lane < nbox * hg && bid >= 0 && bid < a.num_blocks) {
+              ks_n = __ldg(a.k_scales + (size_t)bid * a.Hkv + h0 + lane % hg);
+              vs_n = __ldg(a.v_scales + (size_t)bid * a.Hkv + h0 + lane % hg);
+            }
+          }
+        };
+        int id1 = fetch(s0), id2 = fetch(s0 + 1);
+        fetch_scales(id1);
+        for (int k = s0; k < s1; ++k, ++seq) {
+          const int id = id1;
+          const float ks = ks_n, vs = vs_n;
+          id1 = id2;
+          id2 = fetch(k + 2);
+          fetch_scales(id1);
+          const int v = k * nbox + lane;
+          const bool want = lane < nbox && v < sp.n;
+          const int t0 = want ? sp.tile(v) * kTok : -1;
+          const bool ok = want && id >= 0 && id < a.num_blocks;
+          if (want && !ok) flag_error(a.err_flag, PA_DEV_BAD_BLOCK_ID);
+          const uint32_t have = __ballot_sync(0xffffffffu, ok);
+          const int st = seq % NST;
+          bool room = true;
+          if (lane == 0) room = mbar_wait(empty(st), ((seq / NST) & 1) ^ 1, abort_flag, a.wait_ns);
+          if (!__shfl_sync(0xffffffffu, room, 0)) { stop = true; break; }
+          if (lane < kMaxSub) {
+            meta[st].t0[lane] = ok ? t0 : -1;
+            if (BSC) {
+              const bool there = lane < nbox * hg && ((have >> (lane / hg)) & 1u);
+              const bool good = block_scale_ok(ks) && block_scale_ok(vs);
+              if (there && !good) flag_error(a.err_flag, PA_DEV_BAD_SCALE);
+              meta[st].ks[lane] = there && good ? ks : 1.f;
+              meta[st].lvs[lane] = !there || good ? (there ? block_scale_log2(vs) : 0) : kNoScale;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(full(st), (uint32_t)__popc(have) * (kboxb + vboxb));
+          __syncwarp();
+          if (ok) {
+            const uint32_t dst = sring + st * C::STAGE;
+            const int off = t0 & (a.bs - 1);
+            tma_load_5d(dst + lane * kboxb, &tmK, 0, off, h0, 0, id, full(st));
+            tma_load_5d(dst + C::KBYTES + lane * vboxb, &tmV, 0, off, h0, 0, id, full(st));
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      if (stop) {
+        *abort_flag = 1u;
+        flag_error(a.err_flag, PA_DEV_TIMEOUT);
+      }
+      // never leave with copies in flight
+      for (int q = max(0, seq - NST); q < seq; ++q) {
+        const uint64_t b0 = globaltimer();
+        while (!mbar_try(full(q % NST), (q / NST) & 1) && globaltimer() - b0 < kWaitNs) {}
+      }
     }
     return;
   }
-  const Span sp = span_of(ctx, a.window, a.sinks);
-  const int v0 = part * a.ptiles;
-  if (v0 >= sp.n) return;
-  const int v1 = min(sp.n, v0 + a.ptiles);
-  const int32_t* table = a.block_tables + (size_t)b * a.max_blocks;
-  uint8_t* ring_p = smem + warp * (NST * STAGE);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_p);
-  const int mine = (v1 - v0 - warp + kWarps - 1) / kWarps;
-  auto block_of = [&](int k) {
-    return look_up<false>(a, table, sp, v0 + warp + kWarps * k, v1, h).id;
-  };
-  auto issue = [&](int k, int id) {
-    const int t0 = sp.tile(v0 + warp + kWarps * k) * kTok;
-    issue_tile<PA_F32, PA_F32, D>(a, ring + (k % NST) * STAGE, sp, t0, id, t0 & (a.bs - 1), h, lane);
-  };
-  int ids[NST];                                 // blocks of the tiles in the ring
-#pragma unroll
-  for (int k = 0; k < NST - 1; ++k) {
-    ids[k] = block_of(k);
-    if (k < mine) issue(k, ids[k]);
-    copy_commit();
-  }
-  for (int i = threadIdx.x; i < HC * D; i += kWarps * 32)
-    sm_q[i] = i < gc * D ? static_cast<const float*>(a.q)[((size_t)b * a.Hq + hq0) * D + i] * a.scale_log2
-                         : 0.f;
-  __syncthreads();
 
-  float m[HC], l[HC], o[HC][PER];
-#pragma unroll
-  for (int g = 0; g < HC; ++g) {
-    m[g] = -FLT_MAX;
-    l[g] = 0.f;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[g][e] = 0.f;
-  }
-  const int row = lane & 15, hf = lane >> 4;
-  for (int k0 = 0; k0 < mine; k0 += NST) {
-#pragma unroll
-    for (int u = 0; u < NST; ++u) {             // stage = u, so ids[] stays in registers
-      const int k = k0 + u;
-      if (k >= mine) break;
-      const int ki = k + NST - 1;
-      const int nid = block_of(ki);
-      __syncwarp();
-      if (ki < mine) issue(ki, nid);
-      ids[(u + NST - 1) % NST] = nid;
-      copy_commit();
-      copy_wait<NST - 1>();
-      __syncwarp();
-      if (ids[u] < 0) continue;
-      const int t0 = sp.tile(v0 + warp + kWarps * k) * kTok;
-      const uint8_t* kst = ring_p + u * STAGE;
-      const uint8_t* vst = kst + R::BYTES;
-      float s[HC];
-#pragma unroll
-      for (int g = 0; g < HC; ++g) s[g] = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const int cc = hf * (D / 8) + c;
-        const float4 kv = *reinterpret_cast<const float4*>(kst + R::k_at(row, cc));
-#pragma unroll
-        for (int g = 0; g < HC; ++g) {
-          const float4 q = *reinterpret_cast<const float4*>(sm_q + g * D + 4 * cc);
-          s[g] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, fmaf(q.w, kv.w, s[g]))));
+  // -------------------------------------------------------------- consumers
+  const int hd = warp % hg, sub = warp / hg;    // the warp's head of the group and its sub-tile
+  const uint32_t khead = (uint32_t)(hd * kTok * C::LBK), vhead = (uint32_t)(hd * kTok * C::LBV);
+  const uint32_t khalf = (uint32_t)(hg * kTok * C::LBK), vhalf = (uint32_t)(hg * kTok * C::LBV);
+  auto cons_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kCons * 32) : "memory"); };
+  C core;
+  core.init(lane);
+  bool failed = false;
+  int seq = 0;
+  while (w.p0 < units && w.base0 < w.hi) {
+    const int p0 = w.p0;
+    const Batch u = next_batch(a, w, ny, nbox, cta, lane);
+#pragma unroll 1
+    for (int i = 0; i < u.count; ++i) {
+      const int b = __shfl_sync(0xffffffffu, u.b, i), y = __shfl_sync(0xffffffffu, u.y, i);
+      const int s0 = __shfl_sync(0xffffffffu, u.s0, i), s1 = __shfl_sync(0xffffffffu, u.s1, i);
+      const int ctx = __shfl_sync(0xffffffffu, u.ctx, i), n = __shfl_sync(0xffffffffu, u.n, i);
+      const int first = __shfl_sync(0xffffffffu, u.first, i), last = __shfl_sync(0xffffffffu, u.last, i);
+      const bool starts = __shfl_sync(0xffffffffu, (int)u.starts, i);
+      const int h = y / chunks * hg + hd, chunk = y % chunks;
+      const int gc = min(kHeads, G - chunk * kHeads);
+      const size_t row0 = (size_t)b * a.Hq + h * G + chunk * kHeads;   // of this warp's head
+      if (starts && threadIdx.x == 0) a.cuts[p0 + i] = make_int2(first, last);
+      if (n == 0) {
+        // an empty sequence's (or one of a bad length) rows are zeros
+        if (starts && sub == 0) {
+          if (y == 0 && threadIdx.x == 0 && ctx != 0) flag_error(a.err_flag, PA_DEV_BAD_CTX);
+          for (int x = lane; x < gc * D; x += 32) store_out(a.out, row0 * D + x, 0.f, a.out_dtype);
         }
+        continue;
       }
-      const bool sees = sp.sees(t0 + row);
-      float p[HC];
-#pragma unroll
-      for (int g = 0; g < HC; ++g) {
-        s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
-        if (!sees) s[g] = -CUDART_INF_F;
-        float mx = s[g];
-#pragma unroll
-        for (int x = 8; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        const float mn = fmaxf(m[g], mx);
-        const float alpha = exp2f(m[g] - mn);
-        m[g] = mn;
-        p[g] = exp2f(s[g] - mn);
-        l[g] = l[g] * alpha + p[g];             // lanes 0-15 and 16-31 hold the same tokens
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[g][e] *= alpha;
-      }
-#pragma unroll 4
-      for (int r = 0; r < kTok; ++r) {
-        float v[PER];
-        const int d0 = lane * PER;
-        const uint8_t* vr = vst + R::v_at(r, d0 / 4) + (d0 % 4) * 4;
-        if constexpr (PER == 4) {
-          const float4 w = *reinterpret_cast<const float4*>(vr);
-          v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-        } else {
-          const float2 w = *reinterpret_cast<const float2*>(vr);
-          v[0] = w.x; v[1] = w.y;
+      if (s0 >= s1) continue;
+      const Span sp = span_of(a, ctx);
+      core.start(a, row0 * D, gc, lane);
+#pragma unroll 1
+      for (int k = s0; k < s1; ++k, ++seq) {
+        const int st = seq % NST;
+        if (!failed && !mbar_wait(full(st), (seq / NST) & 1, abort_flag, a.wait_ns)) {
+          failed = true;
+          *abort_flag = 1u;
+          flag_error(a.err_flag, PA_DEV_TIMEOUT);
         }
+        if (failed) continue;
+        int t0[TW], lvs[TW];
+        float ks[TW];
+        bool any = false;
 #pragma unroll
-        for (int g = 0; g < HC; ++g) {
-          const float pr = __shfl_sync(0xffffffffu, p[g], r);
+        for (int x = 0; x < TW; ++x) {
+          const int box = sub * TW + x;
+          t0[x] = meta[st].t0[box];
+          ks[x] = 1.f;
+          lvs[x] = 0;
+          if (BSC) {
+            ks[x] = meta[st].ks[box * hg + hd];
+            lvs[x] = meta[st].lvs[box * hg + hd];
+            if (lvs[x] == kNoScale) { t0[x] = -1; lvs[x] = 0; }
+          }
+          any |= t0[x] >= 0;
+        }
+        if (any)
+          core.step(sring + st * C::STAGE + sub * TW * kboxb + khead,
+                    sring + st * C::STAGE + C::KBYTES + sub * TW * vboxb + vhead, kboxb, vboxb, khalf,
+                    vhalf, sp, t0, ks, lvs, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(st));
+      }
+      // ---- the unit's end: this warp's sums to the output or to a piece
+      core.l += __shfl_xor_sync(0xffffffffu, core.l, 1);
+      core.l += __shfl_xor_sync(0xffffffffu, core.l, 2);
+      const bool whole = first == last;
+      const int g = lane >> 2;
+      const size_t slot = 2 * (size_t)cta + (cta == first ? 1 : 0);
+      const size_t prow = slot * (hg * kHeads) + hd * kHeads;          // of the pieces
+      if (nsub == 1) {
+        const float inv = !whole ? 1.f : core.l == 0.f ? 0.f : a.v_scale / core.l;
 #pragma unroll
-          for (int e = 0; e < PER; ++e) o[g][e] = fmaf(pr, v[e], o[g][e]);
+        for (int s = 0; s < C::NS; s += 8) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = core.value(s + k) * inv;
+          const int d = C::dim_of(s, lane);
+          if (whole) {
+            if (g < gc) store8_out(a.out, (row0 + g) * D + d, f, a.out_dtype);
+          } else {
+            store8_out(a.ws_acc, (prow + g) * D + d, f, PA_F32);
+          }
+        }
+        if (!whole && (lane & 3) == 0) {
+          a.ws_m[prow + g] = core.m;
+          a.ws_l[prow + g] = core.l;
+        }
+      } else {
+        // the sub-tiles' warps of a head join their sums, each a part of the values
+        cons_sync();                            // the last unit's sums have been read
+        if ((lane & 3) == 0) { sm_m[warp][g] = core.m; sm_l[warp][g] = core.l; }
+#pragma unroll
+        for (int s = 0; s < C::NS; ++s) sm_join[(warp * C::NS + s) * 32 + lane] = core.value(s);
+        cons_sync();
+        float M = -FLT_MAX, L = 0.f;
+        for (int x = 0; x < nsub; ++x) M = fmaxf(M, sm_m[x * hg + hd][g]);
+        float cf[kCons];
+#pragma unroll
+        for (int x = 0; x < kCons; ++x) {
+          cf[x] = x < nsub ? ex2(sm_m[x * hg + hd][g] - M) : 0.f;
+          if (x < nsub) L = fmaf(sm_l[x * hg + hd][g], cf[x], L);
+        }
+        const float inv = !whole ? 1.f : L == 0.f ? 0.f : a.v_scale / L;
+        for (int s = sub * (C::NS / nsub); s < (sub + 1) * (C::NS / nsub); ++s) {
+          float O = 0.f;
+#pragma unroll
+          for (int x = 0; x < kCons; ++x)
+            if (x < nsub) O = fmaf(sm_join[((x * hg + hd) * C::NS + s) * 32 + lane], cf[x], O);
+          const int d = C::dim_of(s, lane);
+          if (whole) {
+            if (g < gc) store_out(a.out, (row0 + g) * D + d, O * inv, a.out_dtype);
+          } else {
+            a.ws_acc[(prow + g) * D + d] = O;
+          }
+        }
+        if (!whole && sub == 0 && (lane & 3) == 0) {
+          a.ws_m[prow + g] = M;
+          a.ws_l[prow + g] = L;
         }
       }
     }
   }
-  copy_wait<0>();
-  __syncthreads();
-  float* sm_acc = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int g = 0; g < HC; ++g) {
-#pragma unroll
-    for (int x = 8; x >= 1; x >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], x);
-    if (lane == 0) { sm_m[warp * HC + g] = m[g]; sm_l[warp * HC + g] = l[g]; }
-#pragma unroll
-    for (int e = 0; e < PER; ++e) sm_acc[(warp * HC + g) * D + lane * PER + e] = o[g][e];
-  }
-  __syncthreads();
-  finish<D, HC>(a, sm_acc, sm_m, sm_l, gc, b, hq0, part, sp.n <= a.ptiles);
 }
 
-// Sequences cut into parts: one warp per (sequence, query head) joins them.
-template <int D>
+// Units cut between CTAs: NW warps per (sequence, query head) join its pieces.
+template <int D, int NW>
 __global__ void __launch_bounds__(128) decode_window_merge_kernel(const WinArgs a) {
   constexpr int PER = D / 32;
+  __shared__ float sm_l[4], sm_o[4][D];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = blockIdx.x * 4ll + warp;
+  const long long row = blockIdx.x * (4ll / NW) + warp / NW;
+  const int part = warp % NW;
+  // (for NW > 1 the block is one row and takes every branch together)
   if (row >= (long long)a.B * a.Hq) return;
   const int b = (int)(row / a.Hq), hq = (int)(row - (long long)b * a.Hq);
-  const int ctx = a.context_lens[b];
-  if (bad_context(a, ctx) || ctx == 0) return;
-  const Span sp = span_of(ctx, a.window, a.sinks);
-  const int parts = (sp.n + a.ptiles - 1) / a.ptiles;
-  if (parts <= 1) return;
-  const size_t base = (size_t)b * a.P * a.Hq + hq;
+  const int G = a.Hq / a.Hkv, h = hq / G, g = hq - h * G;
+  const int chunks = (G + a.heads - 1) / a.heads;
+  const int y = h / a.hg * chunks + g / a.heads;
+  const int2 cut = a.cuts[(size_t)b * (a.Hkv / a.hg * chunks) + y];
+  if (cut.x == cut.y) return;                  // whole, or empty
+  const int rows = a.hg * a.heads, r = h % a.hg * a.heads + g % a.heads;
+  auto slot = [&](int c) { return (2 * (size_t)c + (c == cut.x ? 1 : 0)) * rows + r; };
   float M = -FLT_MAX;
-  for (int j = lane; j < parts; j += 32) M = fmaxf(M, a.ws_m[base + (size_t)j * a.Hq]);
+  for (int c = cut.x + lane; c <= cut.y; c += 32) M = fmaxf(M, a.ws_m[slot(c)]);
 #pragma unroll
   for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   float L = 0.f, O[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) O[e] = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < parts; ++j) {
-    const size_t slot = base + (size_t)j * a.Hq;
-    const float c = ex2(a.ws_m[slot] - M);
-    L = fmaf(a.ws_l[slot], c, L);
+#pragma unroll 8
+  for (int c = cut.x + part; c <= cut.y; c += NW) {
+    const size_t s = slot(c);
+    const float f = ex2(a.ws_m[s] - M);
+    L = fmaf(a.ws_l[s], f, L);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) O[e] = fmaf(a.ws_acc[slot * D + e * 32 + lane], c, O[e]);
+    for (int e = 0; e < PER; ++e) O[e] = fmaf(a.ws_acc[s * D + e * 32 + lane], f, O[e]);
+  }
+  if (NW > 1) {
+    if (lane == 0) sm_l[warp] = L;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) sm_o[warp][e * 32 + lane] = O[e];
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int x = 1; x < NW; ++x) {
+      L += sm_l[x];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) O[e] += sm_o[x][e * 32 + lane];
+    }
   }
   const float inv = L == 0.f ? 0.f : a.v_scale / L;
 #pragma unroll
@@ -705,32 +658,50 @@ __global__ void __launch_bounds__(128) decode_window_merge_kernel(const WinArgs 
 
 namespace {
 
-// Dynamic shared memory above 48 KB needs the attribute, per device.
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// Pool [NB][bs][Hkv][D] seen as [NB][lines of a row][Hkv][bs][line]: a box of 16
+// tokens of hg heads, every line of their rows.
+bool make_map(const WinArgs& a, const void* pool, int dt, CUtensorMap* m) {
+  auto enc = encode_fn();
+  if (!enc || a.num_blocks <= 0) return false;
+  const int es = dt == PA_FP8_E4M3 ? 1 : 2;
+  const int lb = a.D * es < 128 ? a.D * es : 128, lines = a.D * es / lb;
+  const cuuint64_t row = (cuuint64_t)a.D * es, tok = row * a.Hkv;
+  const cuuint64_t dims[5] = {(cuuint64_t)(lb / es), (cuuint64_t)a.bs, (cuuint64_t)a.Hkv,
+                              (cuuint64_t)lines, (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[4] = {tok, row, (cuuint64_t)lb, tok * a.bs};
+  const cuuint32_t box[5] = {(cuuint32_t)(lb / es), (cuuint32_t)kTok, (cuuint32_t)a.hg, (cuuint32_t)lines, 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return enc(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                        : dt == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             5, const_cast<void*>(pool), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             lb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KT, int VT, int D, bool BSC>
 int launch_window_t(const WinArgs& a, cudaStream_t stream) {
-  constexpr int STAGE = Rows<KT, D>::BYTES + Rows<VT, D>::BYTES;
-  constexpr int SMEM = kWarps * stages_for(STAGE) * STAGE;
-  const int G = a.Hq / a.Hkv, chunks = (G + kHeads - 1) / kHeads;
+  constexpr int SMEM = smem_bytes<Core<KT, VT, D, BSC>>();
+  static_assert(SMEM + 1024 <= 227 * 1024, "shared memory per CTA");
   auto kern = decode_window_kernel<KT, VT, D, BSC>;
-  if (allow_smem(kern, SMEM) != cudaSuccess) return PA_ERR_CUDA;
-  const dim3 grid((unsigned)a.P, (unsigned)(a.Hkv * chunks), (unsigned)a.B);
-  return launch_k(kern, grid, dim3(kWarps * 32), SMEM, stream, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-}
-
-template <int D>
-int launch_window_f32(const WinArgs& a, cudaStream_t stream) {
-  constexpr int STAGE = 2 * Rows<PA_F32, D>::BYTES;
-  constexpr int SMEM = kWarps * stages_for(STAGE) * STAGE;
-  const int G = a.Hq / a.Hkv, chunks = (G + 3) / 4;
-  auto kern = decode_window_f32_kernel<D>;
-  if (allow_smem(kern, SMEM) != cudaSuccess) return PA_ERR_CUDA;
-  const dim3 grid((unsigned)a.P, (unsigned)(a.Hkv * chunks), (unsigned)a.B);
-  return launch_k(kern, grid, dim3(kWarps * 32), SMEM, stream, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  // dynamic shared memory above 48 KB needs the attribute, on the current device
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
+    return PA_ERR_CUDA;
+  CUtensorMap k, v;
+  if (!make_map(a, a.k_cache, KT, &k) || !make_map(a, a.v_cache, VT, &v)) return PA_ERR_CUDA;
+  return launch_k(kern, dim3((unsigned)a.grid), dim3(kThreads), SMEM, stream, a, k, v) == cudaSuccess
+             ? PA_OK : PA_ERR_CUDA;
 }
 
 template <int D>
@@ -738,7 +709,6 @@ int launch_window_d(const WinArgs& a, cudaStream_t stream) {
   constexpr int F8 = PA_FP8_E4M3;
   if (a.k_scales) return launch_window_t<F8, F8, D, true>(a, stream);
   const int k = a.k_dtype, v = a.v_dtype;
-  if (k == PA_F32 && v == PA_F32) return launch_window_f32<D>(a, stream);
   if (k == F8 && v == F8) return launch_window_t<F8, F8, D, false>(a, stream);
   if (k == PA_F16 && v == PA_F16) return launch_window_t<PA_F16, PA_F16, D, false>(a, stream);
   if (k == PA_BF16 && v == PA_BF16) return launch_window_t<PA_BF16, PA_BF16, D, false>(a, stream);
@@ -749,12 +719,31 @@ int launch_window_d(const WinArgs& a, cudaStream_t stream) {
   return PA_ERR_DTYPE;
 }
 
+template <int D>
+int launch_merge_d(const WinArgs& a, cudaStream_t stream) {
+  const long long rows = (long long)a.B * a.Hq;
+  // few rows: four warps share one, as their units may be cut between many CTAs
+  const cudaError_t e =
+      rows <= 2048 ? launch_k(decode_window_merge_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, stream, a)
+                   : launch_k(decode_window_merge_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0,
+                              stream, a);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
 }  // namespace
 
-// Parts: enough CTAs for every SM several times over, at least two tiles per
-// warp in each.
+// The unit of work, and one CTA per SM (fewer when there cannot be that many shares).
 void plan_window(WinArgs& a) {
   const int G = a.Hq / a.Hkv;
+  if (a.k_dtype == PA_F32) {
+    a.hg = 1;
+    a.heads = 4;
+  } else {
+    a.hg = a.Hkv % 8 == 0 ? 8 : a.Hkv % 4 == 0 ? 4 : a.Hkv % 2 == 0 ? 2 : 1;
+    a.heads = kHeads;
+  }
   const int mc = a.max_context_len > 0 ? a.max_context_len : 1;
   long long tiles = (mc + (long long)kTok - 1) / kTok;
   if (a.window > 0) {
@@ -762,26 +751,36 @@ void plan_window(WinArgs& a) {
                         ((long long)a.sinks + kTok - 1) / kTok;
     if (w < tiles) tiles = w;
   }
-  const long long units = (long long)a.B * a.Hkv * ((G + kHeads - 1) / kHeads);
-  long long P = (8LL * kSMs + units - 1) / units;
-  const long long most = (tiles + 2 * kWarps - 1) / (2 * kWarps);
-  if (P > most) P = most;
-  if (P < 1) P = 1;
-  a.ptiles = (int)((tiles + P - 1) / P);
-  a.P = (int)((tiles + a.ptiles - 1) / a.ptiles);
+  const double units = (double)a.B * (a.Hkv / a.hg) * ((G + a.heads - 1) / a.heads);
+  const double most = units * ((double)tiles * kTileCost + kUnitCost) / kMinShare;
+  const int sms = sm_count_cached();
+  a.grid = most >= sms ? sms : most < 1 ? 1 : (int)most;
 }
 
-size_t window_scratch_bytes(int B, int Hq, int D, int P) { return workspace_bytes_for(B, Hq, D, P); }
+// Two piece slots per CTA, then where each unit is cut.
+size_t window_scratch_bytes(const WinArgs& a) {
+  const size_t rows = 2 * (size_t)a.grid * a.hg * a.heads;
+  const int G = a.Hq / a.Hkv;
+  return up256(rows * a.D * 4) + 2 * up256(rows * 4) +
+         up256((size_t)a.B * (a.Hkv / a.hg) * ((G + a.heads - 1) / a.heads) * sizeof(int2));
+}
+void carve_window(WinArgs& a, char* w) {
+  const size_t rows = 2 * (size_t)a.grid * a.hg * a.heads;
+  a.ws_acc = reinterpret_cast<float*>(w);
+  w += up256(rows * a.D * 4);
+  a.ws_m = reinterpret_cast<float*>(w);
+  w += up256(rows * 4);
+  a.ws_l = reinterpret_cast<float*>(w);
+  w += up256(rows * 4);
+  a.cuts = reinterpret_cast<int2*>(w);
+}
 
 int launch_decode_window(const WinArgs& a, cudaStream_t stream) {
-  int rc = a.D == 64 ? launch_window_d<64>(a, stream) : launch_window_d<128>(a, stream);
-  if (rc == PA_OK && a.P > 1) {
-    const dim3 grid((unsigned)(((long long)a.B * a.Hq + 3) / 4));
-    const cudaError_t e = a.D == 64
-        ? launch_k(decode_window_merge_kernel<64>, grid, dim3(128), 0, stream, a)
-        : launch_k(decode_window_merge_kernel<128>, grid, dim3(128), 0, stream, a);
-    rc = e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-  }
+  int rc = a.k_dtype == PA_F32 ? launch_decode_window_f32(a, stream)
+           : a.D == 64 ? launch_window_d<64>(a, stream) : launch_window_d<128>(a, stream);
+  // one CTA holds every unit whole
+  if (rc == PA_OK && a.grid > 1)
+    rc = a.D == 64 ? launch_merge_d<64>(a, stream) : launch_merge_d<128>(a, stream);
   return rc;
 }
 

@@ -37,16 +37,6 @@ int kernel_override() {
   return 0;
 }
 
-// Limit of every pipeline wait of the tensor-core kernels, in ns (1 s; the
-// environment variable PA_TC_WAIT_NS lowers it, for tests of the timeout path).
-unsigned long long tc_wait_ns() {
-  const char* s = std::getenv("PA_TC_WAIT_NS");
-  if (!s || !*s) return 1000000000ull;
-  char* end = nullptr;
-  const unsigned long long v = std::strtoull(s, &end, 10);
-  return (end && *end == 0 && v <= 1000000000ull) ? v : 1000000000ull;
-}
-
 // The timeout-path test's hook (PA_TC_TEST_WITHHOLD_Q=1): the tensor-core
 // kernel leaves the first unit's query unloaded, so the wait for it runs out.
 int tc_test_withhold_q() {
@@ -77,6 +67,16 @@ unsigned long long next_epoch() {
 }
 
 }  // namespace
+
+// Limit of every pipeline wait of the tensor-core kernels, in ns (1 s; the
+// environment variable PA_TC_WAIT_NS lowers it, for tests of the timeout path).
+unsigned long long tc_wait_ns() {
+  const char* s = std::getenv("PA_TC_WAIT_NS");
+  if (!s || !*s) return 1000000000ull;
+  char* end = nullptr;
+  const unsigned long long v = std::strtoull(s, &end, 10);
+  return (end && *end == 0 && v <= 1000000000ull) ? v : 1000000000ull;
+}
 
 // SM count of the current device (148 on B200; also the fallback with no device).
 int sm_count_cached() {

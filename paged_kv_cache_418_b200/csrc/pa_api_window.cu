@@ -82,17 +82,11 @@ int decode_window_impl(void* out, int out_dtype, const void* query, int q_dtype,
   a.window = window; a.sinks = num_sinks; a.max_context_len = max_context_len;
   a.err_flag = err_flag;
   plan_window(a);
-  const size_t need = window_scratch_bytes(B, Hq, D, a.P);
-  if (need) {
-    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-      return PA_ERR_WORKSPACE;
-    const size_t rows = (size_t)B * Hq * a.P;
-    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    char* w = static_cast<char*>(workspace);
-    a.ws_acc = reinterpret_cast<float*>(w);
-    a.ws_m = reinterpret_cast<float*>(w + up(rows * D * 4));
-    a.ws_l = reinterpret_cast<float*>(w + up(rows * D * 4) + up(rows * 4));
-  }
+  const size_t need = window_scratch_bytes(a);
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PA_ERR_WORKSPACE;
+  carve_window(a, static_cast<char*>(workspace));
+  a.wait_ns = tc_wait_ns();
   return launch_decode_window(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -213,8 +207,14 @@ size_t pa_window_workspace_size(int B, int Hq, int Hkv, int D, int max_context_l
   WinArgs a{};
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.max_context_len = max_context_len;
   a.window = window; a.sinks = num_sinks;
+  // enough for any pool type
+  a.k_dtype = PA_F32;
   plan_window(a);
-  return window_scratch_bytes(B, Hq, D, a.P);
+  const size_t f32 = window_scratch_bytes(a);
+  a.k_dtype = PA_F16;
+  plan_window(a);
+  const size_t other = window_scratch_bytes(a);
+  return f32 > other ? f32 : other;
 }
 
 int pa_decode_window_kv(void* out, int out_dtype, const void* query, int q_dtype,

@@ -211,15 +211,22 @@ struct WinArgs {
   float v_scale;                // value of one V unit (per-pool scale; 1 otherwise)
   int window, sinks;            // window 0: every token
   int max_context_len;
-  int P, ptiles;                // parts per (sequence, KV head chunk), 16-token tiles per part
-  float* ws_acc;                // [B][P][Hq][D]
-  float* ws_m;                  // [B][P][Hq]
+  int hg, heads;                // a unit of work: hg KV heads, up to `heads` query heads of each
+  int grid;                     // CTAs
+  float* ws_acc;                // [2 * grid] pieces [hg * heads][D]
+  float* ws_m;                  // [2 * grid][hg * heads]
   float* ws_l;
+  int2* cuts;                   // per unit: the CTAs that hold its first and last step
+  unsigned long long wait_ns;   // limit of every pipeline wait
   uint32_t* err_flag;
 };
-// Parts and tiles per part of a windowed decode; its scratch.
+// Grid of a windowed decode; its scratch and the carve-up of it.
 void plan_window(WinArgs& a);
-size_t window_scratch_bytes(int B, int Hq, int D, int P);
+size_t window_scratch_bytes(const WinArgs& a);
+void carve_window(WinArgs& a, char* workspace);
+int launch_decode_window_f32(const WinArgs& a, cudaStream_t stream);
+// Limit of every pipeline wait of the tensor-core kernels, in ns.
+unsigned long long tc_wait_ns();
 int launch_decode_window(const WinArgs& a, cudaStream_t stream);
 
 int launch_swap_blocks(void* dst_key, void* dst_value, const void* src_key,

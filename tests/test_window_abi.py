@@ -73,7 +73,7 @@ def test_rope_blk8_refusals(kw, status):
     (dict(kdt=1), 3), (dict(kdt=3, ksc=0.0), 2), (dict(vdt=3, vsc=INF), 2), (dict(qdt=0, kdt=0, vdt=3), 3),
     (dict(odt=1), 3), (dict(D=80), 4), (dict(bs=64), 4), (dict(Hq=6), 4), (dict(Hq=7), 4), (dict(scale=NAN), 2),
     (dict(mb=0), 2), (dict(mc=-1), 2), (dict(B=65536), 4), (dict(q=None), 1), (dict(cl=None), 1),
-    (dict(out=8), 7), (dict(B=1, Hq=1, Hkv=1, mc=100000, window=90000, mb=9000), 5),
+    (dict(out=8), 7), (dict(ws=256, wsb=100), 5), (dict(B=1, Hq=1, Hkv=1, mc=100000, window=90000, mb=9000), 5),
     (dict(B=1, Hq=1, Hkv=1, mc=100000, window=90000, mb=9000, ws=257, wsb=1 << 40), 5)])
 def test_decode_window_refusals(kw, status):
     assert call("pa_decode_window_kv", DEC, **kw) == status
@@ -112,8 +112,11 @@ def test_copy_scales_refusals():
 def test_workspace_size():
     n = ops.pa_window_workspace_size
     assert n(0, 8, 2, 128, 100) == 0 and n(1, 7, 2, 128, 100) == 0 and n(1, 8, 2, 128, 100, -1) == 0
-    assert n(1, 8, 2, 128, 16) == 0                               # one tile: nothing to join
-    assert n(1, 8, 2, 128, 100000) > 0
+    # two piece slots per CTA (148 without a device) of 2 KV heads' 8 query heads each, and where each
+    # unit of work is cut
+    up = lambda x: (x + 255) // 256 * 256
+    assert n(1, 8, 2, 128, 100000) == up(296 * 16 * 128 * 4) + 2 * up(296 * 16 * 4) + up(8)
+    assert 0 < n(1, 8, 2, 128, 16) < n(1, 8, 2, 128, 100000)
     # a window bounds it, whatever the context
     assert n(1, 8, 2, 128, 10 ** 9, 512, 4) == n(1, 8, 2, 128, 10 ** 6, 512, 4)
     for B in (1, 3, 64, 1000, 65535):

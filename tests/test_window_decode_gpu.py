@@ -57,7 +57,7 @@ TYPES = [("f32", "f32", "f32"), ("f16", "f16", "f16"), ("bf16", "bf16", "bf16"),
 @pytest.mark.parametrize("qt,kt,vt", TYPES)
 @pytest.mark.parametrize("D,bs,G,Hkv,window,sinks", [
     (128, 16, 8, 2, 100, 4), (64, 32, 1, 3, 33, 17), (128, 32, 16, 1, 16, 0), (64, 16, 4, 2, 1, 1),
-    (128, 16, 2, 2, 257, 40)])
+    (128, 16, 2, 2, 257, 40), (128, 32, 2, 8, 90, 3), (64, 16, 16, 8, 200, 70), (128, 16, 1, 12, 70, 0)])
 def test_window_every_type(qt, kt, vt, D, bs, G, Hkv, window, sinks):
     ks, vs = (0.5, 0.25)
     P, q, scale, ref, tol = _case(D + bs + G + window, CTX, G * Hkv, Hkv, D, bs, qt, kt, vt, window,
@@ -84,7 +84,7 @@ def test_window_edges(window, sinks):
 @pytest.mark.parametrize("qt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("D,bs,G,Hkv,window,sinks", [
     (128, 16, 8, 2, 0, 0), (64, 32, 1, 3, 0, 9), (128, 32, 16, 1, 70, 5), (64, 16, 4, 2, 300, 0),
-    (128, 16, 1, 4, 0, 0)])
+    (128, 16, 1, 4, 0, 0), (128, 16, 8, 8, 0, 0), (64, 32, 2, 16, 150, 20), (128, 32, 16, 8, 0, 0)])
 def test_blk8_decode(qt, D, bs, G, Hkv, window, sinks):
     P, q, scale, ref, tol = _case(3 * D + bs + G, CTX, G * Hkv, Hkv, D, bs, qt, "fp8", "fp8", window,
                                   sinks, blk8=True, spread=3)
@@ -178,7 +178,6 @@ def test_long_context_one_sequence_and_a_large_loose_bound():
 
 
 def test_two_graphs_share_a_workspace_and_replay():
-    kw = dict(window=500, sinks=4)
     A = _case(61, [900, 20, 333], 16, 2, 128, 16, "bf16", "bf16", "bf16", 500, 4)
     B = _case(62, [77, 1200], 16, 2, 128, 16, "bf16", "fp8", "fp8", 0, 0, blk8=True, spread=2)
     n = max(ops.pa_window_workspace_size(3, 16, 2, 128, 900, 500, 4),
@@ -203,13 +202,13 @@ def test_two_graphs_share_a_workspace_and_replay():
         gr = torch.cuda.CUDAGraph()
         with torch.cuda.graph(gr):
             call()
-        graphs.append((gr, out, first))
+        graphs.append((gr, out, first, call))    # (call keeps the inputs alive)
     for _ in range(3):
-        for gr, out, _ in graphs:
+        for gr, out, *_ in graphs:
             out.fill_(float("nan"))
             gr.replay()
     torch.cuda.synchronize()
-    for _, out, first in graphs:
+    for _, out, first, _ in graphs:
         assert torch.equal(out, first)              # the same bits, replay after replay
 
 
