@@ -66,7 +66,7 @@ namespace {
 using namespace tc;
 
 constexpr int kCons = 8;                        // consumer warps
-constexpr int kThreads = (kCons + 1) * 32;
+constexpr int kThreads = (kCons + 4) * 32;      // two warpgroups of consumers, one with the producer
 constexpr int kRing = 192 * 1024;
 constexpr int kHeads = 8;                       // query heads of a KV head per unit
 constexpr int kMaxSub = 16;                     // (box, head) pairs of a step
@@ -198,8 +198,11 @@ struct Core {
           if (K8) {
             const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma<false>(c[nt], qa[(4 * i + j) % KS], widen2(ww[j]), widen2(ww[j] >> 16));
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b0, b1;
+              widen4(ww[j], b0, b1);
+              mma<false>(c[nt], qa[(4 * i + j) % KS], b0, b1);
+            }
           } else {
             mma<KBF>(c[nt], qa[(2 * i) % KS], v.x, v.y);
             mma<KBF>(c[nt], qa[(2 * i + 1) % KS], v.z, v.w);
@@ -309,10 +312,15 @@ struct Core {
                                         uint32_t r3) {
     const uint32_t x0 = __byte_perm(r0, r1, 0x5140), x1 = __byte_perm(r0, r1, 0x7362);
     const uint32_t y0 = __byte_perm(r2, r3, 0x5140), y1 = __byte_perm(r2, r3, 0x7362);
-    mma<false>(o[(4 * q) % NT], pw, widen2(x0), widen2(y0));
-    mma<false>(o[(4 * q + 1) % NT], pw, widen2(x0 >> 16), widen2(y0 >> 16));
-    mma<false>(o[(4 * q + 2) % NT], pw, widen2(x1), widen2(y1));
-    mma<false>(o[(4 * q + 3) % NT], pw, widen2(x1 >> 16), widen2(y1 >> 16));
+    uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+    widen4(x0, a0, a1);
+    widen4(x1, a2, a3);
+    widen4(y0, b0, b1);
+    widen4(y1, b2, b3);
+    mma<false>(o[(4 * q) % NT], pw, a0, b0);
+    mma<false>(o[(4 * q + 1) % NT], pw, a1, b1);
+    mma<false>(o[(4 * q + 2) % NT], pw, a2, b2);
+    mma<false>(o[(4 * q + 3) % NT], pw, a3, b3);
   }
   __device__ __forceinline__ float value(int s) const {
     const int e = s / NT, j = s % NT;
@@ -371,6 +379,10 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
   volatile uint32_t* abort_flag = &sm_abort;
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == kCons * 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(full(s), 1);
@@ -391,7 +403,11 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
   const int units = a.B * ny;
   const uint32_t kboxb = (uint32_t)(hg * kTok * D * C::EK), vboxb = (uint32_t)(hg * kTok * D * C::EV);
 
-  if (warp == kCons) {
+  // 384 threads are launched with 168 registers each; the producer's warpgroup gives
+  // half of its own to the consumers: 128 * 88 + 256 * 208 = 64,512 = 384 * 168
+  if (warp >= kCons) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp > kCons) return;
     // ------------------------------------------------------------ producer
     int seq = 0;
     bool stop = false;
@@ -438,6 +454,14 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
           bool room = true;
           if (lane == 0) room = mbar_wait(empty(st), ((seq / NST) & 1) ^ 1, abort_flag, a.wait_ns);
           if (!__shfl_sync(0xffffffffu, room, 0)) { stop = true; break; }
+          // the copies first: the step's barrier cannot complete before lane 0 arrives
+          // with the expected bytes, once the scales are here and written
+          if (ok) {
+            const uint32_t dst = sring + st * C::STAGE;
+            const int off = t0 & (a.bs - 1);
+            tma_load_5d(dst + lane * kboxb, &tmK, 0, off, h0, 0, id, full(st));
+            tma_load_5d(dst + C::KBYTES + lane * vboxb, &tmV, 0, off, h0, 0, id, full(st));
+          }
           if (lane < kMaxSub) {
             meta[st].t0[lane] = ok ? t0 : -1;
             if (BSC) {
@@ -450,13 +474,6 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
           }
           __syncwarp();
           if (lane == 0) mbar_expect_tx(full(st), (uint32_t)__popc(have) * (kboxb + vboxb));
-          __syncwarp();
-          if (ok) {
-            const uint32_t dst = sring + st * C::STAGE;
-            const int off = t0 & (a.bs - 1);
-            tma_load_5d(dst + lane * kboxb, &tmK, 0, off, h0, 0, id, full(st));
-            tma_load_5d(dst + C::KBYTES + lane * vboxb, &tmV, 0, off, h0, 0, id, full(st));
-          }
         }
       }
     }
@@ -475,6 +492,7 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
   }
 
   // -------------------------------------------------------------- consumers
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   const int hd = warp % hg, sub = warp / hg;    // the warp's head of the group and its sub-tile
   const uint32_t khead = (uint32_t)(hd * kTok * C::LBK), vhead = (uint32_t)(hd * kTok * C::LBV);
   const uint32_t khalf = (uint32_t)(hg * kTok * C::LBK), vhalf = (uint32_t)(hg * kTok * C::LBV);
@@ -602,17 +620,18 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
   }
 }
 
-// Units cut between CTAs: NW warps per (sequence, query head) join its pieces.
+// Units cut between CTAs: NW warps per (sequence, query head) join its pieces,
+// every NW-th each, four pieces' loads in flight at a time.
 template <int D, int NW>
-__global__ void __launch_bounds__(128) decode_window_merge_kernel(const WinArgs a) {
-  constexpr int PER = D / 32;
-  __shared__ float sm_l[4], sm_o[4][D];
+__global__ void __launch_bounds__(NW < 4 ? 128 : NW * 32) decode_window_merge_kernel(const WinArgs a) {
+  constexpr int PER = D / 32, RPB = NW < 4 ? 4 / NW : 1;         // rows per block
+  __shared__ float sm_m[NW], sm_l[NW], sm_o[NW][D];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = blockIdx.x * (4ll / NW) + warp / NW;
+  const long long row = blockIdx.x * (long long)RPB + warp / NW;
   const int part = warp % NW;
-  // (for NW > 1 the block is one row and takes every branch together)
+  // (for NW >= 4 the block is one row and takes every branch together)
   if (row >= (long long)a.B * a.Hq) return;
   const int b = (int)(row / a.Hq), hq = (int)(row - (long long)b * a.Hq);
   const int G = a.Hq / a.Hkv, h = hq / G, g = hq - h * G;
@@ -621,39 +640,68 @@ __global__ void __launch_bounds__(128) decode_window_merge_kernel(const WinArgs 
   const int2 cut = a.cuts[(size_t)b * (a.Hkv / a.hg * chunks) + y];
   if (cut.x == cut.y) return;                  // whole, or empty
   const int rows = a.hg * a.heads, r = h % a.hg * a.heads + g % a.heads;
-  auto slot = [&](int c) { return (2 * (size_t)c + (c == cut.x ? 1 : 0)) * rows + r; };
-  float M = -FLT_MAX;
-  for (int c = cut.x + lane; c <= cut.y; c += 32) M = fmaxf(M, a.ws_m[slot(c)]);
-#pragma unroll
-  for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  float L = 0.f, O[PER];
+  float M = -FLT_MAX, L = 0.f, O[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) O[e] = 0.f;
-#pragma unroll 8
-  for (int c = cut.x + part; c <= cut.y; c += NW) {
-    const size_t s = slot(c);
-    const float f = ex2(a.ws_m[s] - M);
-    L = fmaf(a.ws_l[s], f, L);
+  for (int c0 = cut.x + part; c0 <= cut.y; c0 += 4 * NW) {
+    float m[4], l[4], v[4][PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) O[e] = fmaf(a.ws_acc[s * D + e * 32 + lane], f, O[e]);
+    for (int k = 0; k < 4; ++k) {
+      const int c = min(c0 + k * NW, cut.y);
+      const size_t s = (2 * (size_t)c + (c == cut.x ? 1 : 0)) * rows + r;
+      m[k] = a.ws_m[s];
+      l[k] = a.ws_l[s];
+      const float* p = a.ws_acc + s * D + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[k][0] = x.x; v[k][1] = x.y;
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c0 + k * NW <= cut.y) mn = fmaxf(mn, m[k]);
+    const float cs = ex2(M - mn);
+    M = mn;
+    L *= cs;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) O[e] *= cs;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (c0 + k * NW > cut.y) continue;
+      const float f = ex2(m[k] - M);
+      L = fmaf(l[k], f, L);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) O[e] = fmaf(v[k][e], f, O[e]);
+    }
   }
-  if (NW > 1) {
-    if (lane == 0) sm_l[warp] = L;
+  if (NW >= 4) {
+    if (lane == 0) { sm_m[warp] = M; sm_l[warp] = L; }
 #pragma unroll
-    for (int e = 0; e < PER; ++e) sm_o[warp][e * 32 + lane] = O[e];
+    for (int e = 0; e < PER; ++e) sm_o[warp][lane * PER + e] = O[e];
     __syncthreads();
     if (part != 0) return;
+    M = -FLT_MAX;
+    L = 0.f;
 #pragma unroll
-    for (int x = 1; x < NW; ++x) {
-      L += sm_l[x];
+    for (int e = 0; e < PER; ++e) O[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) O[e] += sm_o[x][e * 32 + lane];
+    for (int x = 0; x < NW; ++x) M = fmaxf(M, sm_m[x]);
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+      const float f = ex2(sm_m[x] - M);
+      L = fmaf(sm_l[x], f, L);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) O[e] = fmaf(sm_o[x][lane * PER + e], f, O[e]);
     }
   }
   const float inv = L == 0.f ? 0.f : a.v_scale / L;
 #pragma unroll
   for (int e = 0; e < PER; ++e)
-    store_out(a.out, (size_t)row * D + e * 32 + lane, O[e] * inv, a.out_dtype);
+    store_out(a.out, (size_t)row * D + lane * PER + e, O[e] * inv, a.out_dtype);
 }
 
 namespace {
@@ -722,11 +770,16 @@ int launch_window_d(const WinArgs& a, cudaStream_t stream) {
 template <int D>
 int launch_merge_d(const WinArgs& a, cudaStream_t stream) {
   const long long rows = (long long)a.B * a.Hq;
-  // few rows: four warps share one, as their units may be cut between many CTAs
-  const cudaError_t e =
-      rows <= 2048 ? launch_k(decode_window_merge_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, stream, a)
-                   : launch_k(decode_window_merge_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0,
-                              stream, a);
+  // warps per row by the pieces to expect: with few units most CTAs hold a part of
+  // one; with many, a unit is rarely cut in more than two or three
+  const long long units = rows / (a.hg * a.heads) + 1;
+  cudaError_t e;
+  if (units < a.grid / 8)
+    e = launch_k(decode_window_merge_kernel<D, 16>, dim3((unsigned)rows), dim3(512), 0, stream, a);
+  else if (units < a.grid)
+    e = launch_k(decode_window_merge_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, stream, a);
+  else
+    e = launch_k(decode_window_merge_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

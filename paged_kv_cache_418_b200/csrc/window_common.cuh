@@ -95,13 +95,13 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
   }
 }
 
-// Two E4M3 codes (the low 16 bits) as packed f16, exactly.
-__device__ __forceinline__ uint32_t widen2(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four E4M3 codes as two pairs of packed f16, exactly.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
-constexpr int esize(int dt) { return dt == PA_F32 ? 4 : dt == PA_FP8_E4M3 ? 1 : 2; }
+constexpr int esize(int dt) { return dt == PA_FP8_E4M3 ? 1 : 2; }
 
 // Work split. A unit is (sequence, y) with y < ny the KV heads or groups of them and
 // the chunks of their query heads; it has ceil(n / step) steps of `step` tiles and
@@ -117,9 +117,16 @@ struct Share {
 
 __device__ __forceinline__ int steps_of(const Span& s, int step) { return (s.n + step - 1) / step; }
 
+// a / b for non-negative numbers, in 32 bits where they fit (a 64-bit division is a
+// call of some hundred instructions, and a share starts with several).
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if ((unsigned long long)(a | b) >> 32) return a / b;
+  return (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // The CTA whose share holds position pos: share c is [c C / n, (c + 1) C / n).
 __device__ __forceinline__ int share_of(long long pos, const Share& w) {
-  return (int)(((pos + 1) * w.shares - 1) / w.total);
+  return (int)quot((pos + 1) * w.shares - 1, w.total);
 }
 
 // The share of CTA cta; every thread of the CTA calls it (two barriers).
@@ -154,15 +161,15 @@ __device__ __forceinline__ Share find_share(const WinArgs& a, int ny, int step, 
     w.total += sm_scan[i];
   }
   w.shares = (int)min((long long)ctas, max(1ll, w.total / kMinShare));
-  w.lo = (long long)cta * w.total / w.shares;
-  w.hi = (long long)(cta + 1) * w.total / w.shares;
+  w.lo = quot(cta * w.total, w.shares);
+  w.hi = quot((cta + 1) * w.total, w.shares);
   if (w.lo >= before && w.lo < before + sum) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       const long long cb = cost_of(b);
       if (w.lo < at + cb) {
-        const long long one = cb / ny;
-        const int y = (int)((w.lo - at) / one);
+        const long long one = quot(cb, ny);
+        const int y = (int)quot(w.lo - at, one);
         sm_first = b * ny + y;
         sm_base = at + y * one;
         break;
