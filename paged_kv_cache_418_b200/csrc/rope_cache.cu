@@ -67,78 +67,131 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
   b = rb;
 }
 
-}  // namespace
+// One item is 16 elements of one head: 8 pairs of the rotated part (elements e0 ..
+// and e1 ..), or 16 elements behind it. A thread keeps its place c in the head (its
+// stride over the heads is a multiple of a head's items), so it loads its 8 cosines
+// and sines once per token.
+struct Place {
+  int e0, e1;          // first elements of the item's two runs of 8
+  bool turned;
+};
+template <bool IL> __device__ __forceinline__ Place place_of(int c, int rot) {
+  const int half = rot / 2;
+  Place p;
+  p.turned = c < half / 8;
+  p.e0 = p.turned && !IL ? 8 * c : 16 * c;
+  p.e1 = p.turned && !IL ? half + 8 * c : 16 * c + 8;
+  return p;
+}
+// Rows are read once: keep them out of L1. (Not through the read-only path: a query
+// may be rotated in place.)
+__device__ __forceinline__ uint4 ld_once16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
 
-// One item is 16 elements of one head: 8 pairs of the rotated part, or 16
-// elements behind it. blockIdx.x = token; the CTA's threads stride the token's
-// items (query heads, key heads, value heads), and as the stride is a multiple
-// of a head's items a thread keeps its place in the head: its 8 cosines and
-// sines are loaded once for all its heads. blockIdx.y splits the heads when
-// there are few tokens.
+// The item's bytes, as loaded.
+template <typename T> struct Item {
+  static constexpr int N = 8 * sizeof(T) / 16;
+  uint4 v[2 * N];
+  __device__ __forceinline__ void load(const T* src, const Place& p) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      v[k] = ld_once16(src + p.e0 + k * Vec<T>::N);
+      v[N + k] = ld_once16(src + p.e1 + k * Vec<T>::N);
+    }
+  }
+  __device__ __forceinline__ void widen(float* f) const {
+#pragma unroll
+    for (int k = 0; k < 2 * N; ++k) widen16<T>(v[k], f + k * Vec<T>::N);
+  }
+};
+template <bool IL> __device__ __forceinline__ void turn(float* f, const float* cs, const float* sn) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (IL) rotate(f[2 * i], f[2 * i + 1], cs[i], sn[i]);
+    else rotate(f[i], f[8 + i], cs[i], sn[i]);
+  }
+}
+
+// Heads [h0, heads) in steps of one token's query | key | value heads: the loads of
+// two are in flight before the first is rotated and stored.
 template <typename TS, bool IL>
-__global__ void __launch_bounds__(256)
-rope_and_cache_kernel(const RopeArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  const int t = blockIdx.x;
-  const int64_t slot = a.slot_mapping[t];
+__device__ __forceinline__ void rope_heads(const RopeArgs& a, int t, int h0, int step, int heads) {
+  constexpr int U = 2;
+  const int c = threadIdx.x % (a.D / 16);
+  const Place pl = place_of<IL>(c, a.rot);
+  auto source = [&](int h) -> const TS* {
+    if (h < a.Hq) return static_cast<const TS*>(a.query) + (size_t)t * a.q_stride + (size_t)h * a.D;
+    if (h < a.Hq + a.Hkv)
+      return static_cast<const TS*>(a.key) + (size_t)t * a.k_stride + (size_t)(h - a.Hq) * a.D;
+    return static_cast<const TS*>(a.value) + (size_t)t * a.v_stride + (size_t)(h - a.Hq - a.Hkv) * a.D;
+  };
+  Item<TS> it[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+    if (h0 + k * step < heads) it[k].load(source(h0 + k * step), pl);
+  const int64_t slot = a.slot_mapping[t], pos = a.positions[t];
   if (slot < 0) return;                                   // padding token
-  const int64_t pos = a.positions[t];
   const bool bad_slot = slot >= (int64_t)a.num_blocks * a.bs;
   if (bad_slot || pos < 0 || pos >= a.max_pos) {
-    if (threadIdx.x == 0 && blockIdx.y == 0)
-      flag_error(a.err_flag, bad_slot ? PA_DEV_BAD_SLOT : PA_DEV_BAD_POS);
+    if (h0 == 0 && c == 0) flag_error(a.err_flag, bad_slot ? PA_DEV_BAD_SLOT : PA_DEV_BAD_POS);
     return;
   }
-  const int per_head = a.D / 16;                          // 4 or 8
-  const int c = threadIdx.x % per_head;
-  const int half = a.rot / 2;
-  const bool turned = c < half / 8;
   float cs[8], sn[8];
-  if (turned) {
+  if (pl.turned) {
     const float* row = a.cos_sin + (size_t)pos * a.rot + 8 * c;
     load8<float>(row, cs);
-    load8<float>(row + half, sn);
+    load8<float>(row + a.rot / 2, sn);
   }
-  // the item's two runs of 8 elements
-  const int e0 = turned && !IL ? 8 * c : 16 * c;
-  const int e1 = turned && !IL ? half + 8 * c : 16 * c + 8;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int step = blockDim.x / per_head;
-  for (int h = threadIdx.x / per_head + blockIdx.y * step; h < heads; h += step * gridDim.y) {
-    const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
-    const int hh = isq ? h : isv ? h - a.Hq - a.Hkv : h - a.Hq;
-    const TS* src = isq ? static_cast<const TS*>(a.query) + (size_t)t * a.q_stride
-                  : isv ? static_cast<const TS*>(a.value) + (size_t)t * a.v_stride
-                        : static_cast<const TS*>(a.key) + (size_t)t * a.k_stride;
-    src += (size_t)hh * a.D;
-    float f[16];
-    load8<TS>(src + e0, f);
-    load8<TS>(src + e1, f + 8);
-    if (turned && !isv) {
+  for (int hb = h0; hb < heads; hb += U * step) {
+    if (hb != h0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (IL) rotate(f[2 * i], f[2 * i + 1], cs[i], sn[i]);
-        else rotate(f[i], f[8 + i], cs[i], sn[i]);
-      }
+      for (int k = 0; k < U; ++k)
+        if (hb + k * step < heads) it[k].load(source(hb + k * step), pl);
     }
-    if (isq) {
-      TS* dst = static_cast<TS*>(a.query_out) + (size_t)t * a.qo_stride + (size_t)hh * a.D;
-      store8<TS>(dst + e0, f);
-      store8<TS>(dst + e1, f + 8);
-    } else {
-      const size_t row = ((size_t)slot * a.Hkv + hh) * a.D;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int h = hb + k * step;
+      if (h >= heads) break;
+      float f[16];
+      it[k].widen(f);
+      const bool isv = h >= a.Hq + a.Hkv;
+      if (pl.turned && !isv) turn<IL>(f, cs, sn);
+      if (h < a.Hq) {
+        TS* dst = static_cast<TS*>(a.query_out) + (size_t)t * a.qo_stride + (size_t)h * a.D;
+        store8<TS>(dst + pl.e0, f);
+        store8<TS>(dst + pl.e1, f + 8);
+        continue;
+      }
+      const size_t row = ((size_t)slot * a.Hkv + (isv ? h - a.Hq - a.Hkv : h - a.Hq)) * a.D;
       void* pool = isv ? a.value_cache : a.key_cache;
       if (isv ? a.v_fp8 : a.k_fp8) {
         const float scale = isv ? a.v_scale : a.k_scale;
-        store8_codes(static_cast<uint8_t*>(pool) + row + e0, f, scale);
-        store8_codes(static_cast<uint8_t*>(pool) + row + e1, f + 8, scale);
+        store8_codes(static_cast<uint8_t*>(pool) + row + pl.e0, f, scale);
+        store8_codes(static_cast<uint8_t*>(pool) + row + pl.e1, f + 8, scale);
       } else {
-        store8<TS>(static_cast<TS*>(pool) + row + e0, f);
-        store8<TS>(static_cast<TS*>(pool) + row + e1, f + 8);
+        store8<TS>(static_cast<TS*>(pool) + row + pl.e0, f);
+        store8<TS>(static_cast<TS*>(pool) + row + pl.e1, f + 8);
       }
     }
   }
+}
+
+}  // namespace
+
+// blockIdx.x = token; its items (query heads, key heads, value heads) over the
+// CTA's threads, and over blockIdx.y when there are few tokens.
+template <typename TS, bool IL>
+__global__ void __launch_bounds__(256, sizeof(TS) == 4 ? 2 : 4)
+rope_and_cache_kernel(const RopeArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int step = blockDim.x / (a.D / 16);
+  rope_heads<TS, IL>(a, blockIdx.x, threadIdx.x / (a.D / 16) + blockIdx.y * step, step * gridDim.y,
+                     a.Hq + 2 * a.Hkv);
 }
 
 // ---------------------------------------------------------------------------
@@ -153,235 +206,187 @@ rope_and_cache_kernel(const RopeArgs a) {
 // and when it does the rows that this call does not write are rounded to it.
 //
 // A run is the consecutive tokens that share a physical block (at most one
-// block's rows); its first token's CTAs own the block: one warp per (KV head,
-// K or V) reads the run's rows twice (the largest magnitude, then the codes;
-// the second read hits L1), so scales and codes need no second launch and no
-// atomics. Every CTA also rotates its share of its token's query heads.
+// block's rows). One warp takes a run's rows of one KV head of K or V: 16
+// elements per lane and row, up to four rows of every lane in registers at once, so
+// a run of 16 tokens (32 at D = 64) is read once: the largest magnitude over the warp,
+// the scale, the codes. No second launch, no atomics. (A run of 32 at D = 128 is
+// read twice, the second time from L1.)
 
 namespace {
 
-// A lane's 4 elements of a row of D: pair slots j = 2 l and 2 l + 1 of the
-// head's D / 2 pairs (l = lane within the row's D / 4 lanes).
-struct PairSlot {
-  int e0, e1;          // first of two adjacent elements of each run
-  bool turned;
-};
-template <bool IL>
-__device__ __forceinline__ PairSlot pair_slot(int l, int rot) {
-  const int j = 2 * l, half = rot / 2;
-  PairSlot s;
-  s.turned = j < half;
-  if (s.turned && !IL) { s.e0 = j; s.e1 = half + j; }
-  else { s.e0 = 2 * j; s.e1 = 2 * j + 2; }     // interleaved, or behind the rotated part
-  return s;
-}
-
-template <typename TS> __device__ __forceinline__ void load2(const TS* p, float* f) {
-  if constexpr (sizeof(TS) == 4) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    f[0] = v.x; f[1] = v.y;
-  } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    if constexpr (sizeof(TS) == 2) {
-      if (std::is_same<TS, __half>::value) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        f[0] = v.x; f[1] = v.y;
-      } else {
-        f[0] = __uint_as_float(w << 16);
-        f[1] = __uint_as_float(w & 0xffff0000u);
+template <typename TS, bool IL>
+__device__ __forceinline__ void append_run(const RopeArgs& a, int t, int n, int64_t block, uint32_t written,
+                                           int off, int lpos, int u, int lane) {
+  constexpr int U = 4;                         // rows of a lane at once
+  const bool isv = u >= a.Hkv;
+  const int h = isv ? u - a.Hkv : u;
+  const int lpt = a.D / 16, tps = 32 / lpt;    // lanes per row, rows per step
+  const int c = lane % lpt, sub = lane / lpt;
+  Place pl = place_of<IL>(c, a.rot);
+  pl.turned = pl.turned && !isv;               // (a value row's runs are merely read in that order)
+  const int64_t stride = isv ? a.v_stride : a.k_stride;
+  const TS* src = static_cast<const TS*>(isv ? a.value : a.key) + (size_t)t * stride + (size_t)h * a.D;
+  float* scales = (isv ? a.v_scales : a.k_scales) + (size_t)block * a.Hkv + h;
+  const bool fresh = written & 1u;
+  const float old = fresh ? 0.f : *scales;
+  Item<TS> it[U];
+  int o[U], p[U];
+  // rows i0 + k * tps + sub as loaded; o[k] < 0: not a row of the run
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * tps + sub;
+      o[k] = __shfl_sync(0xffffffffu, off, i & 31);
+      p[k] = __shfl_sync(0xffffffffu, lpos, i & 31);
+      if (i >= n) o[k] = -1;
+      if (o[k] >= 0) it[k].load(src + (size_t)i * stride, pl);
+    }
+  };
+  // row k rotated (the second time its cosines and sines come from L1)
+  auto rotated = [&](int k, float* f) {
+    it[k].widen(f);
+    if (pl.turned) {
+      float cs[8], sn[8];
+      const float* row = a.cos_sin + (size_t)p[k] * a.rot + 8 * c;
+      load8<float>(row, cs);
+      load8<float>(row + a.rot / 2, sn);
+      turn<IL>(f, cs, sn);
+    }
+  };
+  // the largest finite magnitude of the run's rows
+  float top = 0.f;
+  for (int i0 = 0; i0 < n; i0 += U * tps) {
+    load(i0);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (o[k] < 0) continue;
+      float f[16];
+      rotated(k, f);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float m = fabsf(f[e]);
+        top = m <= FLT_MAX ? fmaxf(top, m) : top;
       }
     }
   }
-}
-
-// This lane's 4 values of token tok's row (rotated for a key head).
-template <typename TS, bool IL>
-__device__ __forceinline__ void row4(const RopeArgs& a, const TS* src, const PairSlot& s, bool rot,
-                                     int64_t pos, int l, float* f) {
-  load2<TS>(src + s.e0, f);
-  load2<TS>(src + s.e1, f + 2);
-  if (rot && s.turned) {
-    const float* cs = a.cos_sin + (size_t)pos * a.rot + 2 * l;
-    const float2 c = *reinterpret_cast<const float2*>(cs);
-    const float2 n = *reinterpret_cast<const float2*>(cs + a.rot / 2);
-    if (IL) {
-      rotate(f[0], f[1], c.x, n.x);
-      rotate(f[2], f[3], c.y, n.y);
-    } else {
-      rotate(f[0], f[2], c.x, n.x);
-      rotate(f[1], f[3], c.y, n.y);
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+  float scale = block_scale_for(top);
+  if (!fresh) {
+    if (!block_scale_ok(old)) {
+      if (lane == 0) flag_error(a.err_flag, PA_DEV_BAD_SCALE);
+      return;
+    }
+    scale = fmaxf(scale, old);
+  }
+  const float inv = __fdiv_rn(1.f, scale);     // a power of two: exact
+  uint8_t* pool = static_cast<uint8_t*>(isv ? a.value_cache : a.key_cache) +
+                  ((size_t)block * a.bs * a.Hkv + h) * a.D;
+  const size_t pitch = (size_t)a.Hkv * a.D;
+  const bool again = n > U * tps;              // the registers hold the last rows only
+  for (int i0 = 0; i0 < n; i0 += U * tps) {
+    if (again) load(i0);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (o[k] < 0) continue;
+      float f[16];
+      rotated(k, f);
+      uint32_t w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        w[x] = e4m3x2(__fmul_rn(f[4 * x], inv), __fmul_rn(f[4 * x + 1], inv)) |
+               (e4m3x2(__fmul_rn(f[4 * x + 2], inv), __fmul_rn(f[4 * x + 3], inv)) << 16);
+      uint8_t* row = pool + o[k] * pitch;
+      *reinterpret_cast<uint2*>(row + pl.e0) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(row + pl.e1) = make_uint2(w[2], w[3]);
     }
   }
+  if (!fresh && scale > old) {
+    // the block's other rows, rounded to the larger scale
+    const float ratio = __fdiv_rn(old, scale);
+    for (int r = sub; r < a.bs; r += tps) {
+      if ((written >> r) & 1u) continue;
+      uint4* p = reinterpret_cast<uint4*>(pool + r * pitch) + c;
+      const uint4 v = *p;
+      float x[16];
+      widen16<__nv_fp8_e4m3>(v, x);
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = e4m3x2(__fmul_rn(x[4 * k], ratio), __fmul_rn(x[4 * k + 1], ratio)) |
+               (e4m3x2(__fmul_rn(x[4 * k + 2], ratio), __fmul_rn(x[4 * k + 3], ratio)) << 16);
+      *p = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (lane == 0) *scales = scale;
 }
 
 }  // namespace
 
+// The first kv_ctas CTAs take the pools: CTA (tokens [x tb, (x + 1) tb), 8 of the
+// 2 Hkv (KV head, K or V) pairs), a warp per (run that starts there, pair). The rest
+// rotate the query heads, one token each.
 template <typename TS, bool IL>
-__global__ void __launch_bounds__(256)
-rope_and_cache_blk8_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(256, 2)
+rope_and_cache_blk8_kernel(const RopeArgs a, int kv_ctas, int tb) {
   pdl_trigger();
   pdl_wait();
-  const int t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t slots = (int64_t)a.num_blocks * a.bs;
-  const int64_t slot = a.slot_mapping[t];
-  if (slot < 0) return;                                   // padding token
-  if (slot >= slots) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err_flag, PA_DEV_BAD_SLOT);
+  if ((int)blockIdx.x >= kv_ctas) {
+    const int step = 256 / (a.D / 16);
+    rope_heads<TS, IL>(a, blockIdx.x - kv_ctas, threadIdx.x / (a.D / 16), step, a.Hq);
     return;
   }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ys = (2 * a.Hkv + 7) / 8;
+  const int y = blockIdx.x % ys, t0 = blockIdx.x / ys * tb;
+  const int pairs = min(8, 2 * a.Hkv - 8 * y);
+  const int64_t slots = (int64_t)a.num_blocks * a.bs;
   const bool turn = a.cos_sin != nullptr;
-  auto pos_ok = [&](int64_t p) { return !turn || (p >= 0 && p < a.max_pos); };
-
-  // ---- this token's query heads, split over blockIdx.y
-  const int64_t pos = turn ? a.positions[t] : 0;
-  if (!pos_ok(pos)) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err_flag, PA_DEV_BAD_POS);
-  } else if (turn) {
-    const int per_head = a.D / 16;
-    const int c = threadIdx.x % per_head;
-    const int half = a.rot / 2;
-    const bool turned = c < half / 8;
-    const int e0 = turned && !IL ? 8 * c : 16 * c;
-    const int e1 = turned && !IL ? half + 8 * c : 16 * c + 8;
-    const int step = blockDim.x / per_head;
-    // blockIdx.y takes a contiguous share of the heads
-    const int share = (a.Hq + gridDim.y - 1) / gridDim.y;
-    const int h1 = min(a.Hq, ((int)blockIdx.y + 1) * share);
-    for (int h = blockIdx.y * share + threadIdx.x / per_head; h < h1; h += step) {
-      const TS* src = static_cast<const TS*>(a.query) + (size_t)t * a.q_stride + (size_t)h * a.D;
-      float f[16], cs[8], sn[8];
-      load8<TS>(src + e0, f);
-      load8<TS>(src + e1, f + 8);
-      if (turned) {
-        const float* row = a.cos_sin + (size_t)pos * a.rot + 8 * c;
-        load8<float>(row, cs);
-        load8<float>(row + half, sn);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (IL) rotate(f[2 * i], f[2 * i + 1], cs[i], sn[i]);
-          else rotate(f[i], f[8 + i], cs[i], sn[i]);
-        }
-      }
-      TS* dst = static_cast<TS*>(a.query_out) + (size_t)t * a.qo_stride + (size_t)h * a.D;
-      store8<TS>(dst + e0, f);
-      store8<TS>(dst + e1, f + 8);
-    }
+  const int sh = a.bs == 32 ? 5 : 4;
+  // slots and positions of tokens t0 + lane and t0 + 32 + lane (a run may go on past
+  // the CTA's tokens), and the slot before them
+  auto slot_of = [&](int t) -> int64_t { return t < a.T ? a.slot_mapping[t] : -1; };
+  const int64_t s0 = slot_of(t0 + lane), s1 = tb > 1 ? slot_of(t0 + 32 + lane) : -1;
+  const int64_t before = t0 > 0 ? a.slot_mapping[t0 - 1] : -1;
+  // position, -1 if it is bad
+  auto pos_of = [&](int t) -> int {
+    if (!turn || t >= a.T) return 0;
+    const int64_t p = a.positions[t];
+    return p >= 0 && p < a.max_pos ? (int)p : -1;
+  };
+  const int p0 = pos_of(t0 + lane), p1 = tb > 1 ? pos_of(t0 + 32 + lane) : 0;
+  auto in_pool = [&](int64_t s) { return s >= 0 && s < slots; };
+  const int b0 = in_pool(s0) ? (int)(s0 >> sh) : -1;      // block of the lane's token, -1: none
+  int prev = __shfl_up_sync(0xffffffffu, b0, 1);
+  if (lane == 0) prev = in_pool(before) ? (int)(before >> sh) : -1;
+  if (lane < tb && y == 0 && warp == 0) {
+    if (s0 >= slots) flag_error(a.err_flag, PA_DEV_BAD_SLOT);
+    else if (s0 >= 0 && p0 < 0) flag_error(a.err_flag, PA_DEV_BAD_POS);
   }
-
-  // ---- the block of the run that starts at this token
-  const int64_t block = slot / a.bs;
-  if (t > 0) {
-    const int64_t before = a.slot_mapping[t - 1];
-    if (before >= 0 && before < slots && before / a.bs == block) return;
-  }
-  // lane i: token t + i of the run (off < 0: not of the run, or its position is bad)
-  int off = -1;
-  bool same = false;
-  int64_t lpos = 0;
-  if (lane < a.bs && t + lane < a.T) {
-    const int64_t s = a.slot_mapping[t + lane];
-    same = s >= 0 && s < slots && s / a.bs == block;
-    if (same) {
-      off = (int)(s - block * a.bs);
-      if (turn) lpos = a.positions[t + lane];
-      if (!pos_ok(lpos)) off = -1;
+  const uint32_t heads = __ballot_sync(0xffffffffu, lane < tb && b0 >= 0 && b0 != prev);   // runs start
+  const int work = __popc(heads) * pairs;
+  int block = -1, lpos = 0, run = -1, n = 0, off = -1, first = 0;
+  uint32_t written = 0;
+  for (int x = warp; x < work; x += 8) {
+    if (x / pairs != run) {
+      run = x / pairs;
+      uint32_t rest = heads;                   // its first token: the run-th set bit
+      for (int k = 0; k < run; ++k) rest &= rest - 1;
+      first = __ffs(rest) - 1;
+      block = __shfl_sync(0xffffffffu, b0, first);
+      // lane i: token first + i of the run (off < 0: not of the run, or its position is bad)
+      const int at = first + lane;
+      const int64_t sa = __shfl_sync(0xffffffffu, s0, at & 31), sb = __shfl_sync(0xffffffffu, s1, at & 31);
+      const int pa_ = __shfl_sync(0xffffffffu, p0, at & 31), pb = __shfl_sync(0xffffffffu, p1, at & 31);
+      const int64_t s = at < 32 ? sa : sb;
+      lpos = at < 32 ? pa_ : pb;
+      const bool same = lane < a.bs && in_pool(s) && (int)(s >> sh) == block;
+      const uint32_t in = __ballot_sync(0xffffffffu, same);
+      n = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+      off = lane < n && lpos >= 0 ? (int)(s & (a.bs - 1)) : -1;
+      written = __reduce_or_sync(0xffffffffu, off >= 0 ? 1u << off : 0u);
     }
-  }
-  const uint32_t run = __ballot_sync(0xffffffffu, same);
-  const int n = run == 0xffffffffu ? 32 : __ffs(~run) - 1;      // tokens of the run
-  if (lane >= n) off = -1;
-  const uint32_t written = __reduce_or_sync(0xffffffffu, off >= 0 ? 1u << off : 0u);
-  if (!written) return;
-
-  const int lpr = a.D / 4;                     // lanes per row: 16 or 32
-  const int rpw = 32 / lpr;                    // rows a warp takes at once
-  const int l = lane % lpr, sub = lane / lpr;
-  const PairSlot ps = pair_slot<IL>(l, a.rot);
-  for (int u = blockIdx.y * 8 + warp; u < 2 * a.Hkv; u += 8 * gridDim.y) {
-    const bool isv = u >= a.Hkv;
-    const int h = isv ? u - a.Hkv : u;
-    const int64_t stride = isv ? a.v_stride : a.k_stride;
-    const TS* src = static_cast<const TS*>(isv ? a.value : a.key) + (size_t)t * stride + (size_t)h * a.D;
-    float* scales = isv ? a.v_scales : a.k_scales;
-    const size_t si = (size_t)block * a.Hkv + h;
-    const bool fresh = written & 1u;
-    const float old = fresh ? 0.f : scales[si];
-    // the largest finite magnitude of the run's rows
-    float top = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 4 * rpw) {
-      float f[4][4];
-      bool on[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * rpw + sub;
-        on[k] = __shfl_sync(0xffffffffu, off, i & 31) >= 0 && i < n;
-        const int64_t p = __shfl_sync(0xffffffffu, lpos, i & 31);
-        if (on[k]) row4<TS, IL>(a, src + (size_t)i * stride, ps, turn && !isv, p, l, f[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (!on[k]) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float m = fabsf(f[k][e]);
-          top = m <= FLT_MAX ? fmaxf(top, m) : top;
-        }
-      }
-    }
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    float scale = block_scale_for(top);
-    if (!fresh) {
-      if (!block_scale_ok(old)) {
-        if (lane == 0) flag_error(a.err_flag, PA_DEV_BAD_SCALE);
-        continue;
-      }
-      scale = fmaxf(scale, old);
-    }
-    const float inv = __fdiv_rn(1.f, scale);     // a power of two: exact
-    uint8_t* pool = static_cast<uint8_t*>(isv ? a.value_cache : a.key_cache) +
-                    ((size_t)block * a.bs * a.Hkv + h) * a.D;
-    const size_t pitch = (size_t)a.Hkv * a.D;
-    for (int i0 = 0; i0 < n; i0 += 4 * rpw) {
-      float f[4][4];
-      int o[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * rpw + sub;
-        o[k] = __shfl_sync(0xffffffffu, off, i & 31);
-        if (i >= n) o[k] = -1;
-        const int64_t p = __shfl_sync(0xffffffffu, lpos, i & 31);
-        if (o[k] >= 0) row4<TS, IL>(a, src + (size_t)i * stride, ps, turn && !isv, p, l, f[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (o[k] < 0) continue;
-        uint8_t* row = pool + o[k] * pitch;
-        const uint32_t c0 = e4m3x2(__fmul_rn(f[k][0], inv), __fmul_rn(f[k][1], inv));
-        const uint32_t c1 = e4m3x2(__fmul_rn(f[k][2], inv), __fmul_rn(f[k][3], inv));
-        *reinterpret_cast<uint16_t*>(row + ps.e0) = (uint16_t)c0;
-        *reinterpret_cast<uint16_t*>(row + ps.e1) = (uint16_t)c1;
-      }
-    }
-    if (!fresh && scale > old) {
-      // the block's other rows, rounded to the larger scale
-      const float ratio = __fdiv_rn(old, scale);
-      for (int r = sub; r < a.bs; r += rpw) {
-        if ((written >> r) & 1u) continue;
-        uint32_t* p = reinterpret_cast<uint32_t*>(pool + r * pitch) + l;
-        const uint32_t w = *p;
-        uint32_t out = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-              static_cast<__nv_fp8x2_storage_t>((w >> (16 * k)) & 0xffffu), __NV_E4M3);
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-          out |= e4m3x2(__fmul_rn(v.x, ratio), __fmul_rn(v.y, ratio)) << (16 * k);
-        }
-        *p = out;
-      }
-    }
-    if (lane == 0) scales[si] = scale;
+    if (written)
+      append_run<TS, IL>(a, t0 + first, n, block, written, off, lpos, 8 * y + x % pairs, lane);
   }
 }
 
@@ -420,24 +425,30 @@ namespace {
 
 template <typename TS>
 int launch_rope_t(const RopeArgs& a, bool blk8, cudaStream_t stream) {
-  // blk8: one warp per (KV head, K or V). Else: split the heads only while the
-  // tokens leave SMs empty.
-  int y;
-  if (blk8) {
-    y = (2 * a.Hkv + 7) / 8;
-  } else {
-    const int items = (a.Hq + 2 * a.Hkv) * (a.D / 16);
-    y = (items + 255) / 256;
-    while (y > 1 && (long long)a.T * y > 8 * kSMs) --y;
-  }
-  const dim3 grid((unsigned)a.T, (unsigned)y), block(256);
+  const dim3 block(256);
   cudaError_t e;
-  if (blk8)
-    e = a.interleaved ? launch_k(rope_and_cache_blk8_kernel<TS, true>, grid, block, 0, stream, a)
-                      : launch_k(rope_and_cache_blk8_kernel<TS, false>, grid, block, 0, stream, a);
-  else
+  if (blk8) {
+    // Tokens per CTA: one while that leaves a warp per (token, head, K or V) in two
+    // waves of the GPU (a decode step: every token is a run of its own); else 16, of
+    // which a chunk's runs leave about one per CTA.
+    const int ys = (2 * a.Hkv + 7) / 8;
+    const int tb = (long long)a.T * ys <= 4 * kSMs ? 1 : 16;
+    const long long kv = ((long long)a.T + tb - 1) / tb * ys;
+    const long long grid = kv + (a.Hq > 0 ? a.T : 0);
+    if (grid > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    e = a.interleaved ? launch_k(rope_and_cache_blk8_kernel<TS, true>, dim3((unsigned)grid), block, 0, stream,
+                                 a, (int)kv, tb)
+                      : launch_k(rope_and_cache_blk8_kernel<TS, false>, dim3((unsigned)grid), block, 0, stream,
+                                 a, (int)kv, tb);
+  } else {
+    // split a token's heads only while the tokens leave SMs empty
+    const int items = (a.Hq + 2 * a.Hkv) * (a.D / 16);
+    int y = (items + 255) / 256;
+    while (y > 1 && (long long)a.T * y > 8 * kSMs) --y;
+    const dim3 grid((unsigned)a.T, (unsigned)y);
     e = a.interleaved ? launch_k(rope_and_cache_kernel<TS, true>, grid, block, 0, stream, a)
                       : launch_k(rope_and_cache_kernel<TS, false>, grid, block, 0, stream, a);
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
