@@ -35,14 +35,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 8 fp32 values rounded to T and stored to 8 consecutive elements.
+// 8 fp32 values rounded to T and stored to 8 consecutive elements, marked to leave
+// L2 first: a chunk's rows (84 MB written at 8 x 512 tokens of 64 + 8 heads) would
+// push out each other's lines half-written otherwise (33.7 -> 29.9 us there).
 template <typename T> __device__ __forceinline__ void store8(T* p, const float* f) {
   if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
   } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1], p), pack2(f[2], f[3], p),
-                                              pack2(f[4], f[5], p), pack2(f[6], f[7], p));
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack2(f[0], f[1], p), pack2(f[2], f[3], p),
+                                                   pack2(f[4], f[5], p), pack2(f[6], f[7], p)));
   }
 }
 
@@ -83,9 +85,9 @@ template <bool IL> __device__ __forceinline__ Place place_of(int c, int rot) {
   p.e1 = p.turned && !IL ? half + 8 * c : 16 * c + 8;
   return p;
 }
-// Rows are read once: keep them out of L1. (Not through the read-only path: a query
-// may be rotated in place.)
-__device__ __forceinline__ uint4 ld_once16(const void* p) {
+// (Past L1: read once. Not through the read-only path: a query may be rotated in
+// place.)
+__device__ __forceinline__ uint4 ld_row16(const void* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
@@ -99,8 +101,8 @@ template <typename T> struct Item {
   __device__ __forceinline__ void load(const T* src, const Place& p) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      v[k] = ld_once16(src + p.e0 + k * Vec<T>::N);
-      v[N + k] = ld_once16(src + p.e1 + k * Vec<T>::N);
+      v[k] = ld_row16(src + p.e0 + k * Vec<T>::N);
+      v[N + k] = ld_row16(src + p.e1 + k * Vec<T>::N);
     }
   }
   __device__ __forceinline__ void widen(float* f) const {
@@ -116,12 +118,10 @@ template <bool IL> __device__ __forceinline__ void turn(float* f, const float* c
   }
 }
 
-// Heads [h0, heads) in steps of one token's query | key | value heads: the loads of
-// two are in flight before the first is rotated and stored.
-template <typename TS, bool IL>
-__device__ __forceinline__ void rope_heads(const RopeArgs& a, int t, int h0, int step, int heads) {
-  constexpr int U = 2;
-  const int c = threadIdx.x % (a.D / 16);
+// Heads [h0, heads) in steps of one token's query | key | value heads, place c in
+// each: the loads of U heads are in flight before the first is rotated and stored.
+template <typename TS, bool IL, int U>
+__device__ __forceinline__ void rope_heads(const RopeArgs& a, int t, int c, int h0, int step, int heads) {
   const Place pl = place_of<IL>(c, a.rot);
   auto source = [&](int h) -> const TS* {
     if (h < a.Hq) return static_cast<const TS*>(a.query) + (size_t)t * a.q_stride + (size_t)h * a.D;
@@ -183,15 +183,19 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, int t, int h0, int
 }  // namespace
 
 // blockIdx.x = token; its items (query heads, key heads, value heads) over the
-// CTA's threads, and over blockIdx.y when there are few tokens.
+// CTA's 128 threads, and over blockIdx.y when there are few tokens. Five heads of a
+// thread in flight: one round for 64 + 8 + 8 heads of 128. (At 8 x 512 such bf16
+// tokens, 170 MB: 256 threads and two heads 34.1 us, 128 and five 29.9 us, 5.7 TB/s,
+// 87% of a plain copy.)
 template <typename TS, bool IL>
-__global__ void __launch_bounds__(256, sizeof(TS) == 4 ? 2 : 4)
+__global__ void __launch_bounds__(128, 4)
 rope_and_cache_kernel(const RopeArgs a) {
   pdl_trigger();
   pdl_wait();
-  const int step = blockDim.x / (a.D / 16);
-  rope_heads<TS, IL>(a, blockIdx.x, threadIdx.x / (a.D / 16) + blockIdx.y * step, step * gridDim.y,
-                     a.Hq + 2 * a.Hkv);
+  const int per_head = a.D / 16, step = 128 / per_head;
+  rope_heads<TS, IL, sizeof(TS) == 4 ? 2 : 5>(a, blockIdx.x, threadIdx.x % per_head,
+                                              threadIdx.x / per_head + blockIdx.y * step, step * gridDim.y,
+                                              a.Hq + 2 * a.Hkv);
 }
 
 // ---------------------------------------------------------------------------
@@ -210,7 +214,7 @@ rope_and_cache_kernel(const RopeArgs a) {
 // elements per lane and row, up to four rows of every lane in registers at once, so
 // a run of 16 tokens (32 at D = 64) is read once: the largest magnitude over the warp,
 // the scale, the codes. No second launch, no atomics. (A run of 32 at D = 128 is
-// read twice, the second time from L1.)
+// read twice, the second time from L1 or L2.)
 
 namespace {
 
@@ -242,7 +246,8 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, int t, int n, int6
       if (o[k] >= 0) it[k].load(src + (size_t)i * stride, pl);
     }
   };
-  // row k rotated (the second time its cosines and sines come from L1)
+  // row k rotated (the second time its cosines and sines come from L1; keeping the
+  // rotated rows instead of the loaded ones would take twice the registers)
   auto rotated = [&](int k, float* f) {
     it[k].widen(f);
     if (pl.turned) {
@@ -253,7 +258,8 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, int t, int n, int6
       turn<IL>(f, cs, sn);
     }
   };
-  // the largest finite magnitude of the run's rows
+  // the largest finite magnitude of the run's rows (the maximum drops NaN; infinities
+  // are left out in a second look, if there are any)
   float top = 0.f;
   for (int i0 = 0; i0 < n; i0 += U * tps) {
     load(i0);
@@ -262,11 +268,15 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, int t, int n, int6
       if (o[k] < 0) continue;
       float f[16];
       rotated(k, f);
+      float most = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float m = fabsf(f[e]);
-        top = m <= FLT_MAX ? fmaxf(top, m) : top;
+      for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(f[e]));
+      if (most > FLT_MAX) {
+        most = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) most = fabsf(f[e]) <= FLT_MAX ? fmaxf(most, fabsf(f[e])) : most;
       }
+      top = fmaxf(top, most);
     }
   }
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
@@ -322,22 +332,26 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, int t, int n, int6
 
 }  // namespace
 
-// The first kv_ctas CTAs take the pools: CTA (tokens [x tb, (x + 1) tb), 8 of the
-// 2 Hkv (KV head, K or V) pairs), a warp per (run that starts there, pair). The rest
-// rotate the query heads, one token each.
+// kv of the grid's CTAs, spread evenly over it, take the pools (latency-bound, beside
+// the query's copies, which are not): CTA (tokens [x tb, (x + 1) tb), 8 of the 2 Hkv
+// (KV head, K or V) pairs), a warp per (run that starts there, pair). The others
+// rotate the query heads of two tokens each.
 template <typename TS, bool IL>
-__global__ void __launch_bounds__(256, 2)
-rope_and_cache_blk8_kernel(const RopeArgs a, int kv_ctas, int tb) {
+__global__ void __launch_bounds__(256, sizeof(TS) == 4 ? 2 : 3)
+rope_and_cache_blk8_kernel(const RopeArgs a, int kv, int tb) {
   pdl_trigger();
   pdl_wait();
-  if ((int)blockIdx.x >= kv_ctas) {
-    const int step = 256 / (a.D / 16);
-    rope_heads<TS, IL>(a, blockIdx.x - kv_ctas, threadIdx.x / (a.D / 16), step, a.Hq);
+  const long long grid = gridDim.x, id = blockIdx.x;
+  const int kv_id = (int)(id * kv / grid);               // kv CTAs before this one
+  if ((int)((id + 1) * kv / grid) == kv_id) {
+    const int t = 2 * (int)(id - kv_id) + (threadIdx.x >> 7), per_head = a.D / 16;
+    if (t < a.T)
+      rope_heads<TS, IL, 2>(a, t, threadIdx.x % per_head, (threadIdx.x & 127) / per_head, 128 / per_head, a.Hq);
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ys = (2 * a.Hkv + 7) / 8;
-  const int y = blockIdx.x % ys, t0 = blockIdx.x / ys * tb;
+  const int y = kv_id % ys, t0 = kv_id / ys * tb;
   const int pairs = min(8, 2 * a.Hkv - 8 * y);
   const int64_t slots = (int64_t)a.num_blocks * a.bs;
   const bool turn = a.cos_sin != nullptr;
@@ -425,7 +439,6 @@ namespace {
 
 template <typename TS>
 int launch_rope_t(const RopeArgs& a, bool blk8, cudaStream_t stream) {
-  const dim3 block(256);
   cudaError_t e;
   if (blk8) {
     // Tokens per CTA: one while that leaves a warp per (token, head, K or V) in two
@@ -434,20 +447,20 @@ int launch_rope_t(const RopeArgs& a, bool blk8, cudaStream_t stream) {
     const int ys = (2 * a.Hkv + 7) / 8;
     const int tb = (long long)a.T * ys <= 4 * kSMs ? 1 : 16;
     const long long kv = ((long long)a.T + tb - 1) / tb * ys;
-    const long long grid = kv + (a.Hq > 0 ? a.T : 0);
+    const long long grid = kv + (a.Hq > 0 ? (a.T + 1) / 2 : 0);
     if (grid > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-    e = a.interleaved ? launch_k(rope_and_cache_blk8_kernel<TS, true>, dim3((unsigned)grid), block, 0, stream,
-                                 a, (int)kv, tb)
-                      : launch_k(rope_and_cache_blk8_kernel<TS, false>, dim3((unsigned)grid), block, 0, stream,
-                                 a, (int)kv, tb);
+    e = a.interleaved ? launch_k(rope_and_cache_blk8_kernel<TS, true>, dim3((unsigned)grid), dim3(256), 0,
+                                 stream, a, (int)kv, tb)
+                      : launch_k(rope_and_cache_blk8_kernel<TS, false>, dim3((unsigned)grid), dim3(256), 0,
+                                 stream, a, (int)kv, tb);
   } else {
     // split a token's heads only while the tokens leave SMs empty
     const int items = (a.Hq + 2 * a.Hkv) * (a.D / 16);
-    int y = (items + 255) / 256;
+    int y = (items + 127) / 128;
     while (y > 1 && (long long)a.T * y > 8 * kSMs) --y;
     const dim3 grid((unsigned)a.T, (unsigned)y);
-    e = a.interleaved ? launch_k(rope_and_cache_kernel<TS, true>, grid, block, 0, stream, a)
-                      : launch_k(rope_and_cache_kernel<TS, false>, grid, block, 0, stream, a);
+    e = a.interleaved ? launch_k(rope_and_cache_kernel<TS, true>, grid, dim3(128), 0, stream, a)
+                      : launch_k(rope_and_cache_kernel<TS, false>, grid, dim3(128), 0, stream, a);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
