@@ -1,26 +1,863 @@
 // prefill_window.cu -- paged prefill over a sliding window and a few first tokens,
-// and over the block-scaled 8-bit cache: the prefill kernel's run-time-windowed
-// instances (group size at run time too).
+// and over the block-scaled 8-bit cache, on the 5th-generation tensor cores.
 //
-// New token at position p attends keys t <= p with t > p - window or t < sinks. A
-// unit's 128 / G tokens walk the 128-key tiles that hold a key some of them
-// attends: the first tokens' tiles, then those from its first token's window on.
-// Blocks of those tiles that no row attends are not loaded (nor is their table
-// entry read), a row's mask is one bit per key of a 32-key chunk.
-#include "prefill_fa.cuh"
+// The new token at position p of its sequence attends the keys
+//   t <= p  with  t > p - window  or  t < sinks      (window 0: every t <= p).
+// Work unit = (sequence, chunk of 128 / G new tokens, KV head): its 128 query rows
+// (token, head of the group) are the MMA's M. Its tiles are the 128-key tiles with
+// a key some row attends: the first n0 (sinks) and those from w0 on (the window of
+// its first token). Blocks that no row attends are not loaded, nor are their table
+// entries read. Per tile:
+//   S[128 x 128] = Q . K^T (tensor memory, two buffers by tile)
+//   O[128 x 128] += P . V  (two buffers by unit; P is read from tensor memory)
+// Two groups of four softmax warps share the rows: thread (half hf, row r) has keys
+// [64 hf, 64 hf + 64) of every tile in registers (64 scores: one read of S), swaps the
+// tile's row maximum with the other half's thread through shared memory, writes its
+// weights over S, and owns O's columns [64 hf, 64 hf + 64). The reference maximum
+// moves when a tile passes it by 2^8 (then the row's O is rescaled in tensor memory);
+// it is floored at -FLT_MAX, so masked scores (-inf) need no guard. A tile that
+// every row sees whole skips the masks.
+//
+// 16-bit pools: the products take the query's type, and the weights two 16-bit parts
+// (hi + lo, ~16 bits).
+// 8-bit pools: four converter warps widen each tile's codes to f16 (exactly, in place:
+// TMA leaves a row's 128 codes in the line of its second half) ahead of the tensor
+// cores, so neither the softmax nor the MMAs wait for it; a bf16 query is rescaled by
+// a power of two per row and becomes f16 too, exactly (an element 2^-39 of its row's
+// largest is rounded), once per unit. Weights over 8-bit V enter as one f16 part: their
+// 2^-12 is far below the 2^-4 of the codes they multiply, and under half a step of
+// either 16-bit output. (Widened by the softmax warps between two tiles instead, as
+// in prefill_tc.cu, an 8192-token prompt took 2.1 ms.)
+//
+// Block-scaled pools: K's power of two multiplies its keys' scores; V's enters as its
+// log2, s' = s + log2(vs), so the running maximum is that of the whole contribution,
+// the weights 2^(s' - m) are normalised to the largest one, and the row sum counts each
+// over its V scale. The producer leaves a tile's scales and the mask of its missing
+// blocks in a ring of shared-memory slots.
+//
+// CTA, persistent over rounds of units in alternating directions: warps 0-7 softmax,
+// then (8-bit pools) 8-11 converters, then the TMA producer and the MMA issuer. Every
+// pipeline wait is bounded (1 s); one that gives up sets PA_DEV_TIMEOUT, raises the
+// CTA's abort flag, and every role drains its asynchronous work, frees tensor memory
+// and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math_constants.h>
+
+#include <cfloat>
+
+#include "pa_internal.h"
+#include "tc_ptx.cuh"
 
 namespace pa {
 
 namespace {
 
+using namespace tc;
+
+constexpr int kD = 128;
+constexpr int kM = 128;                         // query rows per unit
+constexpr int kTile = 128;                      // keys per tile
+constexpr int kHalf = 128 * 128;                // one 64-wide d-half of a 128-row operand
+constexpr int kOp = 2 * kHalf;                  // one 128 x 128 16-bit operand: 32 KB
+constexpr int kNST = 5;                         // K / V ring stages (odd: a stage serves K and V in turn)
+constexpr float kMove = 8.f;                    // weights stay under 2^8, inside f16
+constexpr int kTmemCols = 512;                  // S/P x2 (by tile), O x2 (by unit)
+constexpr int kSlots = 4;                       // tiles of scales and masks (see the producer)
+
+constexpr int OFF_Q = 0;                        // [2 units][32 KB]
+constexpr int OFF_KV = 2 * kOp;                 // [kNST][32 KB]
+constexpr int OFF_BAR = OFF_KV + kNST * kOp;
+enum { B_FULL = 0, B_EMPTY = kNST, B_CONV = 2 * kNST, B_QFULL = 3 * kNST, B_QEMPTY = B_QFULL + 2,
+       B_QCONV = B_QEMPTY + 2, B_SFULL = B_QCONV + 2, B_PREADY = B_SFULL + 2, B_OSTEP = B_PREADY + 2,
+       B_ODONE = B_OSTEP + 2, B_DONE = B_ODONE + 2, B_COUNT = B_DONE + 1 };
+constexpr int OFF_MISC = OFF_BAR + 8 * B_COUNT;
+constexpr int OFF_SLOT = (OFF_MISC + 8 + 15) / 16 * 16;
+struct Slot {                                   // of a tile: what the producer knows of its blocks
+  float ks[8], lvs[8];                          // K scale, log2 of the V scale
+  uint32_t missing;                             // blocks that were not loaded
+  uint32_t pad[3];
+};
+constexpr int OFF_XCH = OFF_SLOT + kSlots * (int)sizeof(Slot);   // [2 halves][128 rows] maxima, then sums
+constexpr int OFF_ROWE = OFF_XCH + 2 * 128 * 4;                  // [2 units][128] exponents of rescaled rows
+constexpr int kSmem = OFF_ROWE + 2 * 128 + 1024;                 // + alignment slack
+static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+
+struct Args {
+  void* out;
+  int out_dtype;
+  const int32_t* block_tables;
+  int max_blocks;
+  const int32_t* context_lens;
+  const int32_t* query_start;
+  int B, Hq, Hkv, num_blocks, chunks;
+  float scale_log2;
+  float v_scale;        // value of one V unit (FP8 V pool; 1 otherwise)
+  int max_context_len;
+  uint32_t* err_flag;
+  int window, sinks;
+  const float* k_scales;
+  const float* v_scales;
+};
+
+struct Unit {
+  int b, c, h;
+  int qrow0;            // first query row (token) of the chunk in [T]
+  int ntok;             // new tokens of the chunk (0: nothing to do)
+  int pos0;             // position of the chunk's first token
+  int t1;               // some row attends keys t < t1 with t >= lo or t < sk;
+  int lo, sk;           // their tiles are the first n0 and those from w0 on
+  int n0, w0, ntiles;
+  bool bad;             // the sequence's lengths are inconsistent
+  __device__ __forceinline__ int tile0(int k) const { return (k < n0 ? k : k - n0 + w0) * kTile; }
+  // a row attends some of the n keys from t on
+  __device__ __forceinline__ bool needs(int t, int n) const { return t < t1 && (t + n > lo || t < sk); }
+};
+
+__device__ __forceinline__ Unit unit_of(const Args& a, int G, int bs, long long u) {
+  const int tpu = kM / G;
+  Unit x;
+  x.h = (int)(u % a.Hkv);
+  const long long t = u / a.Hkv;
+  x.b = (int)(t % a.B);
+  x.c = a.chunks - 1 - (int)(t / a.B);          // late chunks first: they attend the most keys
+  const int qs = __ldg(a.query_start + x.b), qe = __ldg(a.query_start + x.b + 1);
+  const int n = qe - qs, ctx = __ldg(a.context_lens + x.b);
+  x.bad = n < 0 || ctx < n || ctx > (long long)a.max_blocks * bs || ctx > a.max_context_len;
+  const long long done = (long long)x.c * tpu;  // the sequence's new tokens before the chunk
+  x.ntok = x.bad ? 0 : (int)max(0ll, min((long long)tpu, n - done));
+  x.qrow0 = (int)(qs + done);
+  x.pos0 = (int)(ctx - n + done);
+  x.t1 = x.ntok > 0 ? x.pos0 + x.ntok : 0;
+  x.lo = a.window > 0 && x.ntok > 0 ? max(0, x.pos0 - a.window + 1) : 0;
+  x.sk = min(a.sinks, x.lo);
+  x.w0 = x.lo / kTile;
+  x.n0 = min((x.sk + kTile - 1) / kTile, x.w0);
+  x.ntiles = x.n0 + (x.t1 + kTile - 1) / kTile - x.w0;
+  return x;
+}
+
+// The k-th unit of CTA cta: rounds of grid units in alternating directions.
+__device__ __forceinline__ long long unit_index(long long k, int cta, int grid) {
+  return k * grid + ((k & 1) ? grid - 1 - cta : cta);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 weights as packed 16-bit values, and (LO) what their rounding lost.
+template <bool BF, bool LO>
+__device__ __forceinline__ void pack2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  if (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    if (LO) {
+      const float2 f = __bfloat1622float2(h);
+      const __nv_bfloat162 l = __floats2bfloat162_rn(p0 - f.x, p1 - f.y);
+      lo = *reinterpret_cast<const uint32_t*>(&l);
+    }
+  } else {
+    const __half2 h = __floats2half2_rn(p0, p1);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    if (LO) {
+      const float2 f = __half22float2(h);
+      const __half2 l = __floats2half2_rn(p0 - f.x, p1 - f.y);
+      lo = *reinterpret_cast<const uint32_t*>(&l);
+    }
+  }
+}
+
+// 16 packed columns of this thread's TMEM lane, without waiting.
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Widen row `row` of a stage's codes (its line of the second half) to f16, in place;
+// zero: zeros instead.
+__device__ __forceinline__ void widen_row(uint8_t* stage, int row, bool zero) {
+  const int sw = row & 7;
+  const uint8_t* src = stage + kHalf + row * 128;
+  uint4 c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    c[j] = zero ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src + ((j ^ sw) << 4));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // codes 16 j .. 16 j + 15: d-half j / 4, 16-byte chunks 2 (j % 4) and the next
+    const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+          : "=r"(o[2 * k]), "=r"(o[2 * k + 1]) : "r"(w[k]));
+    uint8_t* dst = stage + (j >> 2) * kHalf + row * 128;
+    const int c0 = 2 * (j & 3);
+    *reinterpret_cast<uint4*>(dst + ((c0 ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ sw) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// Row `row` of a bf16 query operand as f16, in place, times the power of two that
+// puts its largest element into [2^14, 2^15); returns that power's exponent.
+__device__ __forceinline__ int rescale_row(uint8_t* op, int row) {
+  // (the second look at the row is cheaper than 64 registers)
+  auto chunk = [&](int j) {
+    return reinterpret_cast<uint4*>(op + (j >> 3) * kHalf + row * 128 + (((j & 7) ^ (row & 7)) << 4));
+  };
+  float top = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < 16; ++j) {
+    float f[8];
+    widen16<__nv_bfloat16>(*chunk(j), f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
+  }
+  int e = 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+  if (e < -113 || e > 114) e = 0;               // infinite, or too small to matter
+  const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll 4
+  for (int j = 0; j < 16; ++j) {
+    float f[8];
+    widen16<__nv_bfloat16>(*chunk(j), f);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 h = __floats2half2_rn(f[2 * k] * up, f[2 * k + 1] * up);
+      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *chunk(j) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return e;
+}
+
+// Wait for this thread's tensor-memory loads, the 64 registers of which are not to be
+// used before.
+__device__ __forceinline__ void tmem_wait_ld64(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+               :: "memory");
+#pragma unroll
+  for (int i = 28; i < 64; i += 4)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])::"memory");
+}
+
+// Warps of the CTA and their registers. Without converters: 12 warps (two idle), 168
+// registers each. With them: 16 warps launched with 128, moved between warpgroups:
+// 256 * 160 + 128 * 104 + 128 * 88 = 65,536 = 512 * 128.
+template <bool CONV> struct Roles {
+  static constexpr int kConv = 8, kProd = CONV ? 12 : 8, kMma = kProd + 1, kThreads = CONV ? 512 : 384;
+};
+
+}  // namespace
+
+// FMT: the query's type (0 f16, 1 bf16). K8 / V8: that pool holds codes. BSC (K8 and
+// V8): with scales per block and KV head.
+template <int FMT, int BS, bool K8, bool V8, bool BSC>
+__global__ void __launch_bounds__((Roles<K8 || V8>::kThreads), 1)
+prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+  constexpr bool CONV = K8 || V8;               // converter warps
+  constexpr bool QC = K8 && FMT == 1;           // the query becomes f16
+  constexpr int FS = K8 ? 0 : FMT, FO = V8 ? 0 : FMT;     // operand types of the two products
+  constexpr bool LO = !V8;                      // weights in two parts
+  using R = Roles<CONV>;
+  constexpr int NB_T = kTile / BS;              // physical blocks per tile
+  constexpr uint32_t kBlkBits = (uint32_t)((1ull << BS) - 1ull);   // one block's keys in a chunk mask
+  constexpr uint32_t IDESC_S = make_idesc(FS, 0, 0, kTile, kM);
+  constexpr uint32_t IDESC_O = make_idesc(FO, 0, 1, kD, kM);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_addr(smem);
+  auto bar = [&](int i) { return sbase + OFF_BAR + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_MISC + 4);
+  Slot* slots = reinterpret_cast<Slot*>(smem + OFF_SLOT);
+  int8_t* rowe = reinterpret_cast<int8_t*>(smem + OFF_ROWE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.Hq / a.Hkv;
+  const long long U = (long long)a.B * a.chunks * a.Hkv;
+  pdl_trigger();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kNST; ++s) {
+      mbar_init(bar(B_FULL + s), 1);
+      mbar_init(bar(B_EMPTY + s), 1);
+      mbar_init(bar(B_CONV + s), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_QFULL + i), 1);
+      mbar_init(bar(B_QEMPTY + i), QC ? 257 : 1);      // (the softmax threads read the rows' exponents)
+      mbar_init(bar(B_QCONV + i), 128);
+      mbar_init(bar(B_SFULL + i), 1);
+      mbar_init(bar(B_PREADY + i), 256);
+      mbar_init(bar(B_OSTEP + i), 1);
+      mbar_init(bar(B_ODONE + i), 256);
+    }
+    mbar_init(bar(B_DONE), 1);
+    *abort_flag = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == R::kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem_s = tmem;                  // S/P: [0, 128), [128, 256)
+  const uint32_t tmem_o = tmem + 2 * kTile;      // O: [256, 384), [384, 512)
+  auto give_up = [&]() {
+    *abort_flag = 1u;
+    flag_error(a.err_flag, PA_DEV_TIMEOUT);
+  };
+  // a stage holding K (kv = 0) or V (kv = 1) is ready for the tensor cores when TMA
+  // filled it (16-bit pool) or when the converters widened it. FULL completes a phase
+  // on every use of the stage, and so does CONV when both pools hold codes; with one
+  // such pool only its uses are widened, every other one (kNST is odd, so a stage's
+  // uses alternate K and V).
+  auto ready_bar = [&](int kv, int s) { return bar(((kv ? V8 : K8) ? B_CONV : B_FULL) + s); };
+  auto ready_parity = [&](int kv, int seq) -> uint32_t {
+    const int u = seq / kNST;
+    return (uint32_t)(((kv ? V8 : K8) && K8 != V8) ? u >> 1 : u) & 1u;
+  };
+
+  if (warp >= R::kProd) {
+    if constexpr (CONV) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == R::kProd) {
+      // ---------------------------------------------------------- producer
+      // The lanes share a tile's copies: lane q < NB_T has its q-th block, reads its id
+      // two tiles ahead and its scales one ahead. It writes a tile's slot once it has the
+      // tile's K stage, that is after the product P . V of the tile three before it: every
+      // softmax and converter thread is past that tile's slot, so four slots are enough.
+      int tc_ = 0, issued = 0, ui = 0;
+      int q_last[2] = {-1, -1};
+      bool stop = false;
+      for (long long kk = 0; !stop; ++kk) {
+        const long long u = unit_index(kk, blockIdx.x, gridDim.x);
+        if (u >= U) break;
+        const Unit x = unit_of(a, G, BS, u);
+        if (lane == 0 && x.bad && x.c == 0 && x.h == 0) flag_error(a.err_flag, PA_DEV_BAD_CTX);
+        if (x.ntok <= 0) continue;
+        const int qi = ui & 1;
+        bool ok = true;
+        if (lane == 0) {
+          ok = mbar_wait(bar(B_QEMPTY + qi), ((ui >> 1) & 1) ^ 1, abort_flag);
+          if (ok) {
+            mbar_expect_tx(bar(B_QFULL + qi), (uint32_t)kOp);
+            for (int hh = 0; hh < 2; ++hh)
+              tma_load_4d(sbase + OFF_Q + qi * kOp + hh * kHalf, &tmQ, 0, hh, x.h * G, x.qrow0,
+                          bar(B_QFULL + qi));
+            q_last[qi] = ui;
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) { stop = true; break; }
+        const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
+        // this lane's block of tile k is one some row attends; its id (-1: none)
+        auto wants = [&](int k) { return lane < NB_T && x.needs(x.tile0(k) + lane * BS, BS); };
+        auto fetch = [&](int k) -> int {
+          return k < x.ntiles && wants(k) ? __ldg(table + x.tile0(k) / BS + lane) : -1;
+        };
+        float ks_n = 1.f, vs_n = 1.f;
+        auto fetch_scales = [&](int id) {
+          if (BSC && id >= 0 && id < a.num_blocks) {
+            ks_n = __ldg(a.k_scales + (size_t)id * a.Hkv + x.h);
+            vs_n = __ldg(a.v_scales + (size_t)id * a.Hkv + x.h);
+          }
+        };
+        int id1 = fetch(0), id2 = fetch(1);
+        fetch_scales(id1);
+        for (int k = 0; k < x.ntiles && !stop; ++k, ++tc_) {
+          int phys = id1;
+          const float ks = ks_n, vs = vs_n;
+          id1 = id2;
+          id2 = fetch(k + 2);
+          fetch_scales(id1);
+          const bool want = wants(k);
+          if (want && (phys < 0 || phys >= a.num_blocks)) {
+            flag_error(a.err_flag, PA_DEV_BAD_BLOCK_ID);
+            phys = -1;
+          }
+          if (BSC && want && phys >= 0 && !(block_scale_ok(ks) && block_scale_ok(vs))) {
+            flag_error(a.err_flag, PA_DEV_BAD_SCALE);
+            phys = -1;
+          }
+          const uint32_t here = __ballot_sync(0xffffffffu, phys >= 0);
+          // per 128-byte line of rows of the blocks that are loaded
+          const uint32_t bytes = (uint32_t)__popc(here) * (BS * 128u);
+          for (int kv = 0; kv < 2; ++kv) {
+            const int seq = 2 * tc_ + kv, s = seq % kNST;
+            const bool codes = kv ? V8 : K8;
+            bool room = true;
+            if (lane == 0) room = mbar_wait(bar(B_EMPTY + s), ((seq / kNST) & 1) ^ 1, abort_flag);
+            if (!__shfl_sync(0xffffffffu, room, 0)) { stop = true; break; }
+            if (kv == 0) {
+              Slot& slot = slots[tc_ % kSlots];
+              if (BSC && lane < NB_T) {
+                slot.ks[lane] = phys >= 0 ? ks : 1.f;
+                slot.lvs[lane] = phys >= 0 ? (float)block_scale_log2(vs) : 0.f;
+              }
+              if (lane == 0) slot.missing = ~here;
+              __syncwarp();
+            }
+            if (lane == 0) mbar_expect_tx(bar(B_FULL + s), codes ? bytes : 2u * bytes);
+            __syncwarp();
+            const uint32_t dst = sbase + OFF_KV + s * kOp;
+            if (phys >= 0) {
+              if (codes) {
+                tma_load_4d(dst + kHalf + lane * (BS * 128), kv ? &tmV : &tmK, 0, 0, x.h, phys,
+                            bar(B_FULL + s));
+              } else {
+                for (int hh = 0; hh < 2; ++hh)
+                  tma_load_5d(dst + hh * kHalf + lane * (BS * 128), kv ? &tmV : &tmK, 0, 0, x.h, hh, phys,
+                              bar(B_FULL + s));
+              }
+            }
+            ++issued;
+          }
+        }
+        ++ui;
+      }
+      if (lane == 0) {
+        if (stop) give_up();
+        // never leave with copies in flight: the last loads of every stage and query buffer
+        for (int seq = max(0, issued - kNST); seq < issued; ++seq) {
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try(bar(B_FULL + seq % kNST), (seq / kNST) & 1) && globaltimer() - t0 < kWaitNs) {}
+        }
+        for (int qb = 0; qb < 2; ++qb) {
+          if (q_last[qb] < 0) continue;
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try(bar(B_QFULL + qb), (q_last[qb] >> 1) & 1) && globaltimer() - t0 < kWaitNs) {}
+        }
+      }
+    } else if (warp == R::kMma && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      int tc_ = 0, ui = 0;
+      bool ok = true;
+      // output product of tile tt (the unit's first if first) into O buffer ob
+      auto issue_pv = [&](int tt, bool first, int ob) -> bool {
+        const int pb = tt & 1;
+        if (!mbar_wait(bar(B_PREADY + pb), (tt >> 1) & 1, abort_flag)) return false;
+        // the O buffer was last used by unit ui - 2: wait for its epilogue
+        if (first && ui >= 2 && !mbar_wait(bar(B_ODONE + ob), ((ui - 2) >> 1) & 1, abort_flag)) return false;
+        const int seq = 2 * tt + 1, s = seq % kNST;
+        if (!mbar_wait(ready_bar(1, s), ready_parity(1, seq), abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t vst = sbase + OFF_KV + s * kOp;
+#pragma unroll
+        for (int part = 0; part < (LO ? 2 : 1); ++part) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk) {
+            const uint64_t bd = sw128_desc(vst + kk * 16 * 128, kHalf, 1024);
+            mma_f16_ta(tmem_o + ob * kD, tmem_s + pb * kTile + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, bd,
+                       IDESC_O, (first && part == 0 && kk == 0) ? 0u : 1u);
+          }
+        }
+        mma_commit(bar(B_EMPTY + s));
+        mma_commit(bar(B_OSTEP + pb));
+        return true;
+      };
+      for (long long kk = 0; ok; ++kk) {
+        const long long u = unit_index(kk, blockIdx.x, gridDim.x);
+        if (u >= U) break;
+        const Unit x = unit_of(a, G, BS, u);
+        if (x.ntok <= 0) continue;
+        const int qi = ui & 1, ob = ui & 1;
+        if (!mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), (ui >> 1) & 1, abort_flag)) { ok = false; break; }
+        const uint32_t qst = sbase + OFF_Q + qi * kOp;
+        for (int k = 0; k < x.ntiles; ++k, ++tc_) {
+          const int sb = tc_ & 1;
+          const int seq = 2 * tc_, s = seq % kNST;
+          if (!mbar_wait(ready_bar(0, s), ready_parity(0, seq), abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t kst = sbase + OFF_KV + s * kOp;
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint64_t ad = sw128_desc(qst + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024);
+            const uint64_t bd = sw128_desc(kst + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024);
+            mma_f16(tmem_s + sb * kTile, ad, bd, IDESC_S, ks > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(B_EMPTY + s));
+          mma_commit(bar(B_SFULL + sb));
+          if (k == x.ntiles - 1) mma_commit(bar(B_QEMPTY + qi));
+          if (k > 0 && !issue_pv(tc_ - 1, k == 1, ob)) { ok = false; break; }
+        }
+        if (ok && !issue_pv(tc_ - 1, x.ntiles == 1, ob)) ok = false;
+        ++ui;
+      }
+      if (!ok) give_up();
+      mma_commit(bar(B_DONE));                   // every issued MMA done before TMEM is freed
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try(bar(B_DONE), 0) && globaltimer() - t0 < kWaitNs) {}
+    }
+  } else if (CONV && warp >= R::kConv) {
+    // ------------------------------------------------------------ converters
+    if constexpr (CONV) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+      const int r = threadIdx.x - R::kConv * 32;   // this thread's row of every operand
+      int tc_ = 0, ui = 0;
+      bool ok = true;
+      for (long long kk = 0; ok; ++kk) {
+        const long long u = unit_index(kk, blockIdx.x, gridDim.x);
+        if (u >= U) break;
+        const Unit x = unit_of(a, G, BS, u);
+        if (x.ntok <= 0) continue;
+        if constexpr (QC) {
+          const int qi = ui & 1;
+          if (!mbar_wait(bar(B_QFULL + qi), (ui >> 1) & 1, abort_flag)) { ok = false; break; }
+          rowe[qi * 128 + r] = (int8_t)rescale_row(smem + OFF_Q + qi * kOp, r);
+          fence_proxy_async();
+          mbar_arrive(bar(B_QCONV + qi));
+        }
+        for (int k = 0; k < x.ntiles && ok; ++k, ++tc_) {
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!(kv ? V8 : K8)) continue;
+            const int seq = 2 * tc_ + kv, s = seq % kNST;
+            if (!mbar_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) { ok = false; break; }
+            const int t = x.tile0(k) + r;
+            // a V row no row of the unit attends meets only zero weights: it must be finite
+            const bool zero = kv && (!x.needs(t, 1) || ((slots[tc_ % kSlots].missing >> (r / BS)) & 1u));
+            widen_row(smem + OFF_KV + s * kOp, r, zero);
+            fence_proxy_async();
+            mbar_arrive(bar(B_CONV + s));
+          }
+        }
+        ++ui;
+      }
+      if (!ok) give_up();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax / epilogue
+    if constexpr (CONV) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    const int r = threadIdx.x & 127;             // query row = TMEM lane
+    const int hf = threadIdx.x >> 7;             // which half of the keys and of O
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const int tl = r / G, g = r - (r / G) * G;   // token of the unit, head of the group
+    float* xch = reinterpret_cast<float*>(smem + OFF_XCH);    // [2][128]
+    // the two warps that share 32 rows
+    auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
+    auto vote256 = [](bool v) -> bool {
+      uint32_t o;
+      asm volatile("{ .reg .pred pi, po; setp.ne.u32 pi, %1, 0; bar.red.or.pred po, 5, 256, pi;"
+                   " selp.u32 %0, 1, 0, po; }"
+                   : "=r"(o) : "r"((uint32_t)v) : "memory");
+      return o != 0;
+    };
+    bool failed = false;
+    int tc_ = 0, ui = 0;                         // tiles seen, units done
+    // Wait for the output product of tile t. Products alternate between two barriers by
+    // tile parity, so a parity wait is exact: the barrier of t has passed the phase
+    // before t's (S of tile t or a later one has been seen, and the issuer puts S(t)
+    // after O(t - 2) on the in-order tensor pipe) and cannot pass t's own before tile
+    // t + 2 is handed over.
+    auto wait_o = [&](int t) {
+      if (!mbar_wait(bar(B_OSTEP + (t & 1)), (t >> 1) & 1, abort_flag)) failed = true;
+    };
+    for (long long kk = 0; !failed; ++kk) {
+      const long long u = unit_index(kk, blockIdx.x, gridDim.x);
+      if (u >= U) break;
+      const Unit x = unit_of(a, G, BS, u);
+      if (x.ntok <= 0) continue;
+      const int ob = ui & 1;
+      const bool row_ok = tl < x.ntok;
+      const int pos = x.pos0 + tl;               // this row attends keys t <= pos with
+      const int wlo = a.window > 0 ? max(0, pos - a.window + 1) : 0;   // t >= wlo or t < sinks
+      // the window of the unit's last token starts at last_lo
+      const int last_lo = a.window > 0 ? max(0, x.t1 - a.window) : 0;
+      const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
+      float m = -FLT_MAX, l = 0.f;               // l: this half's part of the row sum
+      float f0 = a.scale_log2;                   // score factor of the row
+      if constexpr (QC) {
+        if (!mbar_wait(bar(B_QCONV + (ui & 1)), (ui >> 1) & 1, abort_flag)) failed = true;
+        f0 *= __uint_as_float((uint32_t)(127 - rowe[(ui & 1) * 128 + r]) << 23);
+        mbar_arrive(bar(B_QEMPTY + (ui & 1)));
+      }
+      for (int k = 0; k < x.ntiles; ++k, ++tc_) {
+        const int sb = tc_ & 1;
+        const int ts = x.tile0(k);
+        if (!mbar_wait(bar(B_SFULL + sb), (tc_ >> 1) & 1, abort_flag)) failed = true;
+        tc_fence_after();
+        const uint32_t srow = tmem_s + lane_off + sb * kTile + 64 * hf;
+        uint32_t raw[64];
+        tmem_ld32(srow, raw);
+        tmem_ld32(srow + 32, raw + 32);
+        // blocks that were not loaded: the producer's word (8-bit pools), else the table's
+        const Slot& slot = slots[tc_ % kSlots];
+        uint32_t missing = 0;
+        if constexpr (CONV) {
+          // (the tile's V stage being ready says that its slot is written; the stage cannot
+          // be reused before this thread hands over its weights)
+          const int seq = 2 * tc_ + 1, s = seq % kNST;
+          if (!mbar_wait(ready_bar(1, s), ready_parity(1, seq), abort_flag)) failed = true;
+          missing = *reinterpret_cast<const volatile uint32_t*>(&slot.missing) & ((1u << NB_T) - 1u);
+        } else {
+#pragma unroll
+          for (int q = 0; q < NB_T; ++q) {
+            bool gone = true;
+            if (x.needs(ts + q * BS, BS)) {
+              const int ph = __ldg(table + ts / BS + q);
+              gone = ph < 0 || ph >= a.num_blocks;
+            }
+            missing |= gone ? 1u << q : 0u;
+          }
+        }
+        // every row sees every key of the tile
+        const bool open = missing == 0 && ts + kTile <= x.pos0 + 1 && (ts >= last_lo || ts + kTile <= a.sinks);
+        if (!V8 && !open) {
+          // a V row no row of the unit attends meets only zero weights: it must be finite
+          // (each group zeroes one d-half of the row)
+          if (!x.needs(ts + r, 1) || ((missing >> (r / BS)) & 1u)) {
+            const int seq = 2 * tc_ + 1, s = seq % kNST;
+            if (!mbar_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) failed = true;
+            uint4* z = reinterpret_cast<uint4*>(smem + OFF_KV + s * kOp + hf * kHalf + r * 128);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) z[q] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        tmem_wait_ld64(raw);
+        // scores in the log2 domain, s' = s + log2(V scale) with block scales
+        float s_[64];
+#pragma unroll
+        for (int q = 0; q < 64 / 16; ++q) {
+          const int blk = (64 * hf + 16 * q) / BS;
+          const float f = BSC ? f0 * slot.ks[blk] : f0, e = BSC ? slot.lvs[blk] : 0.f;
+#pragma unroll
+          for (int j = 16 * q; j < 16 * q + 16; ++j)
+            s_[j] = BSC ? fmaf(__uint_as_float(raw[j]), f, e) : __uint_as_float(raw[j]) * f;
+        }
+        if (!open) {
+          // one bit per key of a 32-key chunk: up to the row's position, from its window
+          // on or a first token, in a block that is there
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int t0 = ts + 64 * hf + 32 * c;
+            auto below = [&](int lim) -> uint32_t {            // keys of the chunk under lim
+              const int n = lim - t0;
+              return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : ((1u << n) - 1u);
+            };
+            uint32_t msk = below(pos + 1) & (~below(wlo) | below(a.sinks));
+#pragma unroll
+            for (int q = 0; q < 32 / BS; ++q)
+              if ((missing >> ((64 * hf + 32 * c) / BS + q)) & 1u) msk &= ~(kBlkBits << (q * BS));
+            if (!row_ok) msk = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              s_[32 * c + j] = ((msk >> j) & 1u) ? s_[32 * c + j] : -CUDART_INF_F;
+          }
+        }
+        float t0 = -CUDART_INF_F, t1 = t0, t2 = t0, t3 = t0;
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+          t0 = fmaxf(t0, s_[j]);
+          t1 = fmaxf(t1, s_[j + 1]);
+          t2 = fmaxf(t2, s_[j + 2]);
+          t3 = fmaxf(t3, s_[j + 3]);
+        }
+        float tm = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+        // the row's tile maximum: both halves (the second barrier keeps the buffer until
+        // both have read it)
+        xch[hf * 128 + r] = tm;
+        pair_sync();
+        tm = fmaxf(tm, xch[(hf ^ 1) * 128 + r]);
+        pair_sync();
+        const bool resc = tm > m + kMove;
+        if (k == 0) {
+          m = fmaxf(tm, -FLT_MAX);
+        } else if (__any_sync(0xffffffffu, resc)) {
+          // some rows move their reference; O holds the products of tiles up to k - 1:
+          // wait for the last one, rescale this half's columns (both halves of a row take
+          // the same decision)
+          const float alpha = resc ? ex2(m - tm) : 1.f;
+          if (resc) m = tm;
+          wait_o(tc_ - 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
+            float o[16];
+            tmem_ld16(tmem_o + lane_off + ob * kD + c, o);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+            tmem_put16(tmem_o + lane_off + ob * kD + c, w);
+          }
+          tmem_wait_st();
+          l *= alpha;
+        }
+        // weights and this half's part of the row sum; a 32-key chunk's weights go over
+        // its scores, hi parts in its first 16 columns, lo parts in the next 16
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[16], lo[16];
+          float part[2] = {0.f, 0.f};            // sums of the chunk's 16-key halves
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = ex2(s_[32 * c + 2 * e] - m);
+            const float p1 = ex2(s_[32 * c + 2 * e + 1] - m);
+            part[e >> 3] += p0 + p1;
+            pack2<FO == 1, LO>(p0, p1, hi[e], lo[e]);
+          }
+          tmem_put16(srow + 32 * c, hi);
+          if (LO) tmem_put16(srow + 32 * c + 16, lo);
+          if (BSC) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int blk = (64 * hf + 32 * c + 16 * q) / BS;
+              l = fmaf(part[q], __uint_as_float((uint32_t)(127 - (int)slot.lvs[blk]) << 23), l);
+            }
+          } else {
+            l += part[0] + part[1];
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(B_PREADY + sb));
+      }
+      // ---- epilogue: O / l of this row to the output, each half its 64 columns. The
+      // products of the last two tiles may both be pending; the last one's commit tracks
+      // every earlier MMA, so one wait covers both.
+      xch[hf * 128 + r] = l;
+      pair_sync();
+      const float lrow = xch[r] + xch[128 + r];
+      pair_sync();
+      wait_o(tc_ - 1);
+      tc_fence_after();
+      const float inv = lrow == 0.f ? 0.f : a.v_scale / lrow;
+      const size_t orow = ((size_t)(x.qrow0 + tl) * a.Hq + (size_t)x.h * G + g) * kD;
+#pragma unroll 1
+      for (int c = 64 * hf; c < 64 * hf + 64; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tmem_o + lane_off + ob * kD + c, o);
+        tmem_wait_ld();
+        if (row_ok && !failed) {
+          if (a.out_dtype == PA_F32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+          } else {
+            uint32_t pk[16], none;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float v0 = __uint_as_float(o[2 * e]) * inv, v1 = __uint_as_float(o[2 * e + 1]) * inv;
+              pack2<FMT == 1, false>(v0, v1, pk[e], none);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(B_ODONE + ob));
+      ++ui;
+      // the warps of both groups leave together
+      failed = vote256(failed);
+    }
+    if (failed) give_up();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == R::kMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// Query [T][Hq][128] seen as [T][Hq][2 d-halves][64]: a box of 128 / G tokens x G heads
+// x one d-half lands as 128 rows (token-major, then head) of 128 B, 128-byte swizzled.
+// 16-bit pools [NB][bs][Hkv][128] seen as [NB][2][Hkv][bs][64]: a box of one block's rows
+// of one head and d-half; pools of codes [NB][Hkv][bs][128]: a box of one block's rows of
+// one head, a 128-byte line per row.
+bool make_maps(const PrefillLaunch& p, int G, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
+  auto enc = encode_fn();
+  if (!enc || p.num_blocks <= 0) return false;
+  const CUtensorMapDataType dt =
+      p.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  auto make = [&](CUtensorMap* m, CUtensorMapDataType t, int rank, const void* base, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box) {
+    return enc(m, t, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t qdims[4] = {64, 2, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+  const cuuint64_t qstr[3] = {128, (cuuint64_t)kD * 2, (cuuint64_t)p.Hq * kD * 2};
+  const cuuint32_t qbox[4] = {64, 1, (cuuint32_t)G, (cuuint32_t)(kM / G)};
+  if (!make(q, dt, 4, p.q, qdims, qstr, qbox)) return false;
+  const cuuint64_t hkv = (cuuint64_t)p.Hkv, bs = (cuuint64_t)p.bs, nb = (cuuint64_t)p.num_blocks;
+  const cuuint64_t dims[5] = {64, bs, hkv, 2, nb};
+  const cuuint64_t str[4] = {hkv * kD * 2, (cuuint64_t)kD * 2, 128, bs * hkv * kD * 2};
+  const cuuint32_t box[5] = {64, (cuuint32_t)p.bs, 1, 1, 1};
+  const cuuint64_t cdims[4] = {(cuuint64_t)kD, bs, hkv, nb};
+  const cuuint64_t cstr[3] = {hkv * kD, (cuuint64_t)kD, bs * hkv * kD};
+  const cuuint32_t cbox[4] = {(cuuint32_t)kD, (cuuint32_t)p.bs, 1, 1};
+  for (int i = 0; i < 2; ++i) {
+    const void* pool = i == 0 ? p.k_cache : p.v_cache;
+    CUtensorMap* m = i == 0 ? k : v;
+    const bool ok = (i == 0 ? p.k_dtype : p.v_dtype) == PA_FP8_E4M3
+                        ? make(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pool, cdims, cstr, cbox)
+                        : make(m, dt, 5, pool, dims, str, box);
+    if (!ok) return false;
+  }
+  return true;
+}
+
+template <int FMT, int BS, bool K8, bool V8, bool BSC>
+int launch_t(const Args& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+             cudaStream_t stream) {
+  auto kern = prefill_window_kernel<FMT, BS, K8, V8, BSC>;
+  // dynamic shared memory above 48 KB needs the attribute, on the current device
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const long long U = (long long)a.B * a.chunks * a.Hkv;
+  const long long grid = U < sm_count_cached() ? U : sm_count_cached();
+  return launch_k(kern, dim3((unsigned)grid), dim3(Roles<K8 || V8>::kThreads), kSmem, stream, a, q, k, v) ==
+                 cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 template <bool K8, bool V8, bool BSC>
-int launch_x(const FaArgs& a, int dtype, const CUtensorMap& q, const CUtensorMap& k,
-             const CUtensorMap& v, cudaStream_t stream) {
+int launch_kv(const Args& a, int dtype, int bs, const CUtensorMap& q, const CUtensorMap& k,
+              const CUtensorMap& v, cudaStream_t stream) {
   if (dtype == PA_BF16)
-    return a.bs == 16 ? launch_fa_t<1, 16, 0, K8, V8, true, BSC>(a, q, k, v, stream)
-                      : launch_fa_t<1, 32, 0, K8, V8, true, BSC>(a, q, k, v, stream);
-  return a.bs == 16 ? launch_fa_t<0, 16, 0, K8, V8, true, BSC>(a, q, k, v, stream)
-                    : launch_fa_t<0, 32, 0, K8, V8, true, BSC>(a, q, k, v, stream);
+    return bs == 16 ? launch_t<1, 16, K8, V8, BSC>(a, q, k, v, stream)
+                    : launch_t<1, 32, K8, V8, BSC>(a, q, k, v, stream);
+  return bs == 16 ? launch_t<0, 16, K8, V8, BSC>(a, q, k, v, stream)
+                  : launch_t<0, 32, K8, V8, BSC>(a, q, k, v, stream);
 }
 
 }  // namespace
@@ -29,15 +866,15 @@ int launch_prefill_window(const PrefillLaunch& p, cudaStream_t stream) {
   const int G = p.Hq / p.Hkv;
   const bool k8 = p.k_dtype == PA_FP8_E4M3, v8 = p.v_dtype == PA_FP8_E4M3;
   CUtensorMap q, k, v;
-  if (!make_fa_maps(p, G, k8, v8, &q, &k, &v)) return PA_ERR_CUDA;
-  FaArgs a{};
+  if (!make_maps(p, G, &q, &k, &v)) return PA_ERR_CUDA;
+  Args a{};
   a.out = p.out;
   a.out_dtype = p.out_dtype;
   a.block_tables = p.block_tables;
   a.max_blocks = p.max_blocks;
   a.context_lens = p.context_lens;
   a.query_start = p.query_start;
-  a.B = p.B; a.Hq = p.Hq; a.Hkv = p.Hkv; a.bs = p.bs; a.num_blocks = p.num_blocks;
+  a.B = p.B; a.Hq = p.Hq; a.Hkv = p.Hkv; a.num_blocks = p.num_blocks;
   const int tpu = kM / G;
   a.chunks = p.max_query_len / tpu + (p.max_query_len % tpu != 0);
   a.scale_log2 = p.scale_log2;
@@ -46,11 +883,11 @@ int launch_prefill_window(const PrefillLaunch& p, cudaStream_t stream) {
   a.err_flag = p.err_flag;
   a.window = p.window; a.sinks = p.sinks;
   a.k_scales = p.k_scales; a.v_scales = p.v_scales;
-  if (p.k_scales) return launch_x<true, true, true>(a, p.dtype, q, k, v, stream);
-  if (k8 && v8) return launch_x<true, true, false>(a, p.dtype, q, k, v, stream);
-  if (k8) return launch_x<true, false, false>(a, p.dtype, q, k, v, stream);
-  if (v8) return launch_x<false, true, false>(a, p.dtype, q, k, v, stream);
-  return launch_x<false, false, false>(a, p.dtype, q, k, v, stream);
+  if (p.k_scales) return launch_kv<true, true, true>(a, p.dtype, p.bs, q, k, v, stream);
+  if (k8 && v8) return launch_kv<true, true, false>(a, p.dtype, p.bs, q, k, v, stream);
+  if (k8) return launch_kv<true, false, false>(a, p.dtype, p.bs, q, k, v, stream);
+  if (v8) return launch_kv<false, true, false>(a, p.dtype, p.bs, q, k, v, stream);
+  return launch_kv<false, false, false>(a, p.dtype, p.bs, q, k, v, stream);
 }
 
 }  // namespace pa

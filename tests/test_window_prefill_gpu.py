@@ -11,6 +11,10 @@ from window_testlib import DT, Paged, attend, check, e4m3_values, visible
 pytestmark = pytest.mark.gpu
 
 
+def _w(vt):
+    return 2.0 ** -12 + 2.0 ** -15 if vt == "fp8" else 2.0 ** -15
+
+
 def _case(seed, prior, new, Hq, Hkv, bs, qt, kt, vt, window, sinks, blk8=False, spread=0, ks=1.0, vs=1.0,
           sharp=1.0):
     ctx = [p + n for p, n in zip(prior, new)]
@@ -33,7 +37,7 @@ def _case(seed, prior, new, Hq, Hkv, bs, qt, kt, vt, window, sinks, blk8=False, 
     for b, (c, n) in enumerate(zip(ctx, new)):
         for i in range(n):
             ref[at], tol[at] = attend(q[at].double(), P.k64[b], P.v64[b], visible(c, c - n + i, window, sinks),
-                                      scale)
+                                      scale, _w(vt))
             at += 1
     return P, q, scale, ref, tol, list(new)
 
@@ -122,7 +126,7 @@ def test_bad_lengths_blocks_and_scales():
         out, err = _run(P, q, scale, new, 0, 0)
         assert err == (ops.PA_DEV_BAD_SCALE if what == "scale" else ops.PA_DEV_BAD_BLOCK_ID)
         for i in (0, 7, 19):
-            r, t = attend(q[i].double(), P.k64[0], P.v64[0], keep & visible(100, 80 + i, 0, 0), scale)
+            r, t = attend(q[i].double(), P.k64[0], P.v64[0], keep & visible(100, 80 + i, 0, 0), scale, _w("fp8"))
             check(out[i], r, t, what)
         check(out[20:], ref[20:], tol[20:], what)
 
@@ -185,7 +189,8 @@ def test_serving_run(blk8):
         torch.cuda.synchronize()
         k64, v64 = cached(tab, ctx + n)
         for i in range(n):
-            ref, tol = attend(qo[i].cpu().double(), k64, v64, visible(ctx + n, ctx + i, window, sinks), scale)
+            ref, tol = attend(qo[i].cpu().double(), k64, v64, visible(ctx + n, ctx + i, window, sinks), scale,
+                              _w("fp8") if blk8 and n > 1 else 2.0 ** -15)
             check(out[i], ref, tol, f"token {ctx + i}")
 
     for n in (50, 1, 1, 37, 1, 64, 1):

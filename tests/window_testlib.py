@@ -6,9 +6,10 @@ Attention tolerances. With fp32 output the kernels differ from the exact result 
    so |s' - s| <= e_s = steps * 2^-23 * scale * sum_d |q_d k_d| (+ a few roundings of
    s itself, covered by doubling the steps), and a score error e moves a weighted
    average of values by at most 2 e max|v|;
- * the weights: two 16-bit parts hold at least 16 bits (2^-16 relative), ex2 2^-22;
+ * the weights: two 16-bit parts hold at least 16 bits (2^-16 relative), ex2 2^-22
+   (prefill over 8-bit V: one f16 part, half a step is 2^-12: w = 2^-12 + 2^-15);
  * the sums over N keys: at most N roundings of 2^-24 each;
-so tol = max|v| (2 e_s + 2^-15 + (N + 64) 2^-24), plus half a step of the output type.
+so tol = max|v| (2 e_s + w + (N + 64) 2^-24), w = 2^-15 unless said, plus half a step of the output type.
 """
 
 from __future__ import annotations
@@ -107,9 +108,9 @@ class Paged:
             torch.tensor(self.ctx, dtype=torch.int32, device="cuda")
 
 
-def attend(q, k64, v64, ok, scale):
+def attend(q, k64, v64, ok, scale, w=2.0 ** -15):
     """Exact attention of one query token's heads q [Hq, D] (double) over keys [c, Hkv, D];
-    also the tolerance of each head for fp32 output."""
+    also the tolerance of each head for fp32 output (w: relative rounding of a weight)."""
     Hq, D = q.shape
     Hkv = k64.shape[1]
     out = torch.zeros(Hq, D, dtype=torch.float64)
@@ -125,7 +126,7 @@ def attend(q, k64, v64, ok, scale):
         out[h * G:(h + 1) * G] = p @ vv
         e_s = 2 * max(D / 16, 1) * 2.0 ** -23 * scale * (qq.abs() @ kk.abs().T).amax(dim=-1)
         n = idx.numel()
-        tol[h * G:(h + 1) * G, 0] = vv.abs().max() * (2 * e_s + 2.0 ** -15 + (n + 64) * 2.0 ** -24)
+        tol[h * G:(h + 1) * G, 0] = vv.abs().max() * (2 * e_s + w + (n + 64) * 2.0 ** -24)
     return out, tol
 
 
