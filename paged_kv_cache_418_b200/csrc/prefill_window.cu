@@ -11,12 +11,12 @@
 //   S[128 x 128] = Q . K^T (tensor memory, two buffers by tile)
 //   O[128 x 128] += P . V  (two buffers by unit; P is read from tensor memory)
 // Two groups of four softmax warps share the rows: thread (half hf, row r) has keys
-// [64 hf, 64 hf + 64) of every tile in registers (64 scores: one read of S), swaps the
-// tile's row maximum with the other half's thread through shared memory, writes its
-// weights over S, and owns O's columns [64 hf, 64 hf + 64). The reference maximum
-// moves when a tile passes it by 2^8 (then the row's O is rescaled in tensor memory);
-// it is floored at -FLT_MAX, so masked scores (-inf) need no guard. A tile that
-// every row sees whole skips the masks.
+// [64 hf, 64 hf + 64) of every tile in registers (64 scores: one read of S), writes its
+// weights over S, and owns O's columns [64 hf, 64 hf + 64). The reference maximum of a
+// row moves only when a tile passes it by far: the two threads of a row vote on that
+// with one barrier, and only then swap their maxima through shared memory (and rescale
+// the row's O in tensor memory). It is floored at -FLT_MAX, so masked scores (-inf) need
+// no guard. A tile that every row sees whole skips the masks.
 //
 // 16-bit pools: the products take the query's type, and the weights two 16-bit parts
 // (hi + lo, ~16 bits).
@@ -26,8 +26,14 @@
 // a power of two per row and becomes f16 too, exactly (an element 2^-39 of its row's
 // largest is rounded), once per unit. Weights over 8-bit V enter as one f16 part: their
 // 2^-12 is far below the 2^-4 of the codes they multiply, and under half a step of
-// either 16-bit output. (Widened by the softmax warps between two tiles instead, as
-// in prefill_tc.cu, an 8192-token prompt took 2.1 ms.)
+// either 16-bit output.
+//
+// Measured (8192-token prompt, 32 query heads over 8, block-scaled cache): 762 us, 722
+// TFLOP/s; FP8 pools with one scale 711 us; bf16 pools 947 us. Widened by the softmax
+// warps between two tiles instead, as prefill_tc.cu does, the block-scaled prompt took
+// 2110 us. A tile takes ~3000 cycles: the softmax threads ~2400 (1350 of them the
+// exponentials, 1024 at the special-function units' rate), beside 1750 of shared-memory
+// bandwidth (operands of both products, codes in and f16 out) and ~2000 of the issuer.
 //
 // Block-scaled pools: K's power of two multiplies its keys' scores; V's enters as its
 // log2, s' = s + log2(vs), so the running maximum is that of the whole contribution,
@@ -61,7 +67,6 @@ constexpr int kTile = 128;                      // keys per tile
 constexpr int kHalf = 128 * 128;                // one 64-wide d-half of a 128-row operand
 constexpr int kOp = 2 * kHalf;                  // one 128 x 128 16-bit operand: 32 KB
 constexpr int kNST = 5;                         // K / V ring stages (odd: a stage serves K and V in turn)
-constexpr float kMove = 8.f;                    // weights stay under 2^8, inside f16
 constexpr int kTmemCols = 512;                  // S/P x2 (by tile), O x2 (by unit)
 constexpr int kSlots = 4;                       // tiles of scales and masks (see the producer)
 
@@ -270,6 +275,10 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   constexpr bool QC = K8 && FMT == 1;           // the query becomes f16
   constexpr int FS = K8 ? 0 : FMT, FO = V8 ? 0 : FMT;     // operand types of the two products
   constexpr bool LO = !V8;                      // weights in two parts
+  // The reference maximum of a row moves when a tile passes it by 2^kMove: rarely, as
+  // that waits for the output product in flight. Weights stay under 2^kMove: inside f16,
+  // or, as bf16, with room for 2^60 of values and sums in fp32.
+  constexpr float kMove = FO == 1 ? 64.f : 14.f;
   using R = Roles<CONV>;
   constexpr int NB_T = kTile / BS;              // physical blocks per tile
   constexpr uint32_t kBlkBits = (uint32_t)((1ull << BS) - 1ull);   // one block's keys in a chunk mask
@@ -552,6 +561,13 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
     float* xch = reinterpret_cast<float*>(smem + OFF_XCH);    // [2][128]
     // the two warps that share 32 rows
     auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
+    auto pair_vote = [&](bool v) -> bool {
+      uint32_t o;
+      asm volatile("{ .reg .pred pi, po; setp.ne.u32 pi, %2, 0; bar.red.or.pred po, %1, 64, pi;"
+                   " selp.u32 %0, 1, 0, po; }"
+                   : "=r"(o) : "r"(1 + (warp & 3)), "r"((uint32_t)v) : "memory");
+      return o != 0;
+    };
     auto vote256 = [](bool v) -> bool {
       uint32_t o;
       asm volatile("{ .reg .pred pi, po; setp.ne.u32 pi, %1, 0; bar.red.or.pred po, 5, 256, pi;"
@@ -601,10 +617,6 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         const Slot& slot = slots[tc_ % kSlots];
         uint32_t missing = 0;
         if constexpr (CONV) {
-          // (the tile's V stage being ready says that its slot is written; the stage cannot
-          // be reused before this thread hands over its weights)
-          const int seq = 2 * tc_ + 1, s = seq % kNST;
-          if (!mbar_wait(ready_bar(1, s), ready_parity(1, seq), abort_flag)) failed = true;
           missing = *reinterpret_cast<const volatile uint32_t*>(&slot.missing) & ((1u << NB_T) - 1u);
         } else {
 #pragma unroll
@@ -671,34 +683,35 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           t3 = fmaxf(t3, s_[j + 3]);
         }
         float tm = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-        // the row's tile maximum: both halves (the second barrier keeps the buffer until
-        // both have read it)
-        xch[hf * 128 + r] = tm;
-        pair_sync();
-        tm = fmaxf(tm, xch[(hf ^ 1) * 128 + r]);
-        pair_sync();
-        const bool resc = tm > m + kMove;
-        if (k == 0) {
-          m = fmaxf(tm, -FLT_MAX);
-        } else if (__any_sync(0xffffffffu, resc)) {
-          // some rows move their reference; O holds the products of tiles up to k - 1:
-          // wait for the last one, rescale this half's columns (both halves of a row take
-          // the same decision)
-          const float alpha = resc ? ex2(m - tm) : 1.f;
-          if (resc) m = tm;
-          wait_o(tc_ - 1);
-          tc_fence_after();
+        if (k == 0 || pair_vote(tm > m + kMove)) {
+          // the row's tile maximum: both halves (the second barrier keeps the buffer until
+          // both have read it)
+          xch[hf * 128 + r] = tm;
+          pair_sync();
+          tm = fmaxf(tm, xch[(hf ^ 1) * 128 + r]);
+          pair_sync();
+          if (k == 0) {
+            m = fmaxf(tm, -FLT_MAX);
+          } else {
+            // O holds the products of tiles up to k - 1: wait for the last one, rescale this
+            // half's columns (both halves of a row take the same decision)
+            const bool resc = tm > m + kMove;
+            const float alpha = resc ? ex2(m - tm) : 1.f;
+            if (resc) m = tm;
+            wait_o(tc_ - 1);
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
-            float o[16];
-            tmem_ld16(tmem_o + lane_off + ob * kD + c, o);
-            uint32_t w[16];
+            for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
+              float o[16];
+              tmem_ld16(tmem_o + lane_off + ob * kD + c, o);
+              uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-            tmem_put16(tmem_o + lane_off + ob * kD + c, w);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+              tmem_put16(tmem_o + lane_off + ob * kD + c, w);
+            }
+            tmem_wait_st();
+            l *= alpha;
           }
-          tmem_wait_st();
-          l *= alpha;
         }
         // weights and this half's part of the row sum; a 32-key chunk's weights go over
         // its scores, hi parts in its first 16 columns, lo parts in the next 16

@@ -141,7 +141,10 @@ def check_block_mapping(block_mapping: torch.Tensor, fn: str = "pa_copy_blocks",
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()       # (the declared argtypes make it a pointer)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
 
 
 def _on_device_of(*tensors):
@@ -149,14 +152,17 @@ def _on_device_of(*tensors):
     default stream (and, for pa_decode_static, the scratch) is that device's."""
     for t in tensors:
         if t is not None and t.is_cuda:
-            return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+            # the usual case costs one comparison instead of a switch and its undoing
+            return _SAME_DEVICE if t.get_device() == torch.cuda.current_device() \
+                else torch.cuda.device(t.device)
+    return _SAME_DEVICE
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        # torch.cuda.current_stream().cuda_stream without the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def pa_dtype(t: torch.Tensor) -> int:
@@ -482,10 +488,13 @@ def workspace_for(query: torch.Tensor, key_cache: torch.Tensor, max_context_len:
 def _token_stride(t: torch.Tensor, fn: str) -> int:
     """Elements between tokens of a [T,H,D] tensor whose heads are dense (a slice of a
     fused projection is; a transposed or expanded view is refused)."""
-    if t.dim() != 3 or (t.shape[1] > 0 and t.stride(2) != 1) or \
-            (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    if t.dim() != 3:
         raise PAError(fn, 2)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D):
+        raise PAError(fn, 2)
+    return st if T > 1 else max(st, H * D)
 
 
 def check_block_runs(slot_mapping: torch.Tensor, block_size: int,
