@@ -540,9 +540,9 @@ int pa_copy_scales(float* dst_k_scales, float* dst_v_scales, const float* src_k_
  *               and their table entries, are not read (a cache may have freed
  *               them). context_lens still counts every token.
  * workspace     device scratch of at least pa_window_workspace_size(...) bytes,
- *               256-byte aligned, or NULL when that size is 0; its contents do
- *               not matter before or after.
- * Other arguments, types, shapes and errors as pa_decode_kv.
+ *               256-byte aligned; its contents do not matter before or after.
+ *               Calls that may run at the same time need one each.
+ * num_blocks    >= 1. Other arguments, types, shapes and errors as pa_decode_kv.
  */
 size_t pa_window_workspace_size(int B, int Hq, int Hkv, int D, int max_context_len, int window,
                                 int num_sinks);
@@ -575,7 +575,10 @@ int pa_decode_blk8(void* out, int out_dtype, const void* query, int q_dtype, con
  *   t <= p  with  t > p - window  or  t < num_sinks
  * (window >= 1, num_sinks >= 0). Blocks that none of the call's queries attends,
  * and their table entries, are not read. Positions, types, shapes and errors as
- * pa_prefill_kv. As there, the query rows of up to 128 / G neighbouring tokens
+ * pa_prefill_kv (num_blocks >= 1; a sequence whose query_start passes T also sets
+ * PA_DEV_BAD_CTX). Sums and softmax statistics are fp32; the weights enter the
+ * output product as two 16-bit parts, over an 8-bit V pool as one f16 value
+ * (2^-12 relative). As there, the query rows of up to 128 / G neighbouring tokens
  * are one matrix operand: an infinite or NaN V element of a token that one of
  * them attends may reach the others' rows.
  *

@@ -351,10 +351,10 @@ __device__ __forceinline__ void store8_out(void* out, size_t i, const float* f, 
 }
 
 constexpr int kMaxStages = 6;
-template <class C> constexpr int join_bytes() { return kCons * C::NS * 32 * 4; }
-// ring | sums to join (groups of fewer than 8 heads) | metadata, barriers
-template <class C> constexpr int smem_bytes() {
-  return 1024 + kRing + join_bytes<C>() + C::NST * (int)sizeof(Meta) + 2 * kMaxStages * 8 + 16;
+// ring | metadata, barriers | sums to join (groups of fewer than 8 heads only)
+template <class C> constexpr int meta_bytes() { return C::NST * (int)sizeof(Meta) + 2 * kMaxStages * 8; }
+template <class C> constexpr int smem_bytes(int hg) {
+  return 1024 + kRing + meta_bytes<C>() + (hg < kCons ? kCons * C::NS * 32 * 4 : 0);
 }
 
 }  // namespace
@@ -368,8 +368,8 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* sm_join = reinterpret_cast<float*>(smem + kRing);
-  Meta* meta = reinterpret_cast<Meta*>(smem + kRing + join_bytes<C>());
+  Meta* meta = reinterpret_cast<Meta*>(smem + kRing);
+  float* sm_join = reinterpret_cast<float*>(smem + kRing + meta_bytes<C>());
   const uint32_t sring = smem_addr(smem);
   const uint32_t bars = smem_addr(meta + NST);
   auto full = [&](int s) { return bars + 16u * (uint32_t)s; };
@@ -639,6 +639,8 @@ __global__ void __launch_bounds__(NW < 4 ? 128 : NW * 32) decode_window_merge_ke
   const int y = h / a.hg * chunks + g / a.heads;
   const int2 cut = a.cuts[(size_t)b * (a.Hkv / a.hg * chunks) + y];
   if (cut.x == cut.y) return;                  // whole, or empty
+  // (a launch whose waits gave up may have left no cuts)
+  if (cut.x < 0 || cut.y < cut.x || cut.y >= a.grid) return;
   const int rows = a.hg * a.heads, r = h % a.hg * a.heads + g % a.heads;
   float M = -FLT_MAX, L = 0.f, O[PER];
 #pragma unroll
@@ -740,15 +742,16 @@ bool make_map(const WinArgs& a, const void* pool, int dt, CUtensorMap* m) {
 
 template <int KT, int VT, int D, bool BSC>
 int launch_window_t(const WinArgs& a, cudaStream_t stream) {
-  constexpr int SMEM = smem_bytes<Core<KT, VT, D, BSC>>();
-  static_assert(SMEM + 1024 <= 227 * 1024, "shared memory per CTA");
+  using C = Core<KT, VT, D, BSC>;
+  static_assert(smem_bytes<C>(1) + 1024 <= 227 * 1024, "shared memory per CTA");
+  const int smem = smem_bytes<C>(a.hg);
   auto kern = decode_window_kernel<KT, VT, D, BSC>;
   // dynamic shared memory above 48 KB needs the attribute, on the current device
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return PA_ERR_CUDA;
   CUtensorMap k, v;
   if (!make_map(a, a.k_cache, KT, &k) || !make_map(a, a.v_cache, VT, &v)) return PA_ERR_CUDA;
-  return launch_k(kern, dim3((unsigned)a.grid), dim3(kThreads), SMEM, stream, a, k, v) == cudaSuccess
+  return launch_k(kern, dim3((unsigned)a.grid), dim3(kThreads), smem, stream, a, k, v) == cudaSuccess
              ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -774,9 +777,9 @@ int launch_merge_d(const WinArgs& a, cudaStream_t stream) {
   // one; with many, a unit is rarely cut in more than two or three
   const long long units = rows / (a.hg * a.heads) + 1;
   cudaError_t e;
-  if (units < a.grid / 8)
+  if (units <= a.grid / 8)
     e = launch_k(decode_window_merge_kernel<D, 16>, dim3((unsigned)rows), dim3(512), 0, stream, a);
-  else if (units < a.grid)
+  else if (units <= a.grid / 2)
     e = launch_k(decode_window_merge_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, stream, a);
   else
     e = launch_k(decode_window_merge_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a);

@@ -65,6 +65,7 @@ int decode_window_impl(void* out, int out_dtype, const void* query, int q_dtype,
     return PA_ERR_SHAPE;
   if (B > 65535 || Hq > 65535) return PA_ERR_UNSUPPORTED;
   if (B == 0) return PA_OK;
+  if (num_blocks == 0) return PA_ERR_SHAPE;
   if (!out || !query || !key_cache || !value_cache || !block_tables || !context_lens)
     return PA_ERR_NULL;
   if (blk8 && (!k_scales || !v_scales)) return PA_ERR_NULL;
@@ -113,6 +114,7 @@ int prefill_window_impl(void* out, int out_dtype, const void* query, int q_dtype
   if (!std::isfinite(scale)) return PA_ERR_SHAPE;
   if (!blk8 && ((k8 && !scale_ok(k_scale)) || (v8 && !scale_ok(v_scale)))) return PA_ERR_SHAPE;
   if (B == 0 || T == 0 || max_query_len == 0) return PA_OK;
+  if (num_blocks == 0) return PA_ERR_SHAPE;
   if (!out || !query || !key_cache || !value_cache || !block_tables || !context_lens || !query_start)
     return PA_ERR_NULL;
   if (blk8 && (!k_scales || !v_scales)) return PA_ERR_NULL;

@@ -95,7 +95,7 @@ struct Args {
   int max_blocks;
   const int32_t* context_lens;
   const int32_t* query_start;
-  int B, Hq, Hkv, num_blocks, chunks;
+  int B, T, Hq, Hkv, num_blocks, chunks;
   float scale_log2;
   float v_scale;        // value of one V unit (FP8 V pool; 1 otherwise)
   int max_context_len;
@@ -128,7 +128,7 @@ __device__ __forceinline__ Unit unit_of(const Args& a, int G, int bs, long long 
   x.c = a.chunks - 1 - (int)(t / a.B);          // late chunks first: they attend the most keys
   const int qs = __ldg(a.query_start + x.b), qe = __ldg(a.query_start + x.b + 1);
   const int n = qe - qs, ctx = __ldg(a.context_lens + x.b);
-  x.bad = n < 0 || ctx < n || ctx > (long long)a.max_blocks * bs || ctx > a.max_context_len;
+  x.bad = qs < 0 || n < 0 || qe > a.T || ctx < n || ctx > (long long)a.max_blocks * bs || ctx > a.max_context_len;
   const long long done = (long long)x.c * tpu;  // the sequence's new tokens before the chunk
   x.ntok = x.bad ? 0 : (int)max(0ll, min((long long)tpu, n - done));
   x.qrow0 = (int)(qs + done);
@@ -887,7 +887,7 @@ int launch_prefill_window(const PrefillLaunch& p, cudaStream_t stream) {
   a.max_blocks = p.max_blocks;
   a.context_lens = p.context_lens;
   a.query_start = p.query_start;
-  a.B = p.B; a.Hq = p.Hq; a.Hkv = p.Hkv; a.num_blocks = p.num_blocks;
+  a.B = p.B; a.T = p.T; a.Hq = p.Hq; a.Hkv = p.Hkv; a.num_blocks = p.num_blocks;
   const int tpu = kM / G;
   a.chunks = p.max_query_len / tpu + (p.max_query_len % tpu != 0);
   a.scale_log2 = p.scale_log2;

@@ -72,7 +72,7 @@ def test_rope_blk8_refusals(kw, status):
     (dict(B=0), 0), (dict(window=0), 2), (dict(window=-1), 2), (dict(sinks=-1), 2), (dict(qdt=3), 3),
     (dict(kdt=1), 3), (dict(kdt=3, ksc=0.0), 2), (dict(vdt=3, vsc=INF), 2), (dict(qdt=0, kdt=0, vdt=3), 3),
     (dict(odt=1), 3), (dict(D=80), 4), (dict(bs=64), 4), (dict(Hq=6), 4), (dict(Hq=7), 4), (dict(scale=NAN), 2),
-    (dict(mb=0), 2), (dict(mc=-1), 2), (dict(B=65536), 4), (dict(q=None), 1), (dict(cl=None), 1),
+    (dict(mb=0), 2), (dict(mc=-1), 2), (dict(nb=0), 2), (dict(B=65536), 4), (dict(q=None), 1), (dict(cl=None), 1),
     (dict(out=8), 7), (dict(ws=256, wsb=100), 5), (dict(B=1, Hq=1, Hkv=1, mc=100000, window=90000, mb=9000), 5),
     (dict(B=1, Hq=1, Hkv=1, mc=100000, window=90000, mb=9000, ws=257, wsb=1 << 40), 5)])
 def test_decode_window_refusals(kw, status):
@@ -89,7 +89,7 @@ def test_decode_blk8_refusals(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(B=0), 0), (dict(T=0), 0), (dict(mq=0), 0), (dict(window=0), 2), (dict(sinks=-2), 2), (dict(qdt=0, kdt=0, vdt=0), 4),
     (dict(D=64), 4), (dict(kdt=1), 3), (dict(kdt=3, ksc=-1.0), 2), (dict(odt=1), 3), (dict(scale=INF), 2),
-    (dict(qst=None), 1), (dict(q=8), 7), (dict(T=-1), 2)])
+    (dict(qst=None), 1), (dict(q=8), 7), (dict(T=-1), 2), (dict(nb=0), 2)])
 def test_prefill_window_refusals(kw, status):
     assert call("pa_prefill_window_kv", PRE, **kw) == status
 
@@ -133,6 +133,51 @@ def test_binding_refuses_views_whose_heads_are_not_dense():
                 torch.zeros(3, 4, 128, dtype=torch.bfloat16)[:, ::2], torch.zeros(3, 256, dtype=torch.bfloat16)):
         with pytest.raises(ops.PAError):
             ops.pa_rope_and_cache_kv(x, x, bad, kc[0, :3], i, cs, kc, kc, 1.0, 1.0, i)
+
+
+def test_binding_refuses_wrong_types_and_sizes():
+    bf, i64, i32 = torch.bfloat16, torch.int64, torch.int32
+    kc = torch.zeros(4, 16, 2, 128, dtype=bf)
+    c8 = torch.zeros(4, 16, 2, 128, dtype=torch.uint8)
+    sc = torch.ones(4, 2)
+    q, k = torch.zeros(3, 8, 128, dtype=bf), torch.zeros(3, 2, 128, dtype=bf)
+    p, cs = torch.zeros(3, dtype=i64), torch.zeros(8, 128)
+    bt, cl, qs = torch.zeros(3, 4, dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(4, dtype=i32)
+
+    def refused(f, *args):
+        with pytest.raises(ops.PAError) as e:
+            f(*args)
+        assert e.value.status in (2, 3)
+
+    rope = [q, q, k, k, p, cs, kc, kc, 1.0, 1.0, p]
+    for at, bad in ((3, k.float()), (1, q.float()), (0, q[:2]), (4, p.int()), (4, p[:2]), (5, cs.double()), (10, p.int()),
+                    (3, k[:, :1]), (7, kc[:3]), (6, kc.transpose(0, 1)), (2, k[:, :, :64])):
+        a = list(rope)
+        a[at] = bad
+        refused(ops.pa_rope_and_cache_kv, *a)
+    blk = [q, q, k, k, p, cs, c8, c8, sc, sc, p]
+    for at, bad in ((6, kc), (8, sc.double()), (8, sc[:3]), (9, sc[:, :1]), (9, sc.t().contiguous().t()), (10, p[:2])):
+        a = list(blk)
+        a[at] = bad
+        refused(ops.pa_rope_and_cache_blk8, *a)
+    dec = [q, q, kc, kc, 1.0, 1.0, bt, cl, 0.1, 5, 0, 64]
+    for at, bad in ((0, q[:2]), (3, kc[:2]), (6, bt.long()), (7, cl[:2]), (6, bt[:, ::2]), (1, q.transpose(0, 1))):
+        a = list(dec)
+        a[at] = bad
+        refused(ops.pa_decode_window_kv, *a)
+    d8 = [q, q, c8, c8, sc, sc, bt, cl, 0.1, 64]
+    for at, bad in ((2, kc), (4, sc[:2]), (7, cl.long())):
+        a = list(d8)
+        a[at] = bad
+        refused(ops.pa_decode_blk8, *a)
+    pre = [q, q, kc, kc, 1.0, 1.0, bt, cl, qs, 1, 0.1, 5, 0, 64]
+    for at, bad in ((8, qs[:3]), (8, qs.long()), (0, q[:, :4])):
+        a = list(pre)
+        a[at] = bad
+        refused(ops.pa_prefill_window_kv, *a)
+    refused(ops.pa_prefill_blk8, q, q, c8, kc, sc, sc, bt, cl, qs, 1, 0.1, 64)
+    refused(ops.pa_copy_scales, sc, sc, sc, sc[:2], torch.zeros(1, 2, dtype=i64))
+    refused(ops.pa_copy_scales, sc, sc, sc, sc, torch.zeros(1, 2, dtype=i32))
 
 
 def test_debug_check_of_block_runs():

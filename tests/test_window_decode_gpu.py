@@ -219,3 +219,50 @@ def test_other_stream_and_repeatability():
     again, err = _run(P, q, scale, 640, 0, stream=s)
     assert err == 0 and torch.equal(first, again)
     check(first, ref, tol)
+
+
+def test_blocks_past_4_gib():
+    """Physical blocks whose byte offsets pass 32 bits, in the append and in the decode."""
+    Hq, Hkv, D, bs = 8, 8, 128, 32
+    nb = (1 << 32) // (bs * Hkv * D) + 40                    # 4.3 GB of codes per pool
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    kc = torch.zeros(nb, bs, Hkv, D, dtype=torch.uint8, device="cuda")
+    vc = torch.zeros_like(kc)
+    ks, vs = torch.zeros(nb, Hkv, device="cuda"), torch.zeros(nb, Hkv, device="cuda")
+    g = torch.Generator().manual_seed(5)
+    T = 70
+    blocks = torch.tensor([nb - 1, 3, nb - 30])
+    slots = blocks[torch.arange(T) // bs] * bs + torch.arange(T) % bs
+    x = torch.randn(T, 2 * Hkv, D, generator=g).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ops.pa_rope_and_cache_blk8(None, None, x[:, :Hkv], x[:, Hkv:], None, None, kc, vc, ks, vs, slots.cuda(), False,
+                               err)
+    from window_testlib import e4m3_values
+    val = e4m3_values()
+    at = blocks[torch.arange(T) // bs]
+    k64, v64 = (val[p.cpu()[at, torch.arange(T) % bs].long()] * s.cpu().double()[at][..., None]
+                for p, s in ((kc, ks), (vc, vs)))
+    assert float((k64 - x[:, :Hkv].cpu().double()).abs().max()) < 0.5      # rows did land there
+    q = torch.randn(1, Hq, D, generator=g).bfloat16()
+    ref, tol = attend(q[0].double(), k64, v64, visible(T, T - 1, 0, 0), D ** -0.5)
+    out = torch.empty(1, Hq, D, device="cuda")
+    ws = ops.window_workspace_for(q, kc, T)
+    ws = None if ws is None else ws.cuda()
+    ops.pa_decode_blk8(out, q.cuda(), kc, vc, ks, vs, blocks[None].int().cuda(),
+                       torch.tensor([T], dtype=torch.int32, device="cuda"), D ** -0.5, T, 0, 0, ws, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(out[0], ref, tol)
+
+
+@pytest.mark.parametrize("blk8", [True, False])
+def test_many_sequences_of_all_lengths(blk8):
+    """More units than the GPU has CTAs, empty ones among them: batches of units, cuts inside and
+    between sequences."""
+    ctx = [(i * i * 7) % 400 if i % 5 else 0 for i in range(300)]
+    kt = "fp8" if blk8 else "f16"
+    P, q, scale, ref, tol = _case(81, ctx, 24, 12, 64, 16, "f16", kt, kt, 0 if blk8 else 150, 2, blk8=blk8, spread=3)
+    out, err = _run(P, q, scale, 0 if blk8 else 150, 2)
+    assert err == 0
+    check(out, ref, tol)

@@ -131,6 +131,31 @@ def test_bad_lengths_blocks_and_scales():
         check(out[20:], ref[20:], tol[20:], what)
 
 
+def test_query_starts_past_the_queries_are_flagged_and_nothing_is_written():
+    P, q, scale, ref, tol, new = _case(14, [40, 30], [20, 10], 4, 1, 16, "f16", "f16", "f16", 50, 2)
+    kc, vc, _, _, bt, cl = P.dev()
+    for qs, whole in (([0, 20, 35], 0), ([-3, 20, 30], 1), ([20, 0, 10], 1)):
+        out = torch.full((64, 4, 128), 7.0, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ops.pa_prefill_window_kv(out[:30], q.cuda(), kc, vc, 1.0, 1.0, bt, cl,
+                                 torch.tensor(qs, dtype=torch.int32, device="cuda"), 20, scale, 50, 2, 60, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == ops.PA_DEV_BAD_CTX
+        assert bool((out[30:] == 7.0).all())
+
+
+@pytest.mark.parametrize("qt,kt,vt", [("bf16", "bf16", "bf16"), ("bf16", "fp8", "fp8"), ("f16", "f16", "fp8")])
+def test_many_short_units(qt, kt, vt):
+    """Chunks of one tile and one token, hundreds of units per CTA: every buffer's turn."""
+    n = 700
+    prior = [(37 * i) % 90 for i in range(n)]
+    new = [1 + (i % 3) for i in range(n)]
+    P, q, scale, ref, tol, new = _case(15, prior, new, 8, 4, 16, qt, kt, vt, 60, 1)
+    out, err = _run(P, q, scale, new, 60, 1)
+    assert err == 0
+    check(out, ref, tol)
+
+
 @pytest.mark.parametrize("blk8", [True, False])
 def test_serving_run(blk8):
     """A prompt in chunks, then single tokens: append with rotation, prefill, decode, a fork that
