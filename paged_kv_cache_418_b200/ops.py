@@ -488,21 +488,24 @@ def workspace_for(query: torch.Tensor, key_cache: torch.Tensor, max_context_len:
 def _check(fn: str, elements, dense, index, indices) -> None:
     """The sizes and addresses of the entry points below are read off these tensors, so a
     wrong one would be read past its end: one element type for `elements`, no gaps in
-    `dense` and `indices`, and the integer type `index` for `indices`."""
+    `dense` and `indices`, the integer type `index` for `indices`, and all of them on the
+    device of the first of `dense`."""
+    device = dense[0].get_device()
     for t in elements:
-        if t is not None and t.dtype != elements[0].dtype:
-            raise PAError(fn, 3)
+        if t is not None and (t.dtype != elements[0].dtype or t.get_device() != device):
+            raise PAError(fn, 3 if t.get_device() == device else 2)
     for t in dense:
-        if t is not None and not t.is_contiguous():
+        if t is not None and (not t.is_contiguous() or t.get_device() != device):
             raise PAError(fn, 2)
     for t in indices:
-        if t is not None and (t.dtype != index or not t.is_contiguous()):
+        if t is not None and (t.dtype != index or not t.is_contiguous() or t.get_device() != device):
             raise PAError(fn, 2)
 
 
 def _check_scales(fn: str, cache: torch.Tensor, *scales) -> None:
     for t in scales:
         if t.dtype != torch.float32 or not t.is_contiguous() or \
+                t.get_device() != cache.get_device() or \
                 t.shape[0] != cache.shape[0] or t.shape[1] != cache.shape[2]:
             raise PAError(fn, 2)
 
@@ -546,8 +549,10 @@ def pa_rope_and_cache_kv(query_out: Optional[torch.Tensor], query: Optional[torc
     fn = "pa_rope_and_cache_kv"
     if DEBUG:
         check_slot_mapping(slot_mapping, fn)
-    _check(fn, (key, value, query, query_out), (key_cache, value_cache, cos_sin), torch.int64,
-           (positions, slot_mapping))
+    _check(fn, (key, value, query, query_out), (key_cache, value_cache, cos_sin, err_flag),
+           torch.int64, (positions, slot_mapping))
+    if (query is None) != (query_out is None):
+        raise PAError(fn, 1)
     if key_cache.shape != value_cache.shape or cos_sin.dtype != torch.float32 or \
             key.shape != value.shape or key.shape[1:] != key_cache.shape[2:] or \
             not key.shape[0] == slot_mapping.shape[0] == positions.shape[0] or \
@@ -580,8 +585,10 @@ def pa_rope_and_cache_blk8(query_out: Optional[torch.Tensor], query: Optional[to
     and KV head, k_scales / v_scales [num_blocks, Hkv] (see pa_rope_and_cache_blk8 in
     include/pa.h). cos_sin None (with query and positions None): no rotation."""
     fn = "pa_rope_and_cache_blk8"
-    _check(fn, (key, value, query, query_out), (key_cache, value_cache, cos_sin), torch.int64,
-           (positions, slot_mapping))
+    _check(fn, (key, value, query, query_out), (key_cache, value_cache, cos_sin, err_flag),
+           torch.int64, (positions, slot_mapping))
+    if (query is None) != (query_out is None):
+        raise PAError(fn, 1)
     _check_scales(fn, key_cache, k_scales, v_scales)
     if key_cache.shape != value_cache.shape or pa_dtype(key_cache) != PA_FP8_E4M3 or \
             pa_dtype(value_cache) != PA_FP8_E4M3 or key.shape != value.shape or \
@@ -618,11 +625,15 @@ def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
     if DEBUG:
         check_block_mapping(block_mapping, "pa_copy_scales",
                             same_pool=dst_k_scales.data_ptr() == src_k_scales.data_ptr())
-    _check("pa_copy_scales", (src_k_scales, src_v_scales, dst_k_scales, dst_v_scales),
-           (src_k_scales, src_v_scales, dst_k_scales, dst_v_scales), torch.int64, (block_mapping,))
-    if src_k_scales.dtype != torch.float32 or src_k_scales.shape != src_v_scales.shape or \
-            dst_k_scales.shape != dst_v_scales.shape or src_k_scales.shape[1] != dst_k_scales.shape[1]:
-        raise PAError("pa_copy_scales", 2)
+    fn = "pa_copy_scales"
+    _check(fn, (), (block_mapping, err_flag), torch.int64, (block_mapping,))
+    for t in (src_k_scales, src_v_scales, dst_k_scales, dst_v_scales):
+        if t.dtype != torch.float32 or not t.is_contiguous() or \
+                (t.get_device() != block_mapping.get_device() and not t.is_pinned()):
+            raise PAError(fn, 2)
+    if src_k_scales.shape != src_v_scales.shape or dst_k_scales.shape != dst_v_scales.shape or \
+            src_k_scales.shape[1] != dst_k_scales.shape[1]:
+        raise PAError(fn, 2)
     src_blocks, Hkv = src_k_scales.shape
     with _on_device_of(dst_k_scales, src_k_scales):
         rc = LIB.pa_copy_scales(_ptr(dst_k_scales), _ptr(dst_v_scales), _ptr(src_k_scales),
@@ -630,7 +641,7 @@ def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
                                 Hkv, src_blocks, dst_k_scales.shape[0], _ptr(err_flag),
                                 _stream(stream))
     if rc:
-        raise PAError("pa_copy_scales", rc)
+        raise PAError(fn, rc)
 
 
 def pa_window_workspace_size(B: int, Hq: int, Hkv: int, D: int, max_context_len: int,
@@ -654,8 +665,8 @@ def pa_decode_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torch
                         err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """pa_decode_kv over the last `window` tokens and the first `num_sinks` ones (see
     pa_decode_window_kv in include/pa.h)."""
-    _check("pa_decode_window_kv", (), (out, query, key_cache, value_cache), torch.int32,
-           (block_tables, context_lens))
+    _check("pa_decode_window_kv", (), (out, query, key_cache, value_cache, workspace, err_flag),
+           torch.int32, (block_tables, context_lens))
     if key_cache.shape != value_cache.shape or out.shape != query.shape or \
             key_cache.shape[3] != query.shape[2] or \
             not block_tables.shape[0] == context_lens.shape[0] == query.shape[0]:
@@ -684,8 +695,8 @@ def pa_decode_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tens
     """Decode attention over pools of E4M3 codes with one power-of-two scale per block and KV
     head, k_scales / v_scales [num_blocks, Hkv]; window 0: every token (see pa_decode_blk8 in
     include/pa.h)."""
-    _check("pa_decode_blk8", (), (out, query, key_cache, value_cache), torch.int32,
-           (block_tables, context_lens))
+    _check("pa_decode_blk8", (), (out, query, key_cache, value_cache, workspace, err_flag),
+           torch.int32, (block_tables, context_lens))
     _check_scales("pa_decode_blk8", key_cache, k_scales, v_scales)
     if pa_dtype(key_cache) != PA_FP8_E4M3 or pa_dtype(value_cache) != PA_FP8_E4M3:
         raise PAError("pa_decode_blk8", 3)
@@ -715,8 +726,8 @@ def pa_prefill_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torc
                          err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """pa_prefill_kv over the last `window` tokens up to each query's and the first
     `num_sinks` ones (see pa_prefill_window_kv in include/pa.h)."""
-    _check("pa_prefill_window_kv", (), (out, query, key_cache, value_cache), torch.int32,
-           (block_tables, context_lens, query_start))
+    _check("pa_prefill_window_kv", (), (out, query, key_cache, value_cache, err_flag),
+           torch.int32, (block_tables, context_lens, query_start))
     if key_cache.shape != value_cache.shape or out.shape != query.shape or \
             key_cache.shape[3] != query.shape[2] or \
             not block_tables.shape[0] == context_lens.shape[0] == query_start.shape[0] - 1:
@@ -744,8 +755,8 @@ def pa_prefill_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Ten
                     err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """Paged prefill over the block-scaled 8-bit cache; window 0: every earlier token (see
     pa_prefill_blk8 in include/pa.h)."""
-    _check("pa_prefill_blk8", (), (out, query, key_cache, value_cache), torch.int32,
-           (block_tables, context_lens, query_start))
+    _check("pa_prefill_blk8", (), (out, query, key_cache, value_cache, err_flag),
+           torch.int32, (block_tables, context_lens, query_start))
     _check_scales("pa_prefill_blk8", key_cache, k_scales, v_scales)
     if pa_dtype(key_cache) != PA_FP8_E4M3 or pa_dtype(value_cache) != PA_FP8_E4M3:
         raise PAError("pa_prefill_blk8", 3)

@@ -178,6 +178,42 @@ def test_binding_refuses_wrong_types_and_sizes():
     refused(ops.pa_prefill_blk8, q, q, c8, kc, sc, sc, bt, cl, qs, 1, 0.1, 64)
     refused(ops.pa_copy_scales, sc, sc, sc, sc[:2], torch.zeros(1, 2, dtype=i64))
     refused(ops.pa_copy_scales, sc, sc, sc, sc, torch.zeros(1, 2, dtype=i32))
+    with pytest.raises(ops.PAError) as e:
+        ops.pa_rope_and_cache_kv(None, q, k, k, p, cs, kc, kc, 1.0, 1.0, p)
+    assert e.value.status == 1
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it lies on device 1."""
+
+    def get_device(self):
+        return 1
+
+
+def test_binding_refuses_tensors_of_another_device():
+    bf, i64, i32 = torch.bfloat16, torch.int64, torch.int32
+    kc = torch.zeros(4, 16, 2, 128, dtype=bf)
+    c8, sc = torch.zeros(4, 16, 2, 128, dtype=torch.uint8), torch.ones(4, 2)
+    q, k = torch.zeros(3, 8, 128, dtype=bf), torch.zeros(3, 2, 128, dtype=bf)
+    p, cs = torch.zeros(3, dtype=i64), torch.zeros(8, 128)
+    bt, cl, qs = torch.zeros(3, 4, dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(4, dtype=i32)
+    ws, err, pairs = torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1, dtype=i32), torch.zeros(1, 2, dtype=i64)
+    calls = [(ops.pa_rope_and_cache_kv, [q, q, k, k, p, cs, kc, kc, 1.0, 1.0, p, False, err]),
+             (ops.pa_rope_and_cache_blk8, [q, q, k, k, p, cs, c8, c8, sc, sc, p, False, err]),
+             (ops.pa_copy_scales, [sc, sc, sc, sc, pairs, err]),
+             (ops.pa_decode_window_kv, [q, q, kc, kc, 1.0, 1.0, bt, cl, 0.1, 5, 0, 64, ws, err]),
+             (ops.pa_decode_blk8, [q, q, c8, c8, sc, sc, bt, cl, 0.1, 64, 0, 0, ws, err]),
+             (ops.pa_prefill_window_kv, [q, q, kc, kc, 1.0, 1.0, bt, cl, qs, 1, 0.1, 5, 0, 64, err]),
+             (ops.pa_prefill_blk8, [q, q, c8, c8, sc, sc, bt, cl, qs, 1, 0.1, 64, 0, 0, err])]
+    for f, args in calls:
+        for i, x in enumerate(args):
+            if not isinstance(x, torch.Tensor):
+                continue
+            a = list(args)
+            a[i] = x.as_subclass(Elsewhere)
+            with pytest.raises(ops.PAError) as e:
+                f(*a)
+            assert e.value.status == 2, (f.__name__, i)
 
 
 def test_debug_check_of_block_runs():
