@@ -153,7 +153,7 @@ def _on_device_of(*tensors):
     for t in tensors:
         if t is not None and t.is_cuda:
             # the usual case costs one comparison instead of a switch and its undoing
-            return _SAME_DEVICE if t.get_device() == torch.cuda.current_device() \
+            return _SAME_DEVICE if t.get_device() == torch._C._cuda_getDevice() \
                 else torch.cuda.device(t.device)
     return _SAME_DEVICE
 
@@ -485,15 +485,11 @@ def workspace_for(query: torch.Tensor, key_cache: torch.Tensor, max_context_len:
     return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=query.device)
 
 
-def _check(fn: str, elements, dense, index, indices) -> None:
+def _check(fn: str, dense, index, indices) -> None:
     """The sizes and addresses of the entry points below are read off these tensors, so a
-    wrong one would be read past its end: one element type for `elements`, no gaps in
-    `dense` and `indices`, the integer type `index` for `indices`, and all of them on the
-    device of the first of `dense`."""
+    wrong one would be read past its end: no gaps in `dense` and `indices`, the integer type
+    `index` for `indices`, and all of them on the device of the first of `dense`."""
     device = dense[0].get_device()
-    for t in elements:
-        if t is not None and (t.dtype != elements[0].dtype or t.get_device() != device):
-            raise PAError(fn, 3 if t.get_device() == device else 2)
     for t in dense:
         if t is not None and (not t.is_contiguous() or t.get_device() != device):
             raise PAError(fn, 2)
@@ -503,23 +499,41 @@ def _check(fn: str, elements, dense, index, indices) -> None:
 
 
 def _check_scales(fn: str, cache: torch.Tensor, *scales) -> None:
+    shape, device = (cache.shape[0], cache.shape[2]), cache.get_device()
     for t in scales:
-        if t.dtype != torch.float32 or not t.is_contiguous() or \
-                t.get_device() != cache.get_device() or \
-                t.shape[0] != cache.shape[0] or t.shape[1] != cache.shape[2]:
+        if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous() or \
+                t.get_device() != device:
             raise PAError(fn, 2)
 
 
-def _token_stride(t: torch.Tensor, fn: str) -> int:
-    """Elements between tokens of a [T,H,D] tensor whose heads are dense (a slice of a
-    fused projection is; a transposed or expanded view is refused)."""
-    if t.dim() != 3:
+def _token_stride(t: torch.Tensor, shape: tuple, dtype, device: int, fn: str) -> int:
+    """Elements between tokens of a [T,H,D] tensor of this shape, type and device whose heads
+    are dense (a slice of a fused projection is; a transposed or expanded view is refused)."""
+    if t.shape != shape or t.get_device() != device:
         raise PAError(fn, 2)
-    T, H, D = t.shape
+    if t.dtype != dtype:
+        raise PAError(fn, 3)
     st, sh, sd = t.stride()
+    T, H, D = shape
     if sd != 1 or (H > 1 and sh != D):
         raise PAError(fn, 2)
     return st if T > 1 else max(st, H * D)
+
+
+def _append_sizes(query, query_out, slot_mapping, positions, cos_sin, fn: str):
+    """Tokens, query heads, and the sizes of the table of a rotary append (no table: 0, 0)."""
+    if (query is None) != (query_out is None):
+        raise PAError(fn, 1)
+    if slot_mapping.dim() != 1 or (query is not None and query.dim() != 3):
+        raise PAError(fn, 2)
+    T = slot_mapping.shape[0]
+    Hq = 0 if query is None else query.shape[1]
+    if cos_sin is None:
+        return T, Hq, 0, 0
+    if positions is None or positions.shape != (T,) or cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise PAError(fn, 2)
+    max_positions, rot_dim = cos_sin.shape
+    return T, Hq, max_positions, rot_dim
 
 
 def check_block_runs(slot_mapping: torch.Tensor, block_size: int,
@@ -549,27 +563,22 @@ def pa_rope_and_cache_kv(query_out: Optional[torch.Tensor], query: Optional[torc
     fn = "pa_rope_and_cache_kv"
     if DEBUG:
         check_slot_mapping(slot_mapping, fn)
-    _check(fn, (key, value, query, query_out), (key_cache, value_cache, cos_sin, err_flag),
-           torch.int64, (positions, slot_mapping))
-    if (query is None) != (query_out is None):
-        raise PAError(fn, 1)
-    if key_cache.shape != value_cache.shape or cos_sin.dtype != torch.float32 or \
-            key.shape != value.shape or key.shape[1:] != key_cache.shape[2:] or \
-            not key.shape[0] == slot_mapping.shape[0] == positions.shape[0] or \
-            (query is not None and (query.shape != query_out.shape or
-                                    query.shape[0] != key.shape[0] or query.shape[2] != key.shape[2])):
+    _check(fn, (key_cache, value_cache, cos_sin, err_flag), torch.int64, (positions, slot_mapping))
+    num_blocks, block_size, Hkv, D = shape = key_cache.shape
+    T, Hq, max_positions, rot_dim = _append_sizes(query, query_out, slot_mapping, positions, cos_sin, fn)
+    if value_cache.shape != shape:
         raise PAError(fn, 2)
-    num_blocks, block_size, Hkv, D = key_cache.shape
-    Hq = 0 if query is None else query.shape[1]
+    qs, kvs, dtype, device = (T, Hq, D), (T, Hkv, D), key.dtype, key_cache.get_device()
     with _on_device_of(key_cache):
         rc = LIB.pa_rope_and_cache_kv(
-            _ptr(query_out), 0 if query is None else _token_stride(query_out, fn), _ptr(query),
-            0 if query is None else _token_stride(query, fn), _ptr(key), _token_stride(key, fn),
-            _ptr(value), _token_stride(value, fn), pa_dtype(key), _ptr(positions), _ptr(cos_sin),
-            cos_sin.shape[0], cos_sin.shape[1], int(interleaved), _ptr(key_cache),
-            pa_dtype(key_cache), float(k_scale), _ptr(value_cache), pa_dtype(value_cache),
-            float(v_scale), _ptr(slot_mapping), slot_mapping.shape[0], Hq, Hkv, D, block_size,
-            num_blocks, _ptr(err_flag), _stream(stream))
+            _ptr(query_out), _token_stride(query_out, qs, dtype, device, fn) if Hq else 0,
+            _ptr(query), _token_stride(query, qs, dtype, device, fn) if Hq else 0, key.data_ptr(),
+            _token_stride(key, kvs, dtype, device, fn), value.data_ptr(),
+            _token_stride(value, kvs, dtype, device, fn), pa_dtype(key), _ptr(positions),
+            _ptr(cos_sin), max_positions, rot_dim, bool(interleaved), key_cache.data_ptr(),
+            pa_dtype(key_cache), float(k_scale), value_cache.data_ptr(), pa_dtype(value_cache),
+            float(v_scale), slot_mapping.data_ptr(), T, Hq, Hkv, D, block_size, num_blocks,
+            _ptr(err_flag), _stream(stream))
     if rc:
         raise PAError(fn, rc)
 
@@ -585,33 +594,26 @@ def pa_rope_and_cache_blk8(query_out: Optional[torch.Tensor], query: Optional[to
     and KV head, k_scales / v_scales [num_blocks, Hkv] (see pa_rope_and_cache_blk8 in
     include/pa.h). cos_sin None (with query and positions None): no rotation."""
     fn = "pa_rope_and_cache_blk8"
-    _check(fn, (key, value, query, query_out), (key_cache, value_cache, cos_sin, err_flag),
-           torch.int64, (positions, slot_mapping))
-    if (query is None) != (query_out is None):
-        raise PAError(fn, 1)
+    _check(fn, (key_cache, value_cache, cos_sin, err_flag), torch.int64, (positions, slot_mapping))
     _check_scales(fn, key_cache, k_scales, v_scales)
-    if key_cache.shape != value_cache.shape or pa_dtype(key_cache) != PA_FP8_E4M3 or \
-            pa_dtype(value_cache) != PA_FP8_E4M3 or key.shape != value.shape or \
-            key.shape[1:] != key_cache.shape[2:] or key.shape[0] != slot_mapping.shape[0] or \
-            (cos_sin is not None and (cos_sin.dtype != torch.float32 or positions is None or
-                                      positions.shape[0] != key.shape[0])) or \
-            (query is not None and (query.shape != query_out.shape or
-                                    query.shape[0] != key.shape[0] or query.shape[2] != key.shape[2])):
+    num_blocks, block_size, Hkv, D = shape = key_cache.shape
+    T, Hq, max_positions, rot_dim = _append_sizes(query, query_out, slot_mapping, positions, cos_sin, fn)
+    if value_cache.shape != shape or pa_dtype(key_cache) != PA_FP8_E4M3 or \
+            pa_dtype(value_cache) != PA_FP8_E4M3:
         raise PAError(fn, 2)
-    num_blocks, block_size, Hkv, D = key_cache.shape
     if DEBUG:
         check_slot_mapping(slot_mapping, fn)
         check_block_runs(slot_mapping, block_size, fn)
-    Hq = 0 if query is None else query.shape[1]
+    qs, kvs, dtype, device = (T, Hq, D), (T, Hkv, D), key.dtype, key_cache.get_device()
     with _on_device_of(key_cache):
         rc = LIB.pa_rope_and_cache_blk8(
-            _ptr(query_out), 0 if query is None else _token_stride(query_out, fn), _ptr(query),
-            0 if query is None else _token_stride(query, fn), _ptr(key), _token_stride(key, fn),
-            _ptr(value), _token_stride(value, fn), pa_dtype(key), _ptr(positions), _ptr(cos_sin),
-            0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
-            int(interleaved), _ptr(key_cache), _ptr(value_cache), _ptr(k_scales), _ptr(v_scales),
-            _ptr(slot_mapping), slot_mapping.shape[0], Hq, Hkv, D, block_size, num_blocks,
-            _ptr(err_flag), _stream(stream))
+            _ptr(query_out), _token_stride(query_out, qs, dtype, device, fn) if Hq else 0,
+            _ptr(query), _token_stride(query, qs, dtype, device, fn) if Hq else 0, key.data_ptr(),
+            _token_stride(key, kvs, dtype, device, fn), value.data_ptr(),
+            _token_stride(value, kvs, dtype, device, fn), pa_dtype(key), _ptr(positions), _ptr(cos_sin),
+            max_positions, rot_dim, bool(interleaved), key_cache.data_ptr(), value_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D,
+            block_size, num_blocks, _ptr(err_flag), _stream(stream))
     if rc:
         raise PAError(fn, rc)
 
@@ -626,7 +628,7 @@ def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
         check_block_mapping(block_mapping, "pa_copy_scales",
                             same_pool=dst_k_scales.data_ptr() == src_k_scales.data_ptr())
     fn = "pa_copy_scales"
-    _check(fn, (), (block_mapping, err_flag), torch.int64, (block_mapping,))
+    _check(fn, (block_mapping, err_flag), torch.int64, (block_mapping,))
     for t in (src_k_scales, src_v_scales, dst_k_scales, dst_v_scales):
         if t.dtype != torch.float32 or not t.is_contiguous() or \
                 (t.get_device() != block_mapping.get_device() and not t.is_pinned()):
@@ -665,22 +667,22 @@ def pa_decode_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torch
                         err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """pa_decode_kv over the last `window` tokens and the first `num_sinks` ones (see
     pa_decode_window_kv in include/pa.h)."""
-    _check("pa_decode_window_kv", (), (out, query, key_cache, value_cache, workspace, err_flag),
+    _check("pa_decode_window_kv", (out, query, key_cache, value_cache, workspace, err_flag),
            torch.int32, (block_tables, context_lens))
-    if key_cache.shape != value_cache.shape or out.shape != query.shape or \
-            key_cache.shape[3] != query.shape[2] or \
-            not block_tables.shape[0] == context_lens.shape[0] == query.shape[0]:
+    B, Hq, D = shape = query.shape
+    num_blocks, block_size, Hkv, head_size = pool = key_cache.shape
+    rows, max_blocks = block_tables.shape
+    if value_cache.shape != pool or out.shape != shape or head_size != D or rows != B or \
+            context_lens.shape != (B,):
         raise PAError("pa_decode_window_kv", 2)
-    B, Hq, D = query.shape
-    num_blocks, block_size, Hkv, _ = key_cache.shape
     with _on_device_of(query):
         rc = LIB.pa_decode_window_kv(
-            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
-            pa_dtype(key_cache), float(k_scale), _ptr(value_cache), pa_dtype(value_cache),
-            float(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, Hq,
+            out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
+            pa_dtype(key_cache), float(k_scale), value_cache.data_ptr(), pa_dtype(value_cache),
+            float(v_scale), block_tables.data_ptr(), max_blocks, context_lens.data_ptr(), B, Hq,
             Hkv, D, block_size, num_blocks, float(scale), int(window), int(num_sinks),
             int(max_context_len), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            0 if workspace is None else workspace.nbytes,
             _ptr(err_flag), _stream(stream))
     if rc:
         raise PAError("pa_decode_window_kv", rc)
@@ -695,24 +697,24 @@ def pa_decode_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tens
     """Decode attention over pools of E4M3 codes with one power-of-two scale per block and KV
     head, k_scales / v_scales [num_blocks, Hkv]; window 0: every token (see pa_decode_blk8 in
     include/pa.h)."""
-    _check("pa_decode_blk8", (), (out, query, key_cache, value_cache, workspace, err_flag),
+    _check("pa_decode_blk8", (out, query, key_cache, value_cache, workspace, err_flag),
            torch.int32, (block_tables, context_lens))
     _check_scales("pa_decode_blk8", key_cache, k_scales, v_scales)
     if pa_dtype(key_cache) != PA_FP8_E4M3 or pa_dtype(value_cache) != PA_FP8_E4M3:
         raise PAError("pa_decode_blk8", 3)
-    if key_cache.shape != value_cache.shape or out.shape != query.shape or \
-            key_cache.shape[3] != query.shape[2] or \
-            not block_tables.shape[0] == context_lens.shape[0] == query.shape[0]:
+    B, Hq, D = shape = query.shape
+    num_blocks, block_size, Hkv, head_size = pool = key_cache.shape
+    rows, max_blocks = block_tables.shape
+    if value_cache.shape != pool or out.shape != shape or head_size != D or rows != B or \
+            context_lens.shape != (B,):
         raise PAError("pa_decode_blk8", 2)
-    B, Hq, D = query.shape
-    num_blocks, block_size, Hkv, _ = key_cache.shape
     with _on_device_of(query):
         rc = LIB.pa_decode_blk8(
-            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
-            _ptr(value_cache), _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
-            block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, block_size, num_blocks,
+            out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
+            value_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            max_blocks, context_lens.data_ptr(), B, Hq, Hkv, D, block_size, num_blocks,
             float(scale), int(window), int(num_sinks), int(max_context_len), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            0 if workspace is None else workspace.nbytes,
             _ptr(err_flag), _stream(stream))
     if rc:
         raise PAError("pa_decode_blk8", rc)
@@ -726,21 +728,20 @@ def pa_prefill_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torc
                          err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """pa_prefill_kv over the last `window` tokens up to each query's and the first
     `num_sinks` ones (see pa_prefill_window_kv in include/pa.h)."""
-    _check("pa_prefill_window_kv", (), (out, query, key_cache, value_cache, err_flag),
+    _check("pa_prefill_window_kv", (out, query, key_cache, value_cache, err_flag),
            torch.int32, (block_tables, context_lens, query_start))
-    if key_cache.shape != value_cache.shape or out.shape != query.shape or \
-            key_cache.shape[3] != query.shape[2] or \
-            not block_tables.shape[0] == context_lens.shape[0] == query_start.shape[0] - 1:
+    T, Hq, D = shape = query.shape
+    num_blocks, block_size, Hkv, head_size = pool = key_cache.shape
+    B, max_blocks = block_tables.shape
+    if value_cache.shape != pool or out.shape != shape or head_size != D or \
+            context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_window_kv", 2)
-    T, Hq, D = query.shape
-    num_blocks, block_size, Hkv, _ = key_cache.shape
-    B = query_start.shape[0] - 1
     with _on_device_of(query):
         rc = LIB.pa_prefill_window_kv(
-            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
-            pa_dtype(key_cache), float(k_scale), _ptr(value_cache), pa_dtype(value_cache),
-            float(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-            _ptr(query_start), B, T, int(max_query_len), Hq, Hkv, D, block_size, num_blocks,
+            out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
+            pa_dtype(key_cache), float(k_scale), value_cache.data_ptr(), pa_dtype(value_cache),
+            float(v_scale), block_tables.data_ptr(), max_blocks, context_lens.data_ptr(),
+            query_start.data_ptr(), B, T, int(max_query_len), Hq, Hkv, D, block_size, num_blocks,
             float(scale), int(window), int(num_sinks), int(max_context_len), _ptr(err_flag),
             _stream(stream))
     if rc:
@@ -755,23 +756,22 @@ def pa_prefill_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Ten
                     err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """Paged prefill over the block-scaled 8-bit cache; window 0: every earlier token (see
     pa_prefill_blk8 in include/pa.h)."""
-    _check("pa_prefill_blk8", (), (out, query, key_cache, value_cache, err_flag),
+    _check("pa_prefill_blk8", (out, query, key_cache, value_cache, err_flag),
            torch.int32, (block_tables, context_lens, query_start))
     _check_scales("pa_prefill_blk8", key_cache, k_scales, v_scales)
     if pa_dtype(key_cache) != PA_FP8_E4M3 or pa_dtype(value_cache) != PA_FP8_E4M3:
         raise PAError("pa_prefill_blk8", 3)
-    if key_cache.shape != value_cache.shape or out.shape != query.shape or \
-            key_cache.shape[3] != query.shape[2] or \
-            not block_tables.shape[0] == context_lens.shape[0] == query_start.shape[0] - 1:
+    T, Hq, D = shape = query.shape
+    num_blocks, block_size, Hkv, head_size = pool = key_cache.shape
+    B, max_blocks = block_tables.shape
+    if value_cache.shape != pool or out.shape != shape or head_size != D or \
+            context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_blk8", 2)
-    T, Hq, D = query.shape
-    num_blocks, block_size, Hkv, _ = key_cache.shape
-    B = query_start.shape[0] - 1
     with _on_device_of(query):
         rc = LIB.pa_prefill_blk8(
-            _ptr(out), pa_dtype(out), _ptr(query), pa_dtype(query), _ptr(key_cache),
-            _ptr(value_cache), _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
-            block_tables.shape[1], _ptr(context_lens), _ptr(query_start), B, T,
+            out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
+            value_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            max_blocks, context_lens.data_ptr(), query_start.data_ptr(), B, T,
             int(max_query_len), Hq, Hkv, D, block_size, num_blocks, float(scale), int(window),
             int(num_sinks), int(max_context_len), _ptr(err_flag), _stream(stream))
     if rc:
