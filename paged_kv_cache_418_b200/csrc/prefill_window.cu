@@ -62,20 +62,21 @@ namespace {
 using namespace tc;
 
 constexpr int kD = 128;
-constexpr int kM = 128;                         // query rows per unit
+constexpr int kM = 128;                         // rows of a query tile, two of which make a unit
 constexpr int kTile = 128;                      // keys per tile
 constexpr int kHalf = 128 * 128;                // one 64-wide d-half of a 128-row operand
 constexpr int kOp = 2 * kHalf;                  // one 128 x 128 16-bit operand: 32 KB
-constexpr int kNST = 5;                         // K / V ring stages (odd: a stage serves K and V in turn)
-constexpr int kTmemCols = 512;                  // S/P x2 (by tile), O x2 (by unit)
+constexpr int kNST = 4;                         // ring stages: K in the even ones, V in the odd ones
+constexpr int kNQ = 3;                          // query tiles in shared memory
+constexpr int kTmemCols = 512;                  // S/P x2, O x2 (by query tile of the unit)
 constexpr int kSlots = 4;                       // tiles of scales and masks (see the producer)
 
-constexpr int OFF_Q = 0;                        // [2 units][32 KB]
-constexpr int OFF_KV = 2 * kOp;                 // [kNST][32 KB]
+constexpr int OFF_Q = 0;                        // [kNQ][32 KB]
+constexpr int OFF_KV = kNQ * kOp;               // [kNST][32 KB]
 constexpr int OFF_BAR = OFF_KV + kNST * kOp;
-enum { B_FULL = 0, B_EMPTY = kNST, B_CONV = 2 * kNST, B_QFULL = 3 * kNST, B_QEMPTY = B_QFULL + 2,
-       B_QCONV = B_QEMPTY + 2, B_SFULL = B_QCONV + 2, B_PREADY = B_SFULL + 2, B_OSTEP = B_PREADY + 2,
-       B_ODONE = B_OSTEP + 2, B_DONE = B_ODONE + 2, B_COUNT = B_DONE + 1 };
+enum { B_FULL = 0, B_EMPTY = kNST, B_CONV = 2 * kNST, B_QFULL = 3 * kNST, B_QEMPTY = B_QFULL + kNQ,
+       B_QCONV = B_QEMPTY + kNQ, B_SFULL = B_QCONV + kNQ, B_PREADY = B_SFULL + 4, B_OSTEP = B_PREADY + 4,
+       B_OFULL = B_OSTEP + 2, B_ODONE = B_OFULL + 2, B_DONE = B_ODONE + 2, B_COUNT = B_DONE + 1 };
 constexpr int OFF_MISC = OFF_BAR + 8 * B_COUNT;
 constexpr int OFF_SLOT = (OFF_MISC + 8 + 15) / 16 * 16;
 struct Slot {                                   // of a tile: what the producer knows of its blocks
@@ -83,9 +84,8 @@ struct Slot {                                   // of a tile: what the producer 
   uint32_t missing;                             // blocks that were not loaded
   uint32_t pad[3];
 };
-constexpr int OFF_XCH = OFF_SLOT + kSlots * (int)sizeof(Slot);   // [2 halves][128 rows] maxima, then sums
-constexpr int OFF_ROWE = OFF_XCH + 2 * 128 * 4;                  // [2 units][128] exponents of rescaled rows
-constexpr int kSmem = OFF_ROWE + 2 * 128 + 1024;                 // + alignment slack
+constexpr int OFF_ROWE = OFF_SLOT + kSlots * (int)sizeof(Slot);  // [kNQ][128] exponents of rescaled rows
+constexpr int kSmem = OFF_ROWE + kNQ * 128 + 1024;               // + alignment slack
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 struct Args {
@@ -105,23 +105,39 @@ struct Args {
   const float* v_scales;
 };
 
+// Some rows attend keys t < t1 with t >= lo or t < sk.
+struct Reach {
+  int t1, lo, sk;
+  // some of the n keys from t on are attended
+  __device__ __forceinline__ bool needs(int t, int n) const { return t < t1 && (t + n > lo || t < sk); }
+};
+// ntok new tokens from position pos on
+__device__ __forceinline__ Reach reach_of(const Args& a, int pos, int ntok) {
+  Reach x;
+  x.t1 = ntok > 0 ? pos + ntok : 0;
+  x.lo = a.window > 0 && ntok > 0 ? max(0, pos - a.window + 1) : 0;
+  x.sk = min(a.sinks, x.lo);
+  return x;
+}
+
 struct Unit {
   int b, c, h;
   int qrow0;            // first query row (token) of the chunk in [T]
   int ntok;             // new tokens of the chunk (0: nothing to do)
   int pos0;             // position of the chunk's first token
-  int t1;               // some row attends keys t < t1 with t >= lo or t < sk;
-  int lo, sk;           // their tiles are the first n0 and those from w0 on
+  int tpt;              // tokens of a query tile
+  Reach all;            // of the chunk; its tiles are the first n0 and those from w0 on
   int n0, w0, ntiles;
   bool bad;             // the sequence's lengths are inconsistent
   __device__ __forceinline__ int tile0(int k) const { return (k < n0 ? k : k - n0 + w0) * kTile; }
-  // a row attends some of the n keys from t on
-  __device__ __forceinline__ bool needs(int t, int n) const { return t < t1 && (t + n > lo || t < sk); }
+  __device__ __forceinline__ int tokens(int g) const { return min(tpt, ntok - g * tpt); }   // of query tile g
+  __device__ __forceinline__ int pos(int g) const { return pos0 + g * tpt; }
+  __device__ __forceinline__ bool two() const { return ntok > tpt; }
 };
 
 __device__ __forceinline__ Unit unit_of(const Args& a, int G, int bs, long long u) {
-  const int tpu = kM / G;
   Unit x;
+  x.tpt = kM / G;
   x.h = (int)(u % a.Hkv);
   const long long t = u / a.Hkv;
   x.b = (int)(t % a.B);
@@ -129,22 +145,29 @@ __device__ __forceinline__ Unit unit_of(const Args& a, int G, int bs, long long 
   const int qs = __ldg(a.query_start + x.b), qe = __ldg(a.query_start + x.b + 1);
   const int n = qe - qs, ctx = __ldg(a.context_lens + x.b);
   x.bad = qs < 0 || n < 0 || qe > a.T || ctx < n || ctx > (long long)a.max_blocks * bs || ctx > a.max_context_len;
-  const long long done = (long long)x.c * tpu;  // the sequence's new tokens before the chunk
-  x.ntok = x.bad ? 0 : (int)max(0ll, min((long long)tpu, n - done));
+  const long long done = (long long)x.c * 2 * x.tpt;    // the sequence's new tokens before the chunk
+  x.ntok = x.bad ? 0 : (int)max(0ll, min(2ll * x.tpt, n - done));
   x.qrow0 = (int)(qs + done);
   x.pos0 = (int)(ctx - n + done);
-  x.t1 = x.ntok > 0 ? x.pos0 + x.ntok : 0;
-  x.lo = a.window > 0 && x.ntok > 0 ? max(0, x.pos0 - a.window + 1) : 0;
-  x.sk = min(a.sinks, x.lo);
-  x.w0 = x.lo / kTile;
-  x.n0 = min((x.sk + kTile - 1) / kTile, x.w0);
-  x.ntiles = x.n0 + (x.t1 + kTile - 1) / kTile - x.w0;
+  x.all = reach_of(a, x.pos0, x.ntok);
+  x.w0 = x.all.lo / kTile;
+  x.n0 = min((x.all.sk + kTile - 1) / kTile, x.w0);
+  x.ntiles = x.n0 + (x.all.t1 + kTile - 1) / kTile - x.w0;
   return x;
 }
 
 // The k-th unit of CTA cta: rounds of grid units in alternating directions.
 __device__ __forceinline__ long long unit_index(long long k, int cta, int grid) {
   return k * grid + ((k & 1) ? grid - 1 - cta : cta);
+}
+
+// One lane of the (converged) warp. Not lane == 0: only elect.sync tells the compiler
+// that a single thread goes on, so that the operands of the tensor instructions need no
+// loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -245,20 +268,15 @@ __device__ __forceinline__ int rescale_row(uint8_t* op, int row) {
 // Wait for this thread's tensor-memory loads, the 64 registers of which are not to be
 // used before.
 __device__ __forceinline__ void tmem_wait_ld64(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
-                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
-               :: "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 28; i < 64; i += 4)
+  for (int i = 0; i < 64; i += 4)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])::"memory");
 }
 
-// Warps of the CTA and their registers. Without converters: 12 warps (two idle), 168
-// registers each. With them: 16 warps launched with 128, moved between warpgroups:
-// 256 * 160 + 128 * 104 + 128 * 88 = 65,536 = 512 * 128.
+// Warps of the CTA and their registers, moved between warpgroups: without converters
+// 384 threads are launched with 168 each: 256 * 208 + 128 * 88 = 64,512; with them 512
+// with 128: 256 * 184 + 128 * 80 + 128 * 64 = 65,536.
 template <bool CONV> struct Roles {
   static constexpr int kConv = 8, kProd = CONV ? 12 : 8, kMma = kProd + 1, kThreads = CONV ? 512 : 384;
 };
@@ -282,7 +300,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   using R = Roles<CONV>;
   constexpr int NB_T = kTile / BS;              // physical blocks per tile
   constexpr uint32_t kBlkBits = (uint32_t)((1ull << BS) - 1ull);   // one block's keys in a chunk mask
-  constexpr uint32_t IDESC_S = make_idesc(FS, 0, 0, kTile, kM);
+  constexpr uint32_t IDESC_S = make_idesc(FS, 0, 0, kTile / 2, kM);
   constexpr uint32_t IDESC_O = make_idesc(FO, 0, 1, kD, kM);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -293,7 +311,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + OFF_MISC + 4);
   Slot* slots = reinterpret_cast<Slot*>(smem + OFF_SLOT);
   int8_t* rowe = reinterpret_cast<int8_t*>(smem + OFF_ROWE);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv;
   const long long U = (long long)a.B * a.chunks * a.Hkv;
   pdl_trigger();
@@ -304,14 +322,19 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       mbar_init(bar(B_EMPTY + s), 1);
       mbar_init(bar(B_CONV + s), 128);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kNQ; ++i) {
       mbar_init(bar(B_QFULL + i), 1);
-      mbar_init(bar(B_QEMPTY + i), QC ? 257 : 1);      // (the softmax threads read the rows' exponents)
+      mbar_init(bar(B_QEMPTY + i), QC ? 129 : 1);      // (the softmax threads read the rows' exponents)
       mbar_init(bar(B_QCONV + i), 128);
-      mbar_init(bar(B_SFULL + i), 1);
-      mbar_init(bar(B_PREADY + i), 256);
+    }
+    for (int i = 0; i < 2; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(B_SFULL + 2 * i + h), 1);
+        mbar_init(bar(B_PREADY + 2 * i + h), 128);
+      }
       mbar_init(bar(B_OSTEP + i), 1);
-      mbar_init(bar(B_ODONE + i), 256);
+      mbar_init(bar(B_OFULL + i), 1);
+      mbar_init(bar(B_ODONE + i), 128);
     }
     mbar_init(bar(B_DONE), 1);
     *abort_flag = 0u;
@@ -336,26 +359,20 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
     flag_error(a.err_flag, PA_DEV_TIMEOUT);
   };
   // a stage holding K (kv = 0) or V (kv = 1) is ready for the tensor cores when TMA
-  // filled it (16-bit pool) or when the converters widened it. FULL completes a phase
-  // on every use of the stage, and so does CONV when both pools hold codes; with one
-  // such pool only its uses are widened, every other one (kNST is odd, so a stage's
-  // uses alternate K and V).
+  // filled it (16-bit pool) or when the converters widened it
   auto ready_bar = [&](int kv, int s) { return bar(((kv ? V8 : K8) ? B_CONV : B_FULL) + s); };
-  auto ready_parity = [&](int kv, int seq) -> uint32_t {
-    const int u = seq / kNST;
-    return (uint32_t)(((kv ? V8 : K8) && K8 != V8) ? u >> 1 : u) & 1u;
-  };
 
   if (warp >= R::kProd) {
-    if constexpr (CONV) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (CONV) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == R::kProd) {
       // ---------------------------------------------------------- producer
       // The lanes share a tile's copies: lane q < NB_T has its q-th block, reads its id
       // two tiles ahead and its scales one ahead. It writes a tile's slot once it has the
-      // tile's K stage, that is after the product P . V of the tile three before it: every
-      // softmax and converter thread is past that tile's slot, so four slots are enough.
-      int tc_ = 0, issued = 0, ui = 0;
-      int q_last[2] = {-1, -1};
+      // tile's K stage, that is after the scores of the tile two before it and the output
+      // products of the one before that: every softmax and converter thread is past the
+      // slot of the tile four before, so four slots are enough.
+      int tc_ = 0, issued = 0, qn = 0;
       bool stop = false;
       for (long long kk = 0; !stop; ++kk) {
         const long long u = unit_index(kk, blockIdx.x, gridDim.x);
@@ -363,22 +380,28 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         const Unit x = unit_of(a, G, BS, u);
         if (lane == 0 && x.bad && x.c == 0 && x.h == 0) flag_error(a.err_flag, PA_DEV_BAD_CTX);
         if (x.ntok <= 0) continue;
-        const int qi = ui & 1;
-        bool ok = true;
-        if (lane == 0) {
-          ok = mbar_wait(bar(B_QEMPTY + qi), ((ui >> 1) & 1) ^ 1, abort_flag);
-          if (ok) {
-            mbar_expect_tx(bar(B_QFULL + qi), (uint32_t)kOp);
-            for (int hh = 0; hh < 2; ++hh)
-              tma_load_4d(sbase + OFF_Q + qi * kOp + hh * kHalf, &tmQ, 0, hh, x.h * G, x.qrow0,
-                          bar(B_QFULL + qi));
-            q_last[qi] = ui;
+        // query tile g: the first one ahead of the unit's tiles, the second behind the first
+        // of them (its buffer is that of the last unit's first query tile)
+        auto load_q = [&](int g) -> bool {
+          const int qi = qn % kNQ;
+          bool ok = true;
+          if (lane == 0) {
+            ok = mbar_wait(bar(B_QEMPTY + qi), ((qn / kNQ) & 1) ^ 1, abort_flag);
+            if (ok) {
+              mbar_expect_tx(bar(B_QFULL + qi), (uint32_t)kOp);
+              for (int hh = 0; hh < 2; ++hh)
+                tma_load_4d(sbase + OFF_Q + qi * kOp + hh * kHalf, &tmQ, 0, hh, x.h * G, x.qrow0 + g * x.tpt,
+                            bar(B_QFULL + qi));
+            }
           }
-        }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) { stop = true; break; }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (ok) ++qn;
+          return ok;
+        };
+        if (!load_q(0)) { stop = true; break; }
         const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
         // this lane's block of tile k is one some row attends; its id (-1: none)
-        auto wants = [&](int k) { return lane < NB_T && x.needs(x.tile0(k) + lane * BS, BS); };
+        auto wants = [&](int k) { return lane < NB_T && x.all.needs(x.tile0(k) + lane * BS, BS); };
         auto fetch = [&](int k) -> int {
           return k < x.ntiles && wants(k) ? __ldg(table + x.tile0(k) / BS + lane) : -1;
         };
@@ -439,8 +462,8 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             }
             ++issued;
           }
+          if (k == 0 && !stop && x.two() && !load_q(1)) stop = true;
         }
-        ++ui;
       }
       if (lane == 0) {
         if (stop) give_up();
@@ -449,37 +472,43 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           const uint64_t t0 = globaltimer();
           while (!mbar_try(bar(B_FULL + seq % kNST), (seq / kNST) & 1) && globaltimer() - t0 < kWaitNs) {}
         }
-        for (int qb = 0; qb < 2; ++qb) {
-          if (q_last[qb] < 0) continue;
+        for (int q = max(0, qn - kNQ); q < qn; ++q) {
           const uint64_t t0 = globaltimer();
-          while (!mbar_try(bar(B_QFULL + qb), (q_last[qb] >> 1) & 1) && globaltimer() - t0 < kWaitNs) {}
+          while (!mbar_try(bar(B_QFULL + q % kNQ), (q / kNQ) & 1) && globaltimer() - t0 < kWaitNs) {}
         }
       }
-    } else if (warp == R::kMma && lane == 0) {
+    } else if (warp == R::kMma && elect_one()) {
       // ---------------------------------------------------------- MMA issuer
-      int tc_ = 0, ui = 0;
+      // Per key tile, half of its keys and query tile g: the output product of the half of
+      // g's last key tile, then g's scores of this one (over the weights that product has
+      // read: the tensor pipe is in order). So scores are ready half a tile ahead of the
+      // softmax.
+      int tc_ = 0, qn = 0;                       // key tiles, query tiles so far
+      int tiles[2] = {0, 0}, units[2] = {0, 0};  // of query tile g
       bool ok = true;
-      // output product of tile tt (the unit's first if first) into O buffer ob
-      auto issue_pv = [&](int tt, bool first, int ob) -> bool {
-        const int pb = tt & 1;
-        if (!mbar_wait(bar(B_PREADY + pb), (tt >> 1) & 1, abort_flag)) return false;
-        // the O buffer was last used by unit ui - 2: wait for its epilogue
-        if (first && ui >= 2 && !mbar_wait(bar(B_ODONE + ob), ((ui - 2) >> 1) & 1, abort_flag)) return false;
+      // output product of query tile g with half h of key tile tt, its n-th (the unit's
+      // first if first)
+      auto issue_pv = [&](int g, int h, int tt, int n, bool first) -> bool {
+        if (!mbar_wait(bar(B_PREADY + 2 * g + h), n & 1, abort_flag)) return false;
         const int seq = 2 * tt + 1, s = seq % kNST;
-        if (!mbar_wait(ready_bar(1, s), ready_parity(1, seq), abort_flag)) return false;
+        if (h == 0) {
+          // O is that of the last unit until its epilogue has read it
+          if (first && units[g] > 0 && !mbar_wait(bar(B_ODONE + g), (units[g] - 1) & 1, abort_flag)) return false;
+          if (!mbar_wait(ready_bar(1, s), (seq / kNST) & 1, abort_flag)) return false;
+        }
         tc_fence_after();
-        const uint32_t vst = sbase + OFF_KV + s * kOp;
+        const uint32_t vst = sbase + OFF_KV + s * kOp + h * (kTile / 2) * 128;
 #pragma unroll
         for (int part = 0; part < (LO ? 2 : 1); ++part) {
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk) {
+          for (int kk = 0; kk < kTile / 32; ++kk) {
             const uint64_t bd = sw128_desc(vst + kk * 16 * 128, kHalf, 1024);
-            mma_f16_ta(tmem_o + ob * kD, tmem_s + pb * kTile + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, bd,
-                       IDESC_O, (first && part == 0 && kk == 0) ? 0u : 1u);
+            mma_f16_ta(tmem_o + g * kD,
+                       tmem_s + g * kTile + h * (kTile / 2) + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, bd,
+                       IDESC_O, (first && h == 0 && part == 0 && kk == 0) ? 0u : 1u);
           }
         }
-        mma_commit(bar(B_EMPTY + s));
-        mma_commit(bar(B_OSTEP + pb));
+        if (h == 0) mma_commit(bar(B_OSTEP + g));
         return true;
       };
       for (long long kk = 0; ok; ++kk) {
@@ -487,28 +516,59 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         if (u >= U) break;
         const Unit x = unit_of(a, G, BS, u);
         if (x.ntok <= 0) continue;
-        const int qi = ui & 1, ob = ui & 1;
-        if (!mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), (ui >> 1) & 1, abort_flag)) { ok = false; break; }
-        const uint32_t qst = sbase + OFF_Q + qi * kOp;
-        for (int k = 0; k < x.ntiles; ++k, ++tc_) {
-          const int sb = tc_ & 1;
-          const int seq = 2 * tc_, s = seq % kNST;
-          if (!mbar_wait(ready_bar(0, s), ready_parity(0, seq), abort_flag)) { ok = false; break; }
-          tc_fence_after();
+        const int parts = x.two() ? 2 : 1;
+        const Reach reach[2] = {reach_of(a, x.pos(0), x.tokens(0)), reach_of(a, x.pos(1), x.tokens(1))};
+        int done[2] = {0, 0};                    // tiles whose scores were issued, of this unit
+        bool was[2], pend[2] = {false, false};   // the last tile, this tile is one of g's
+        for (int k = 0; k <= x.ntiles && ok; ++k) {
+          const int t0 = k < x.ntiles ? x.tile0(k) : 0;
+          const int seq = 2 * (tc_ + k), s = seq % kNST;
           const uint32_t kst = sbase + OFF_KV + s * kOp;
 #pragma unroll
-          for (int ks = 0; ks < kD / 16; ++ks) {
-            const uint64_t ad = sw128_desc(qst + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024);
-            const uint64_t bd = sw128_desc(kst + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024);
-            mma_f16(tmem_s + sb * kTile, ad, bd, IDESC_S, ks > 0 ? 1u : 0u);
+          for (int g = 0; g < 2; ++g) {
+            was[g] = pend[g];
+            pend[g] = g < parts && k < x.ntiles && reach[g].needs(t0, kTile);
           }
-          mma_commit(bar(B_EMPTY + s));
-          mma_commit(bar(B_SFULL + sb));
-          if (k == x.ntiles - 1) mma_commit(bar(B_QEMPTY + qi));
-          if (k > 0 && !issue_pv(tc_ - 1, k == 1, ob)) { ok = false; break; }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (was[g] && ok)
+                ok = issue_pv(g, h, tc_ + k - 1, tiles[g] - 1 - (h == 1 && pend[g]), done[g] - (h == 1 && pend[g]) == 1);
+              // (a query tile's key tiles lie in two runs, sinks and window: was its last one)
+              if (ok && h == 1 && was[g] && !pend[g] && (k == x.ntiles || t0 >= reach[g].t1)) {
+                mma_commit(bar(B_OFULL + g));
+                ++units[g];
+              }
+              if (pend[g] && ok) {
+                const int qi = (qn + g) % kNQ;
+                if (h == 0) {
+                  if (done[g] == 0)
+                    ok = mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), ((qn + g) / kNQ) & 1, abort_flag);
+                  ok = ok && mbar_wait(ready_bar(0, s), (seq / kNST) & 1, abort_flag);
+                  ++done[g];
+                  ++tiles[g];
+                }
+                if (ok) {
+                  tc_fence_after();
+                  const uint32_t qst = sbase + OFF_Q + qi * kOp;
+#pragma unroll
+                  for (int ks = 0; ks < kD / 16; ++ks) {
+                    const uint64_t ad = sw128_desc(qst + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024);
+                    const uint64_t bd = sw128_desc(kst + (ks >> 2) * kHalf + h * (kTile / 2) * 128 + (ks & 3) * 32, 16, 1024);
+                    mma_f16(tmem_s + g * kTile + h * (kTile / 2), ad, bd, IDESC_S, ks > 0 ? 1u : 0u);
+                  }
+                  mma_commit(bar(B_SFULL + 2 * g + h));
+                  if (h == 1 && t0 + kTile >= reach[g].t1) mma_commit(bar(B_QEMPTY + qi));
+                }
+              }
+            }
+          }
+          if (ok && k > 0) mma_commit(bar(B_EMPTY + (seq - 1) % kNST));
+          if (ok && k < x.ntiles) mma_commit(bar(B_EMPTY + s));
         }
-        if (ok && !issue_pv(tc_ - 1, x.ntiles == 1, ob)) ok = false;
-        ++ui;
+        tc_ += x.ntiles;
+        qn += parts;
       }
       if (!ok) give_up();
       mma_commit(bar(B_DONE));                   // every issued MMA done before TMEM is freed
@@ -518,22 +578,25 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   } else if (CONV && warp >= R::kConv) {
     // ------------------------------------------------------------ converters
     if constexpr (CONV) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       const int r = threadIdx.x - R::kConv * 32;   // this thread's row of every operand
-      int tc_ = 0, ui = 0;
+      int tc_ = 0, qn = 0;
       bool ok = true;
+      auto convert_q = [&]() -> bool {
+        const int qi = qn % kNQ;
+        if (!mbar_wait(bar(B_QFULL + qi), (qn / kNQ) & 1, abort_flag)) return false;
+        rowe[qi * 128 + r] = (int8_t)rescale_row(smem + OFF_Q + qi * kOp, r);
+        fence_proxy_async();
+        mbar_arrive(bar(B_QCONV + qi));
+        ++qn;
+        return true;
+      };
       for (long long kk = 0; ok; ++kk) {
         const long long u = unit_index(kk, blockIdx.x, gridDim.x);
         if (u >= U) break;
         const Unit x = unit_of(a, G, BS, u);
         if (x.ntok <= 0) continue;
-        if constexpr (QC) {
-          const int qi = ui & 1;
-          if (!mbar_wait(bar(B_QFULL + qi), (ui >> 1) & 1, abort_flag)) { ok = false; break; }
-          rowe[qi * 128 + r] = (int8_t)rescale_row(smem + OFF_Q + qi * kOp, r);
-          fence_proxy_async();
-          mbar_arrive(bar(B_QCONV + qi));
-        }
+        if (QC && !convert_q()) { ok = false; break; }
         for (int k = 0; k < x.ntiles && ok; ++k, ++tc_) {
           for (int kv = 0; kv < 2; ++kv) {
             if (!(kv ? V8 : K8)) continue;
@@ -541,222 +604,204 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             if (!mbar_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) { ok = false; break; }
             const int t = x.tile0(k) + r;
             // a V row no row of the unit attends meets only zero weights: it must be finite
-            const bool zero = kv && (!x.needs(t, 1) || ((slots[tc_ % kSlots].missing >> (r / BS)) & 1u));
+            const bool zero = kv && (!x.all.needs(t, 1) || ((slots[tc_ % kSlots].missing >> (r / BS)) & 1u));
             widen_row(smem + OFF_KV + s * kOp, r, zero);
             fence_proxy_async();
             mbar_arrive(bar(B_CONV + s));
           }
+          if (QC && k == 0 && ok && x.two() && !convert_q()) ok = false;
         }
-        ++ui;
       }
       if (!ok) give_up();
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
-    if constexpr (CONV) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    if constexpr (CONV) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int r = threadIdx.x & 127;             // query row = TMEM lane
-    const int hf = threadIdx.x >> 7;             // which half of the keys and of O
+    const int qt = threadIdx.x >> 7;             // query tile of the unit
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const int tl = r / G, g = r - (r / G) * G;   // token of the unit, head of the group
-    float* xch = reinterpret_cast<float*>(smem + OFF_XCH);    // [2][128]
-    // the two warps that share 32 rows
-    auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
-    auto pair_vote = [&](bool v) -> bool {
-      uint32_t o;
-      asm volatile("{ .reg .pred pi, po; setp.ne.u32 pi, %2, 0; bar.red.or.pred po, %1, 64, pi;"
-                   " selp.u32 %0, 1, 0, po; }"
-                   : "=r"(o) : "r"(1 + (warp & 3)), "r"((uint32_t)v) : "memory");
-      return o != 0;
-    };
-    auto vote256 = [](bool v) -> bool {
-      uint32_t o;
-      asm volatile("{ .reg .pred pi, po; setp.ne.u32 pi, %1, 0; bar.red.or.pred po, 5, 256, pi;"
-                   " selp.u32 %0, 1, 0, po; }"
-                   : "=r"(o) : "r"((uint32_t)v) : "memory");
-      return o != 0;
-    };
+    const uint32_t srow = tmem_s + lane_off + qt * kTile, orow_t = tmem_o + lane_off + qt * kD;
+    const int tl = r / G, hg = r - (r / G) * G;  // token of the query tile, head of the group
     bool failed = false;
-    int tc_ = 0, ui = 0;                         // tiles seen, units done
-    // Wait for the output product of tile t. Products alternate between two barriers by
-    // tile parity, so a parity wait is exact: the barrier of t has passed the phase
-    // before t's (S of tile t or a later one has been seen, and the issuer puts S(t)
-    // after O(t - 2) on the in-order tensor pipe) and cannot pass t's own before tile
-    // t + 2 is handed over.
-    auto wait_o = [&](int t) {
-      if (!mbar_wait(bar(B_OSTEP + (t & 1)), (t >> 1) & 1, abort_flag)) failed = true;
-    };
+    int tc_ = 0, qn = 0;                         // key tiles and query tiles of the CTA so far
+    int tiles = 0, units = 0;                    // of this query tile
     for (long long kk = 0; !failed; ++kk) {
       const long long u = unit_index(kk, blockIdx.x, gridDim.x);
       if (u >= U) break;
       const Unit x = unit_of(a, G, BS, u);
       if (x.ntok <= 0) continue;
-      const int ob = ui & 1;
-      const bool row_ok = tl < x.ntok;
-      const int pos = x.pos0 + tl;               // this row attends keys t <= pos with
+      const int base = tc_, q = qn + qt;
+      tc_ += x.ntiles;
+      qn += x.two() ? 2 : 1;
+      if (qt == 1 && !x.two()) continue;
+      const int ntok = x.tokens(qt), pos0 = x.pos(qt);
+      const Reach mine = reach_of(a, pos0, ntok);
+      const bool row_ok = tl < ntok;
+      const int pos = pos0 + tl;                 // this row attends keys t <= pos with
       const int wlo = a.window > 0 ? max(0, pos - a.window + 1) : 0;   // t >= wlo or t < sinks
-      // the window of the unit's last token starts at last_lo
-      const int last_lo = a.window > 0 ? max(0, x.t1 - a.window) : 0;
+      // the window of the query tile's last token starts at last_lo
+      const int last_lo = a.window > 0 ? max(0, mine.t1 - a.window) : 0;
       const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
-      float m = -FLT_MAX, l = 0.f;               // l: this half's part of the row sum
+      float m = -FLT_MAX, l = 0.f;
       float f0 = a.scale_log2;                   // score factor of the row
       if constexpr (QC) {
-        if (!mbar_wait(bar(B_QCONV + (ui & 1)), (ui >> 1) & 1, abort_flag)) failed = true;
-        f0 *= __uint_as_float((uint32_t)(127 - rowe[(ui & 1) * 128 + r]) << 23);
-        mbar_arrive(bar(B_QEMPTY + (ui & 1)));
+        const int qi = q % kNQ;
+        if (!mbar_wait(bar(B_QCONV + qi), (q / kNQ) & 1, abort_flag)) failed = true;
+        f0 *= __uint_as_float((uint32_t)(127 - rowe[qi * 128 + r]) << 23);
+        mbar_arrive(bar(B_QEMPTY + qi));
       }
-      for (int k = 0; k < x.ntiles; ++k, ++tc_) {
-        const int sb = tc_ & 1;
+      bool first = true;
+      for (int k = 0; k < x.ntiles; ++k) {
         const int ts = x.tile0(k);
-        if (!mbar_wait(bar(B_SFULL + sb), (tc_ >> 1) & 1, abort_flag)) failed = true;
-        tc_fence_after();
-        const uint32_t srow = tmem_s + lane_off + sb * kTile + 64 * hf;
-        uint32_t raw[64];
-        tmem_ld32(srow, raw);
-        tmem_ld32(srow + 32, raw + 32);
+        if (!mine.needs(ts, kTile)) continue;
+        const int n = tiles++;
         // blocks that were not loaded: the producer's word (8-bit pools), else the table's
-        const Slot& slot = slots[tc_ % kSlots];
+        const Slot& slot = slots[(base + k) % kSlots];
         uint32_t missing = 0;
-        if constexpr (CONV) {
-          missing = *reinterpret_cast<const volatile uint32_t*>(&slot.missing) & ((1u << NB_T) - 1u);
-        } else {
+        bool open = false;                       // every row sees every key of the tile
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait(bar(B_SFULL + 2 * qt + h), n & 1, abort_flag)) failed = true;
+          __syncwarp();
+          tc_fence_after();
+          uint32_t raw[64];
+          tmem_ld32(srow + 64 * h, raw);
+          tmem_ld32(srow + 64 * h + 32, raw + 32);
+          if (h == 0) {
+            if constexpr (CONV) {
+              missing = *reinterpret_cast<const volatile uint32_t*>(&slot.missing) & ((1u << NB_T) - 1u);
+            } else {
 #pragma unroll
-          for (int q = 0; q < NB_T; ++q) {
-            bool gone = true;
-            if (x.needs(ts + q * BS, BS)) {
-              const int ph = __ldg(table + ts / BS + q);
-              gone = ph < 0 || ph >= a.num_blocks;
+              for (int b = 0; b < NB_T; ++b) {
+                bool gone = true;
+                if (x.all.needs(ts + b * BS, BS)) {
+                  const int ph = __ldg(table + ts / BS + b);
+                  gone = ph < 0 || ph >= a.num_blocks;
+                }
+                missing |= gone ? 1u << b : 0u;
+              }
             }
-            missing |= gone ? 1u << q : 0u;
+            open = missing == 0 && ts + kTile <= pos0 + 1 && (ts >= last_lo || ts + kTile <= a.sinks);
+            if (!V8 && !open) {
+              // a V row no row of the unit attends meets only zero weights: it must be finite
+              // (both query tiles' threads write the zeros, ahead of their own product)
+              if (!x.all.needs(ts + r, 1) || ((missing >> (r / BS)) & 1u)) {
+                const int seq = 2 * (base + k) + 1, s = seq % kNST;
+                if (!mbar_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) failed = true;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  uint4* z = reinterpret_cast<uint4*>(smem + OFF_KV + s * kOp + hh * kHalf + r * 128);
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) z[c] = make_uint4(0, 0, 0, 0);
+                }
+              }
+              fence_proxy_async();
+            }
+            __syncwarp();
           }
-        }
-        // every row sees every key of the tile
-        const bool open = missing == 0 && ts + kTile <= x.pos0 + 1 && (ts >= last_lo || ts + kTile <= a.sinks);
-        if (!V8 && !open) {
-          // a V row no row of the unit attends meets only zero weights: it must be finite
-          // (each group zeroes one d-half of the row)
-          if (!x.needs(ts + r, 1) || ((missing >> (r / BS)) & 1u)) {
-            const int seq = 2 * tc_ + 1, s = seq % kNST;
-            if (!mbar_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) failed = true;
-            uint4* z = reinterpret_cast<uint4*>(smem + OFF_KV + s * kOp + hf * kHalf + r * 128);
+          tmem_wait_ld64(raw);
+          // scores in the log2 domain, s' = s + log2(V scale) with block scales
+          float s_[64];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) z[q] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 64 / 16; ++c) {
+            const int blk = (64 * h + 16 * c) / BS;
+            const float f = BSC ? f0 * slot.ks[blk] : f0, e = BSC ? slot.lvs[blk] : 0.f;
+#pragma unroll
+            for (int j = 16 * c; j < 16 * c + 16; ++j)
+              s_[j] = BSC ? fmaf(__uint_as_float(raw[j]), f, e) : __uint_as_float(raw[j]) * f;
           }
-          fence_proxy_async();
-        }
-        tmem_wait_ld64(raw);
-        // scores in the log2 domain, s' = s + log2(V scale) with block scales
-        float s_[64];
+          if (!open) {
+            // one bit per key of a 32-key chunk: up to the row's position, from its window
+            // on or a first token, in a block that is there
 #pragma unroll
-        for (int q = 0; q < 64 / 16; ++q) {
-          const int blk = (64 * hf + 16 * q) / BS;
-          const float f = BSC ? f0 * slot.ks[blk] : f0, e = BSC ? slot.lvs[blk] : 0.f;
+            for (int c = 0; c < 2; ++c) {
+              const int t0 = ts + 64 * h + 32 * c;
+              auto below = [&](int lim) -> uint32_t {          // keys of the chunk under lim
+                const int n = lim - t0;
+                return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : ((1u << n) - 1u);
+              };
+              uint32_t msk = below(pos + 1) & (~below(wlo) | below(a.sinks));
 #pragma unroll
-          for (int j = 16 * q; j < 16 * q + 16; ++j)
-            s_[j] = BSC ? fmaf(__uint_as_float(raw[j]), f, e) : __uint_as_float(raw[j]) * f;
-        }
-        if (!open) {
-          // one bit per key of a 32-key chunk: up to the row's position, from its window
-          // on or a first token, in a block that is there
+              for (int b = 0; b < 32 / BS; ++b)
+                if ((missing >> ((64 * h + 32 * c) / BS + b)) & 1u) msk &= ~(kBlkBits << (b * BS));
+              if (!row_ok) msk = 0;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int t0 = ts + 64 * hf + 32 * c;
-            auto below = [&](int lim) -> uint32_t {            // keys of the chunk under lim
-              const int n = lim - t0;
-              return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : ((1u << n) - 1u);
-            };
-            uint32_t msk = below(pos + 1) & (~below(wlo) | below(a.sinks));
-#pragma unroll
-            for (int q = 0; q < 32 / BS; ++q)
-              if ((missing >> ((64 * hf + 32 * c) / BS + q)) & 1u) msk &= ~(kBlkBits << (q * BS));
-            if (!row_ok) msk = 0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              s_[32 * c + j] = ((msk >> j) & 1u) ? s_[32 * c + j] : -CUDART_INF_F;
+              for (int j = 0; j < 32; ++j)
+                s_[32 * c + j] = ((msk >> j) & 1u) ? s_[32 * c + j] : -CUDART_INF_F;
+            }
           }
-        }
-        float t0 = -CUDART_INF_F, t1 = t0, t2 = t0, t3 = t0;
+          float t0 = -CUDART_INF_F, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-          t0 = fmaxf(t0, s_[j]);
-          t1 = fmaxf(t1, s_[j + 1]);
-          t2 = fmaxf(t2, s_[j + 2]);
-          t3 = fmaxf(t3, s_[j + 3]);
-        }
-        float tm = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-        if (k == 0 || pair_vote(tm > m + kMove)) {
-          // the row's tile maximum: both halves (the second barrier keeps the buffer until
-          // both have read it)
-          xch[hf * 128 + r] = tm;
-          pair_sync();
-          tm = fmaxf(tm, xch[(hf ^ 1) * 128 + r]);
-          pair_sync();
-          if (k == 0) {
+          for (int j = 0; j < 64; j += 4) {
+            t0 = fmaxf(t0, s_[j]);
+            t1 = fmaxf(t1, s_[j + 1]);
+            t2 = fmaxf(t2, s_[j + 2]);
+            t3 = fmaxf(t3, s_[j + 3]);
+          }
+          const float tm = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+          if (first) {
             m = fmaxf(tm, -FLT_MAX);
-          } else {
-            // O holds the products of tiles up to k - 1: wait for the last one, rescale this
-            // half's columns (both halves of a row take the same decision)
+          } else if (__any_sync(0xffffffffu, tm > m + kMove)) {
+            // rescale the row of O, once every product before this half's is in it: those of
+            // the last tile's second half (the scores of this tile's come after it), or that
+            // of this tile's first half
             const bool resc = tm > m + kMove;
             const float alpha = resc ? ex2(m - tm) : 1.f;
             if (resc) m = tm;
-            wait_o(tc_ - 1);
+            if (!mbar_wait(bar(h == 0 ? B_SFULL + 2 * qt + 1 : B_OSTEP + qt), n & 1, abort_flag)) failed = true;
+            __syncwarp();
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 64 * hf; c < 64 * hf + 64; c += 16) {
+            for (int c = 0; c < kD; c += 16) {
               float o[16];
-              tmem_ld16(tmem_o + lane_off + ob * kD + c, o);
+              tmem_ld16(orow_t + c, o);
               uint32_t w[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-              tmem_put16(tmem_o + lane_off + ob * kD + c, w);
+              tmem_put16(orow_t + c, w);
             }
-            tmem_wait_st();
             l *= alpha;
           }
-        }
-        // weights and this half's part of the row sum; a 32-key chunk's weights go over
-        // its scores, hi parts in its first 16 columns, lo parts in the next 16
+          first = false;
+          // weights and the row sum; a 32-key chunk's weights go over its scores, hi parts in
+          // its first 16 columns, lo parts in the next 16
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t hi[16], lo[16];
-          float part[2] = {0.f, 0.f};            // sums of the chunk's 16-key halves
+          for (int c = 0; c < 2; ++c) {
+            uint32_t hi[16], lo[16];
+            float part[2] = {0.f, 0.f};          // sums of the chunk's 16-key halves
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(s_[32 * c + 2 * e] - m);
-            const float p1 = ex2(s_[32 * c + 2 * e + 1] - m);
-            part[e >> 3] += p0 + p1;
-            pack2<FO == 1, LO>(p0, p1, hi[e], lo[e]);
-          }
-          tmem_put16(srow + 32 * c, hi);
-          if (LO) tmem_put16(srow + 32 * c + 16, lo);
-          if (BSC) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int blk = (64 * hf + 32 * c + 16 * q) / BS;
-              l = fmaf(part[q], __uint_as_float((uint32_t)(127 - (int)slot.lvs[blk]) << 23), l);
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ex2(s_[32 * c + 2 * e] - m);
+              const float p1 = ex2(s_[32 * c + 2 * e + 1] - m);
+              part[e >> 3] += p0 + p1;
+              pack2<FO == 1, LO>(p0, p1, hi[e], lo[e]);
             }
-          } else {
-            l += part[0] + part[1];
+            tmem_put16(srow + 64 * h + 32 * c, hi);
+            if (LO) tmem_put16(srow + 64 * h + 32 * c + 16, lo);
+            if (BSC) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                l = fmaf(part[b], __uint_as_float((uint32_t)(127 - (int)slot.lvs[(64 * h + 32 * c + 16 * b) / BS]) << 23), l);
+            } else {
+              l += part[0] + part[1];
+            }
           }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(B_PREADY + 2 * qt + h));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(B_PREADY + sb));
       }
-      // ---- epilogue: O / l of this row to the output, each half its 64 columns. The
-      // products of the last two tiles may both be pending; the last one's commit tracks
-      // every earlier MMA, so one wait covers both.
-      xch[hf * 128 + r] = l;
-      pair_sync();
-      const float lrow = xch[r] + xch[128 + r];
-      pair_sync();
-      wait_o(tc_ - 1);
+      // ---- epilogue: O / l of this row to the output
+      if (!mbar_wait(bar(B_OFULL + qt), units & 1, abort_flag)) failed = true;
+      ++units;
       tc_fence_after();
-      const float inv = lrow == 0.f ? 0.f : a.v_scale / lrow;
-      const size_t orow = ((size_t)(x.qrow0 + tl) * a.Hq + (size_t)x.h * G + g) * kD;
+      const float inv = l == 0.f ? 0.f : a.v_scale / l;
+      const size_t orow = ((size_t)(x.qrow0 + qt * x.tpt + tl) * a.Hq + (size_t)x.h * G + hg) * kD;
 #pragma unroll 1
-      for (int c = 64 * hf; c < 64 * hf + 64; c += 32) {
+      for (int c = 0; c < kD; c += 32) {
         uint32_t o[32];
-        tmem_ld32(tmem_o + lane_off + ob * kD + c, o);
+        tmem_ld32(orow_t + c, o);
         tmem_wait_ld();
         if (row_ok && !failed) {
           if (a.out_dtype == PA_F32) {
@@ -779,10 +824,8 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         }
       }
       tc_fence_before();
-      mbar_arrive(bar(B_ODONE + ob));
-      ++ui;
-      // the warps of both groups leave together
-      failed = vote256(failed);
+      mbar_arrive(bar(B_ODONE + qt));
+      failed = __any_sync(0xffffffffu, failed);
     }
     if (failed) give_up();
   }
@@ -888,7 +931,7 @@ int launch_prefill_window(const PrefillLaunch& p, cudaStream_t stream) {
   a.context_lens = p.context_lens;
   a.query_start = p.query_start;
   a.B = p.B; a.T = p.T; a.Hq = p.Hq; a.Hkv = p.Hkv; a.num_blocks = p.num_blocks;
-  const int tpu = kM / G;
+  const int tpu = 2 * kM / G;
   a.chunks = p.max_query_len / tpu + (p.max_query_len % tpu != 0);
   a.scale_log2 = p.scale_log2;
   a.v_scale = v8 ? p.v_scale : 1.f;
