@@ -76,7 +76,7 @@ constexpr int OFF_KV = kNQ * kOp;               // [kNST][32 KB]
 constexpr int OFF_BAR = OFF_KV + kNST * kOp;
 enum { B_FULL = 0, B_EMPTY = kNST, B_CONV = 2 * kNST, B_QFULL = 3 * kNST, B_QEMPTY = B_QFULL + kNQ,
        B_QCONV = B_QEMPTY + kNQ, B_SFULL = B_QCONV + kNQ, B_PREADY = B_SFULL + 4, B_OSTEP = B_PREADY + 4,
-       B_OFULL = B_OSTEP + 2, B_ODONE = B_OFULL + 2, B_DONE = B_ODONE + 2, B_COUNT = B_DONE + 1 };
+       B_OFULL = B_OSTEP + 2, B_ODONE = B_OFULL + 2, B_DONE = B_ODONE + 2, B_COUNT = B_DONE + 2 };
 constexpr int OFF_MISC = OFF_BAR + 8 * B_COUNT;
 constexpr int OFF_SLOT = (OFF_MISC + 8 + 15) / 16 * 16;
 struct Slot {                                   // of a tile: what the producer knows of its blocks
@@ -319,7 +319,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   if (threadIdx.x == 0) {
     for (int s = 0; s < kNST; ++s) {
       mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), 1);
+      mbar_init(bar(B_EMPTY + s), 2);
       mbar_init(bar(B_CONV + s), 128);
     }
     for (int i = 0; i < kNQ; ++i) {
@@ -333,10 +333,10 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         mbar_init(bar(B_PREADY + 2 * i + h), 128);
       }
       mbar_init(bar(B_OSTEP + i), 1);
+      mbar_init(bar(B_DONE + i), 1);
       mbar_init(bar(B_OFULL + i), 1);
       mbar_init(bar(B_ODONE + i), 128);
     }
-    mbar_init(bar(B_DONE), 1);
     *abort_flag = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -477,103 +477,98 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           while (!mbar_try(bar(B_QFULL + q % kNQ), (q / kNQ) & 1) && globaltimer() - t0 < kWaitNs) {}
         }
       }
-    } else if (warp == R::kMma && elect_one()) {
-      // ---------------------------------------------------------- MMA issuer
-      // Per key tile, half of its keys and query tile g: the output product of the half of
-      // g's last key tile, then g's scores of this one (over the weights that product has
-      // read: the tensor pipe is in order). So scores are ready half a tile ahead of the
-      // softmax.
-      int tc_ = 0, qn = 0;                       // key tiles, query tiles so far
-      int tiles[2] = {0, 0}, units[2] = {0, 0};  // of query tile g
+    } else if (warp <= R::kMma + 1 && elect_one()) {
+      // ---------------------------------------------------------- MMA issuers
+      // One warp per query tile: a step of the issue (three waits, 12 or 16 products, two
+      // commits) takes ~1100 cycles, so one warp for both would set the pace. Per key tile
+      // and half of its keys: the output product of that half of the last key tile, then
+      // this one's scores (over the weights that product has read: the tensor pipe is in
+      // order), so that scores are ready half a tile ahead of the softmax. A stage is empty
+      // when both issuers are past it.
+      const int g = warp - R::kMma;
+      int tc_ = 0, qn = 0;                       // key tiles, query tiles of the CTA so far
+      int tiles = 0, units = 0;                  // of this query tile
       bool ok = true;
-      // output product of query tile g with half h of key tile tt, its n-th (the unit's
-      // first if first)
-      auto issue_pv = [&](int g, int h, int tt, int n, bool first) -> bool {
-        if (!mbar_wait(bar(B_PREADY + 2 * g + h), n & 1, abort_flag)) return false;
-        const int seq = 2 * tt + 1, s = seq % kNST;
-        if (h == 0) {
-          // O is that of the last unit until its epilogue has read it
-          if (first && units[g] > 0 && !mbar_wait(bar(B_ODONE + g), (units[g] - 1) & 1, abort_flag)) return false;
-          if (!mbar_wait(ready_bar(1, s), (seq / kNST) & 1, abort_flag)) return false;
-        }
-        tc_fence_after();
-        const uint32_t vst = sbase + OFF_KV + s * kOp + h * (kTile / 2) * 128;
-#pragma unroll
-        for (int part = 0; part < (LO ? 2 : 1); ++part) {
-#pragma unroll
-          for (int kk = 0; kk < kTile / 32; ++kk) {
-            const uint64_t bd = sw128_desc(vst + kk * 16 * 128, kHalf, 1024);
-            mma_f16_ta(tmem_o + g * kD,
-                       tmem_s + g * kTile + h * (kTile / 2) + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, bd,
-                       IDESC_O, (first && h == 0 && part == 0 && kk == 0) ? 0u : 1u);
-          }
-        }
-        if (h == 0) mma_commit(bar(B_OSTEP + g));
-        return true;
-      };
       for (long long kk = 0; ok; ++kk) {
         const long long u = unit_index(kk, blockIdx.x, gridDim.x);
         if (u >= U) break;
         const Unit x = unit_of(a, G, BS, u);
         if (x.ntok <= 0) continue;
         const int parts = x.two() ? 2 : 1;
-        const Reach reach[2] = {reach_of(a, x.pos(0), x.tokens(0)), reach_of(a, x.pos(1), x.tokens(1))};
-        int done[2] = {0, 0};                    // tiles whose scores were issued, of this unit
-        bool was[2], pend[2] = {false, false};   // the last tile, this tile is one of g's
+        const Reach mine = reach_of(a, x.pos(g), x.tokens(g));
+        const int qi = (qn + g) % kNQ;
+        const uint32_t qst = sbase + OFF_Q + qi * kOp;
+        int done = 0;                            // tiles whose scores were issued, of this unit
+        bool pend = false;
         for (int k = 0; k <= x.ntiles && ok; ++k) {
-          const int t0 = k < x.ntiles ? x.tile0(k) : 0;
-          const int seq = 2 * (tc_ + k), s = seq % kNST;
-          const uint32_t kst = sbase + OFF_KV + s * kOp;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            was[g] = pend[g];
-            pend[g] = g < parts && k < x.ntiles && reach[g].needs(t0, kTile);
-          }
+          const bool was = pend, more = k < x.ntiles;
+          const int t0 = more ? x.tile0(k) : 0;
+          const int seq = 2 * (tc_ + k), s = seq % kNST, sv = (seq - 1) % kNST;
+          pend = g < parts && more && mine.needs(t0, kTile);
+          const uint32_t kst = sbase + OFF_KV + s * kOp, vst = sbase + OFF_KV + sv * kOp;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            // ---- the last tile: n-th of the query tile, the unit's first if first
+            if (was) {
+              const int n = tiles - 1 - (h == 1 && pend);
+              const bool first = h == 0 && done == 1;
+              ok = mbar_wait(bar(B_PREADY + 2 * g + h), n & 1, abort_flag);
+              // O is that of the last unit until its epilogue has read it
+              if (ok && first && units > 0) ok = mbar_wait(bar(B_ODONE + g), (units - 1) & 1, abort_flag);
+              if (ok && h == 0) ok = mbar_wait(ready_bar(1, sv), ((seq - 1) / kNST) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (was[g] && ok)
-                ok = issue_pv(g, h, tc_ + k - 1, tiles[g] - 1 - (h == 1 && pend[g]), done[g] - (h == 1 && pend[g]) == 1);
+              for (int part = 0; part < (LO ? 2 : 1); ++part) {
+#pragma unroll
+                for (int kk = 0; kk < kTile / 32; ++kk) {
+                  const uint64_t bd = sw128_desc(vst + h * (kTile / 2) * 128 + kk * 16 * 128, kHalf, 1024);
+                  mma_f16_ta(tmem_o + g * kD,
+                             tmem_s + g * kTile + h * (kTile / 2) + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
+                             bd, IDESC_O, (first && part == 0 && kk == 0) ? 0u : 1u);
+                }
+              }
+              if (h == 0) mma_commit(bar(B_OSTEP + g));
               // (a query tile's key tiles lie in two runs, sinks and window: was its last one)
-              if (ok && h == 1 && was[g] && !pend[g] && (k == x.ntiles || t0 >= reach[g].t1)) {
+              if (h == 1 && !pend && (!more || t0 >= mine.t1)) {
                 mma_commit(bar(B_OFULL + g));
-                ++units[g];
+                ++units;
               }
-              if (pend[g] && ok) {
-                const int qi = (qn + g) % kNQ;
-                if (h == 0) {
-                  if (done[g] == 0)
-                    ok = mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), ((qn + g) / kNQ) & 1, abort_flag);
-                  ok = ok && mbar_wait(ready_bar(0, s), (seq / kNST) & 1, abort_flag);
-                  ++done[g];
-                  ++tiles[g];
-                }
-                if (ok) {
-                  tc_fence_after();
-                  const uint32_t qst = sbase + OFF_Q + qi * kOp;
-#pragma unroll
-                  for (int ks = 0; ks < kD / 16; ++ks) {
-                    const uint64_t ad = sw128_desc(qst + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024);
-                    const uint64_t bd = sw128_desc(kst + (ks >> 2) * kHalf + h * (kTile / 2) * 128 + (ks & 3) * 32, 16, 1024);
-                    mma_f16(tmem_s + g * kTile + h * (kTile / 2), ad, bd, IDESC_S, ks > 0 ? 1u : 0u);
-                  }
-                  mma_commit(bar(B_SFULL + 2 * g + h));
-                  if (h == 1 && t0 + kTile >= reach[g].t1) mma_commit(bar(B_QEMPTY + qi));
-                }
-              }
+            } else if (k > 0 && h == 0 && !mbar_wait(ready_bar(1, sv), ((seq - 1) / kNST) & 1, abort_flag)) {
+              ok = false;
+              break;
             }
+            if (k > 0 && h == 1) mma_commit(bar(B_EMPTY + sv));
+            // ---- this one
+            if (more && h == 0) {
+              if (pend && done == 0)
+                ok = mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), ((qn + g) / kNQ) & 1, abort_flag);
+              ok = ok && mbar_wait(ready_bar(0, s), (seq / kNST) & 1, abort_flag);
+              if (!ok) break;
+              done += pend;
+              tiles += pend;
+            }
+            if (pend) {
+              tc_fence_after();
+#pragma unroll
+              for (int ks = 0; ks < kD / 16; ++ks) {
+                const uint64_t ad = sw128_desc(qst + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024);
+                const uint64_t bd = sw128_desc(kst + (ks >> 2) * kHalf + h * (kTile / 2) * 128 + (ks & 3) * 32, 16, 1024);
+                mma_f16(tmem_s + g * kTile + h * (kTile / 2), ad, bd, IDESC_S, ks > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(B_SFULL + 2 * g + h));
+              if (h == 1 && t0 + kTile >= mine.t1) mma_commit(bar(B_QEMPTY + qi));
+            }
+            if (more && h == 1) mma_commit(bar(B_EMPTY + s));
           }
-          if (ok && k > 0) mma_commit(bar(B_EMPTY + (seq - 1) % kNST));
-          if (ok && k < x.ntiles) mma_commit(bar(B_EMPTY + s));
         }
         tc_ += x.ntiles;
         qn += parts;
       }
       if (!ok) give_up();
-      mma_commit(bar(B_DONE));                   // every issued MMA done before TMEM is freed
+      mma_commit(bar(B_DONE + g));               // every issued MMA done before TMEM is freed
       const uint64_t t0 = globaltimer();
-      while (!mbar_try(bar(B_DONE), 0) && globaltimer() - t0 < kWaitNs) {}
+      while (!mbar_try(bar(B_DONE + g), 0) && globaltimer() - t0 < kWaitNs) {}
     }
   } else if (CONV && warp >= R::kConv) {
     // ------------------------------------------------------------ converters
