@@ -578,9 +578,9 @@ int pa_decode_blk8(void* out, int out_dtype, const void* query, int q_dtype, con
  * pa_prefill_kv (num_blocks >= 1; a sequence whose query_start passes T also sets
  * PA_DEV_BAD_CTX). Sums and softmax statistics are fp32; the weights enter the
  * output product as two 16-bit parts, over an 8-bit V pool as one f16 value
- * (2^-12 relative). As there, the query rows of up to 128 / G neighbouring tokens
- * are one matrix operand: an infinite or NaN V element of a token that one of
- * them attends may reach the others' rows.
+ * (2^-12 relative). As there, the query rows of neighbouring tokens (up to 256 / G
+ * of them) meet the same key tiles: an infinite or NaN V element of a token that
+ * one of them attends may reach the others' rows.
  *
  * pa_prefill_blk8 -- the same over the block-scaled 8-bit cache (scales and
  * their errors as pa_decode_blk8); window 0: every earlier token.

@@ -3,37 +3,42 @@
 //
 // The new token at position p of its sequence attends the keys
 //   t <= p  with  t > p - window  or  t < sinks      (window 0: every t <= p).
-// Work unit = (sequence, chunk of 128 / G new tokens, KV head): its 128 query rows
-// (token, head of the group) are the MMA's M. Its tiles are the 128-key tiles with
-// a key some row attends: the first n0 (sinks) and those from w0 on (the window of
-// its first token). Blocks that no row attends are not loaded, nor are their table
-// entries read. Per tile:
-//   S[128 x 128] = Q . K^T (tensor memory, two buffers by tile)
-//   O[128 x 128] += P . V  (two buffers by unit; P is read from tensor memory)
-// Two groups of four softmax warps share the rows: thread (half hf, row r) has keys
-// [64 hf, 64 hf + 64) of every tile in registers (64 scores: one read of S), writes its
-// weights over S, and owns O's columns [64 hf, 64 hf + 64). The reference maximum of a
-// row moves only when a tile passes it by far: the two threads of a row vote on that
-// with one barrier, and only then swap their maxima through shared memory (and rescale
-// the row's O in tensor memory). It is floored at -FLT_MAX, so masked scores (-inf) need
-// no guard. A tile that every row sees whole skips the masks.
+// Work unit = (sequence, chunk of 256 / G new tokens, KV head): two query tiles of 128
+// rows (token, head of the group), each the M of its MMAs. Its key tiles are the 128-key
+// tiles with a key some row attends: the first n0 (sinks) and those from w0 on (the window
+// of its first token); a query tile skips those it attends nothing of. Blocks that no row
+// attends are not loaded, nor are their table entries read. Per query tile and key tile
+//   S[128 x 128] = Q . K^T, in two halves of 64 keys,
+//   O[128 x 128] += P . V, P written over S in tensor memory,
+// which fills tensor memory: 2 x (S 128 + O 128) columns. The two query tiles share every
+// K and V tile (one copy, one widening), and one's products run while the other's softmax
+// does; the scores of a half are issued as soon as the output product of the last tile's
+// same half has read the weights under them, half a tile ahead of the softmax.
+// A query tile has four softmax warps, a row per thread, 64 scores in registers at a time,
+// and its own issuing warp. The reference maximum of a row moves only when a half passes it
+// by far, and is floored at -FLT_MAX, so masked scores (-inf) need no guard. A tile that
+// every row sees whole skips the masks.
 //
 // 16-bit pools: the products take the query's type, and the weights two 16-bit parts
 // (hi + lo, ~16 bits).
 // 8-bit pools: four converter warps widen each tile's codes to f16 (exactly, in place:
 // TMA leaves a row's 128 codes in the line of its second half) ahead of the tensor
-// cores, so neither the softmax nor the MMAs wait for it; a bf16 query is rescaled by
-// a power of two per row and becomes f16 too, exactly (an element 2^-39 of its row's
-// largest is rounded), once per unit. Weights over 8-bit V enter as one f16 part: their
-// 2^-12 is far below the 2^-4 of the codes they multiply, and under half a step of
-// either 16-bit output.
+// cores; a bf16 query is rescaled by a power of two per row and becomes f16 too, exactly
+// (an element 2^-39 of its row's largest is rounded), once per unit. Weights over 8-bit V
+// enter as one f16 part: their 2^-12 is far below the 2^-4 of the codes they multiply, and
+// under half a step of either 16-bit output.
 //
-// Measured (8192-token prompt, 32 query heads over 8, block-scaled cache): 762 us, 722
-// TFLOP/s; FP8 pools with one scale 711 us; bf16 pools 947 us. Widened by the softmax
-// warps between two tiles instead, as prefill_tc.cu does, the block-scaled prompt took
-// 2110 us. A tile takes ~3000 cycles: the softmax threads ~2400 (1350 of them the
-// exponentials, 1024 at the special-function units' rate), beside 1750 of shared-memory
-// bandwidth (operands of both products, codes in and f16 out) and ~2000 of the issuer.
+// Measured (8192-token prompt, 32 query heads over 8, 550 GFLOP): block-scaled cache 628
+// us, 875 TFLOP/s; bf16 pools 667 us; windowed bf16 chunks 270 us. Units of one query tile
+// whose rows two threads share took 762, 925 and 298 us there, and with the codes widened
+// by the softmax warps 2110. A pair of tiles takes ~5000 cycles: a softmax warp ~2100 for
+// each half (some 1100 of them its 64 exponentials, beside the other query tile's) without
+// ever waiting for scores; the tensor cores are busy for 2048 of them, shared memory for
+// ~3000 (operands of S are read once per 64 keys), the special-function units for 2048.
+// What mattered besides the layout: elect.sync for the issuing threads (a product's issue
+// took 110 cycles without it, 25 with it), an issuing warp per query tile (a step of the
+// issue, waits and commits included, is ~1100 cycles), packed fp32 operations, and reading
+// the block scales before the scores (shared-memory loads are slow beside the MMAs').
 //
 // Block-scaled pools: K's power of two multiplies its keys' scores; V's enters as its
 // log2, s' = s + log2(vs), so the running maximum is that of the whole contribution,
@@ -42,7 +47,7 @@
 // blocks in a ring of shared-memory slots.
 //
 // CTA, persistent over rounds of units in alternating directions: warps 0-7 softmax,
-// then (8-bit pools) 8-11 converters, then the TMA producer and the MMA issuer. Every
+// then (8-bit pools) 8-11 converters, then the TMA producer and the two MMA issuers. Every
 // pipeline wait is bounded (1 s); one that gives up sets PA_DEV_TIMEOUT, raises the
 // CTA's abort flag, and every role drains its asynchronous work, frees tensor memory
 // and returns.
@@ -174,6 +179,22 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
+      " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};"
+      " add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // Two fp32 weights as packed 16-bit values, and (LO) what their rounding lost.
@@ -661,6 +682,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           __syncwarp();
           tc_fence_after();
           uint32_t raw[64];
+          float* s_ = reinterpret_cast<float*>(raw);
           tmem_ld32(srow + 64 * h, raw);
           tmem_ld32(srow + 64 * h + 32, raw + 32);
           if (h == 0) {
@@ -695,17 +717,18 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             }
             __syncwarp();
           }
-          tmem_wait_ld64(raw);
-          // scores in the log2 domain, s' = s + log2(V scale) with block scales
-          float s_[64];
+          // Scores in the log2 domain, s' = s + log2(V scale) with block scales, are
+          // raw f + e with f and e per 16 keys; where some are masked they are formed and
+          // masked first, and f = 1, e = 0 from then on.
+          float f[4], e[4], back[4];             // back: what a weight counts in the row sum
 #pragma unroll
-          for (int c = 0; c < 64 / 16; ++c) {
+          for (int c = 0; c < 4; ++c) {
             const int blk = (64 * h + 16 * c) / BS;
-            const float f = BSC ? f0 * slot.ks[blk] : f0, e = BSC ? slot.lvs[blk] : 0.f;
-#pragma unroll
-            for (int j = 16 * c; j < 16 * c + 16; ++j)
-              s_[j] = BSC ? fmaf(__uint_as_float(raw[j]), f, e) : __uint_as_float(raw[j]) * f;
+            f[c] = BSC ? f0 * slot.ks[blk] : f0;
+            e[c] = BSC ? slot.lvs[blk] : 0.f;
+            back[c] = __uint_as_float((uint32_t)(127 - (int)e[c]) << 23);
           }
+          tmem_wait_ld64(raw);
           if (!open) {
             // one bit per key of a 32-key chunk: up to the row's position, from its window
             // on or a first token, in a block that is there
@@ -722,19 +745,39 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
                 if ((missing >> ((64 * h + 32 * c) / BS + b)) & 1u) msk &= ~(kBlkBits << (b * BS));
               if (!row_ok) msk = 0;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                s_[32 * c + j] = ((msk >> j) & 1u) ? s_[32 * c + j] : -CUDART_INF_F;
+              for (int j = 0; j < 32; ++j) {
+                const int q = 2 * c + j / 16;
+                s_[32 * c + j] = ((msk >> j) & 1u) ? fmaf(s_[32 * c + j], f[q], e[q]) : -CUDART_INF_F;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              f[c] = 1.f;
+              e[c] = 0.f;
             }
           }
-          float t0 = -CUDART_INF_F, t1 = t0, t2 = t0, t3 = t0;
+          float tm = -CUDART_INF_F;
 #pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            t0 = fmaxf(t0, s_[j]);
-            t1 = fmaxf(t1, s_[j + 1]);
-            t2 = fmaxf(t2, s_[j + 2]);
-            t3 = fmaxf(t3, s_[j + 3]);
+          for (int c = 0; c < 4; ++c) {
+            // (f has one sign in all of a launch, but for the masked tiles' f = 1)
+            float t0 = s_[16 * c], t1 = s_[16 * c + 1];
+            if (f[0] >= 0.f) {
+#pragma unroll
+              for (int j = 16 * c + 2; j < 16 * c + 16; j += 2) {
+                t0 = fmaxf(t0, s_[j]);
+                t1 = fmaxf(t1, s_[j + 1]);
+              }
+              t0 = fmaxf(t0, t1);
+            } else {
+#pragma unroll
+              for (int j = 16 * c + 2; j < 16 * c + 16; j += 2) {
+                t0 = fminf(t0, s_[j]);
+                t1 = fminf(t1, s_[j + 1]);
+              }
+              t0 = fminf(t0, t1);
+            }
+            tm = fmaxf(tm, fmaf(t0, f[c], e[c]));
           }
-          const float tm = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
           if (first) {
             m = fmaxf(tm, -FLT_MAX);
           } else if (__any_sync(0xffffffffu, tm > m + kMove)) {
@@ -764,23 +807,25 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t hi[16], lo[16];
-            float part[2] = {0.f, 0.f};          // sums of the chunk's 16-key halves
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(s_[32 * c + 2 * e] - m);
-              const float p1 = ex2(s_[32 * c + 2 * e + 1] - m);
-              part[e >> 3] += p0 + p1;
-              pack2<FO == 1, LO>(p0, p1, hi[e], lo[e]);
+            for (int q = 0; q < 2; ++q) {
+              const float2 ff = make_float2(f[2 * c + q], f[2 * c + q]);
+              const float em = e[2 * c + q] - m;
+              const float2 ee = make_float2(em, em);
+              float2 sum = make_float2(0.f, 0.f);          // of the 16 keys
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int i = 32 * c + 16 * q + 2 * j;
+                float2 p = fma2(make_float2(s_[i], s_[i + 1]), ff, ee);
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                sum = add2(sum, p);
+                pack2<FO == 1, LO>(p.x, p.y, hi[8 * q + j], lo[8 * q + j]);
+              }
+              l = BSC ? fmaf(sum.x + sum.y, back[2 * c + q], l) : l + (sum.x + sum.y);
             }
             tmem_put16(srow + 64 * h + 32 * c, hi);
             if (LO) tmem_put16(srow + 64 * h + 32 * c + 16, lo);
-            if (BSC) {
-#pragma unroll
-              for (int b = 0; b < 2; ++b)
-                l = fmaf(part[b], __uint_as_float((uint32_t)(127 - (int)slot.lvs[(64 * h + 32 * c + 16 * b) / BS]) << 23), l);
-            } else {
-              l += part[0] + part[1];
-            }
           }
           tmem_wait_st();
           tc_fence_before();
