@@ -25,8 +25,8 @@
 // TMA leaves a row's 128 codes in the line of its second half) ahead of the tensor
 // cores; a bf16 query is rescaled by a power of two per row and becomes f16 too, exactly
 // (an element 2^-39 of its row's largest is rounded), once per unit. Weights over 8-bit V
-// enter as one f16 part: their 2^-12 is far below the 2^-4 of the codes they multiply, and
-// under half a step of either 16-bit output.
+// enter as one f16 part: their 2^-11 is far below the 2^-4 of the codes they multiply, and
+// no more than half a step of either 16-bit output.
 //
 // Measured (8192-token prompt, 32 query heads over 8, 550 GFLOP): block-scaled cache 628
 // us, 875 TFLOP/s; bf16 pools 667 us; windowed bf16 chunks 270 us. Units of one query tile
@@ -81,7 +81,7 @@ constexpr int OFF_KV = kNQ * kOp;               // [kNST][32 KB]
 constexpr int OFF_BAR = OFF_KV + kNST * kOp;
 enum { B_FULL = 0, B_EMPTY = kNST, B_CONV = 2 * kNST, B_QFULL = 3 * kNST, B_QEMPTY = B_QFULL + kNQ,
        B_QCONV = B_QEMPTY + kNQ, B_SFULL = B_QCONV + kNQ, B_PREADY = B_SFULL + 4, B_OSTEP = B_PREADY + 4,
-       B_OFULL = B_OSTEP + 2, B_ODONE = B_OFULL + 2, B_DONE = B_ODONE + 2, B_COUNT = B_DONE + 2 };
+       B_OFULL = B_OSTEP + 2, B_ODONE = B_OFULL + 2, B_DONE = B_ODONE + 2, B_XCH = B_DONE + 2, B_COUNT = B_XCH + 1 };
 constexpr int OFF_MISC = OFF_BAR + 8 * B_COUNT;
 constexpr int OFF_SLOT = (OFF_MISC + 8 + 15) / 16 * 16;
 struct Slot {                                   // of a tile: what the producer knows of its blocks
@@ -90,7 +90,8 @@ struct Slot {                                   // of a tile: what the producer 
   uint32_t pad[3];
 };
 constexpr int OFF_ROWE = OFF_SLOT + kSlots * (int)sizeof(Slot);  // [kNQ][128] exponents of rescaled rows
-constexpr int kSmem = OFF_ROWE + kNQ * 128 + 1024;               // + alignment slack
+constexpr int OFF_XCH = OFF_ROWE + kNQ * 128;                    // [2][128] maxima and sums of a second part
+constexpr int kSmem = OFF_XCH + 2 * 128 * 4 + 1024;              // + alignment slack
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 struct Args {
@@ -139,6 +140,26 @@ struct Unit {
   __device__ __forceinline__ int pos(int g) const { return pos0 + g * tpt; }
   __device__ __forceinline__ bool two() const { return ntok > tpt; }
 };
+
+// What the g-th issuer and softmax warps do of a unit: query tile g and the key tiles it
+// attends something of, or, where there is only one query tile, every other key tile of
+// it (the two parts are joined at the end).
+struct Part {
+  Reach reach;
+  int last;             // its last key tile
+  bool on, split;
+  __device__ __forceinline__ bool takes(const Unit& x, int g, int k) const {
+    return on && (split ? (k & 1) == g : reach.needs(x.tile0(k), kTile));
+  }
+};
+__device__ __forceinline__ Part part_of(const Args& a, const Unit& x, int g) {
+  Part p;
+  p.split = !x.two() && x.ntiles > 1;
+  p.on = g == 0 || x.two() || p.split;
+  p.reach = x.two() ? reach_of(a, x.pos(g), x.tokens(g)) : x.all;
+  p.last = x.two() ? (p.reach.t1 - 1) / kTile - x.w0 + x.n0 : x.ntiles - 1 - (p.split && ((x.ntiles - 1 - g) & 1));
+  return p;
+}
 
 __device__ __forceinline__ Unit unit_of(const Args& a, int G, int bs, long long u) {
   Unit x;
@@ -345,7 +366,9 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
     }
     for (int i = 0; i < kNQ; ++i) {
       mbar_init(bar(B_QFULL + i), 1);
-      mbar_init(bar(B_QEMPTY + i), QC ? 129 : 1);      // (the softmax threads read the rows' exponents)
+      // both issuers, and (QC) the softmax threads of both parts, which read the rows'
+      // exponents: those of a part alone arrive twice
+      mbar_init(bar(B_QEMPTY + i), QC ? 258 : 2);
       mbar_init(bar(B_QCONV + i), 128);
     }
     for (int i = 0; i < 2; ++i) {
@@ -355,6 +378,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       }
       mbar_init(bar(B_OSTEP + i), 1);
       mbar_init(bar(B_DONE + i), 1);
+      if (i == 0) mbar_init(bar(B_XCH), 128);
       mbar_init(bar(B_OFULL + i), 1);
       mbar_init(bar(B_ODONE + i), 128);
     }
@@ -504,8 +528,9 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       // commits) takes ~1100 cycles, so one warp for both would set the pace. Per key tile
       // and half of its keys: the output product of that half of the last key tile, then
       // this one's scores (over the weights that product has read: the tensor pipe is in
-      // order), so that scores are ready half a tile ahead of the softmax. A stage is empty
-      // when both issuers are past it.
+      // order), so that scores are ready half a tile ahead of the softmax. Stages and query
+      // tiles are empty when both issuers are past them, and each issuer waits for every one
+      // in turn, its own or not: a parity wait is only exact within one phase.
       const int g = warp - R::kMma;
       int tc_ = 0, qn = 0;                       // key tiles, query tiles of the CTA so far
       int tiles = 0, units = 0;                  // of this query tile
@@ -515,17 +540,22 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         if (u >= U) break;
         const Unit x = unit_of(a, G, BS, u);
         if (x.ntok <= 0) continue;
-        const int parts = x.two() ? 2 : 1;
-        const Reach mine = reach_of(a, x.pos(g), x.tokens(g));
-        const int qi = (qn + g) % kNQ;
+        const Part mine = part_of(a, x, g);
+        const int qt = qn + (mine.split ? 0 : g), qi = qt % kNQ;
         const uint32_t qst = sbase + OFF_Q + qi * kOp;
+        // the other part's query tile
+        auto pass_q = [&](int q) -> bool {
+          if (!mbar_wait(bar((QC ? B_QCONV : B_QFULL) + q % kNQ), (q / kNQ) & 1, abort_flag)) return false;
+          mbar_arrive(bar(B_QEMPTY + q % kNQ));
+          return true;
+        };
+        if (g == 1 && !mine.split && !pass_q(qn)) { ok = false; break; }
         int done = 0;                            // tiles whose scores were issued, of this unit
         bool pend = false;
         for (int k = 0; k <= x.ntiles && ok; ++k) {
           const bool was = pend, more = k < x.ntiles;
-          const int t0 = more ? x.tile0(k) : 0;
           const int seq = 2 * (tc_ + k), s = seq % kNST, sv = (seq - 1) % kNST;
-          pend = g < parts && more && mine.needs(t0, kTile);
+          pend = more && mine.takes(x, g, k);
           const uint32_t kst = sbase + OFF_KV + s * kOp, vst = sbase + OFF_KV + sv * kOp;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -550,8 +580,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
                 }
               }
               if (h == 0) mma_commit(bar(B_OSTEP + g));
-              // (a query tile's key tiles lie in two runs, sinks and window: was its last one)
-              if (h == 1 && !pend && (!more || t0 >= mine.t1)) {
+              if (h == 1 && k - 1 == mine.last) {
                 mma_commit(bar(B_OFULL + g));
                 ++units;
               }
@@ -563,7 +592,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             // ---- this one
             if (more && h == 0) {
               if (pend && done == 0)
-                ok = mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), ((qn + g) / kNQ) & 1, abort_flag);
+                ok = mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), (qt / kNQ) & 1, abort_flag);
               ok = ok && mbar_wait(ready_bar(0, s), (seq / kNST) & 1, abort_flag);
               if (!ok) break;
               done += pend;
@@ -578,13 +607,14 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
                 mma_f16(tmem_s + g * kTile + h * (kTile / 2), ad, bd, IDESC_S, ks > 0 ? 1u : 0u);
               }
               mma_commit(bar(B_SFULL + 2 * g + h));
-              if (h == 1 && t0 + kTile >= mine.t1) mma_commit(bar(B_QEMPTY + qi));
+              if (h == 1 && k == mine.last) mma_commit(bar(B_QEMPTY + qi));
             }
             if (more && h == 1) mma_commit(bar(B_EMPTY + s));
           }
         }
+        if (ok && g == 0 && x.two()) ok = pass_q(qn + 1);
         tc_ += x.ntiles;
-        qn += parts;
+        qn += x.two() ? 2 : 1;
       }
       if (!ok) give_up();
       mma_commit(bar(B_DONE + g));               // every issued MMA done before TMEM is freed
@@ -641,36 +671,31 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
     const int tl = r / G, hg = r - (r / G) * G;  // token of the query tile, head of the group
     bool failed = false;
     int tc_ = 0, qn = 0;                         // key tiles and query tiles of the CTA so far
-    int tiles = 0, units = 0;                    // of this query tile
+    int tiles = 0, units = 0, splits = 0;        // of this part; units in two parts
+    float* xch = reinterpret_cast<float*>(smem + OFF_XCH);
     for (long long kk = 0; !failed; ++kk) {
       const long long u = unit_index(kk, blockIdx.x, gridDim.x);
       if (u >= U) break;
       const Unit x = unit_of(a, G, BS, u);
       if (x.ntok <= 0) continue;
-      const int base = tc_, q = qn + qt;
+      const Part part = part_of(a, x, qt);
+      const int base = tc_, qs = part.split ? 0 : qt, q = qn + qs;     // its query tile: qs
       tc_ += x.ntiles;
       qn += x.two() ? 2 : 1;
-      if (qt == 1 && !x.two()) continue;
-      const int ntok = x.tokens(qt), pos0 = x.pos(qt);
-      const Reach mine = reach_of(a, pos0, ntok);
+      if (!part.on) continue;
+      const int ntok = x.tokens(qs), pos0 = x.pos(qs);
       const bool row_ok = tl < ntok;
       const int pos = pos0 + tl;                 // this row attends keys t <= pos with
       const int wlo = a.window > 0 ? max(0, pos - a.window + 1) : 0;   // t >= wlo or t < sinks
       // the window of the query tile's last token starts at last_lo
-      const int last_lo = a.window > 0 ? max(0, mine.t1 - a.window) : 0;
+      const int last_lo = a.window > 0 ? max(0, part.reach.t1 - a.window) : 0;
       const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
       float m = -FLT_MAX, l = 0.f;
       float f0 = a.scale_log2;                   // score factor of the row
-      if constexpr (QC) {
-        const int qi = q % kNQ;
-        if (!mbar_wait(bar(B_QCONV + qi), (q / kNQ) & 1, abort_flag)) failed = true;
-        f0 *= __uint_as_float((uint32_t)(127 - rowe[qi * 128 + r]) << 23);
-        mbar_arrive(bar(B_QEMPTY + qi));
-      }
       bool first = true;
       for (int k = 0; k < x.ntiles; ++k) {
+        if (!part.takes(x, qt, k)) continue;
         const int ts = x.tile0(k);
-        if (!mine.needs(ts, kTile)) continue;
         const int n = tiles++;
         // blocks that were not loaded: the producer's word (8-bit pools), else the table's
         const Slot& slot = slots[(base + k) % kSlots];
@@ -681,6 +706,13 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           if (!mbar_wait(bar(B_SFULL + 2 * qt + h), n & 1, abort_flag)) failed = true;
           __syncwarp();
           tc_fence_after();
+          if (QC && first) {
+            // (the scores say that the query tile was converted. Waiting for that instead would
+            // not do: a part that sits out units may be phases ahead of it.)
+            f0 *= __uint_as_float((uint32_t)(127 - rowe[q % kNQ * 128 + r]) << 23);
+            mbar_arrive(bar(B_QEMPTY + q % kNQ));
+            if (!part.split) mbar_arrive(bar(B_QEMPTY + q % kNQ));
+          }
           uint32_t raw[64];
           float* s_ = reinterpret_cast<float*>(raw);
           tmem_ld32(srow + 64 * h, raw);
@@ -836,25 +868,56 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       if (!mbar_wait(bar(B_OFULL + qt), units & 1, abort_flag)) failed = true;
       ++units;
       tc_fence_after();
+      if (part.split && qt == 1) {
+        // the second part: its maximum and sum to the first, which reads its O
+        xch[r] = m;
+        xch[128 + r] = l;
+        tc_fence_before();
+        mbar_arrive(bar(B_XCH));
+        failed = __any_sync(0xffffffffu, failed);
+        continue;
+      }
+      float wa = 1.f, wb = 0.f;
+      if (part.split) {
+        if (!mbar_wait(bar(B_XCH), splits & 1, abort_flag)) failed = true;
+        __syncwarp();
+        tc_fence_after();
+        const float m2 = xch[r], top = fmaxf(m, m2);
+        wa = ex2(m - top);
+        wb = ex2(m2 - top);
+        l = fmaf(l, wa, xch[128 + r] * wb);
+      }
       const float inv = l == 0.f ? 0.f : a.v_scale / l;
-      const size_t orow = ((size_t)(x.qrow0 + qt * x.tpt + tl) * a.Hq + (size_t)x.h * G + hg) * kD;
+      wa *= inv;
+      wb *= inv;
+      const size_t orow = ((size_t)(x.qrow0 + qs * x.tpt + tl) * a.Hq + (size_t)x.h * G + hg) * kD;
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
         uint32_t o[32];
         tmem_ld32(orow_t + c, o);
         tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * wa);
+        if (part.split) {
+          uint32_t o2[32];
+          tmem_ld32(orow_t + kD + c, o2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(fmaf(__uint_as_float(o2[e]), wb, __uint_as_float(o[e])));
+        }
         if (row_ok && !failed) {
           if (a.out_dtype == PA_F32) {
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow + c);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+              dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           } else {
             uint32_t pk[16], none;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float v0 = __uint_as_float(o[2 * e]) * inv, v1 = __uint_as_float(o[2 * e + 1]) * inv;
+              const float v0 = __uint_as_float(o[2 * e]), v1 = __uint_as_float(o[2 * e + 1]);
               pack2<FMT == 1, false>(v0, v1, pk[e], none);
             }
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow + c);
@@ -865,6 +928,10 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       }
       tc_fence_before();
       mbar_arrive(bar(B_ODONE + qt));
+      if (part.split) {
+        mbar_arrive(bar(B_ODONE + 1));
+        ++splits;
+      }
       failed = __any_sync(0xffffffffu, failed);
     }
     if (failed) give_up();

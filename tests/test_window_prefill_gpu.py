@@ -12,7 +12,11 @@ pytestmark = pytest.mark.gpu
 
 
 def _w(vt):
-    return 2.0 ** -12 + 2.0 ** -15 if vt == "fp8" else 2.0 ** -15
+    """Error of a weight, relative. Over an 8-bit V pool it is one f16 value: 10 fraction bits, so
+    half a step is 2^-11 of a power of two and at most 2^-11 of any value (not 2^-12, which is half
+    a step of 11 fraction bits). Each term of a row is then off by up to 2^-11 of itself, and so is
+    the row by 2^-11 of the sum of the terms' magnitudes."""
+    return 2.0 ** -11 + 2.0 ** -15 if vt == "fp8" else 2.0 ** -15
 
 
 def _case(seed, prior, new, Hq, Hkv, bs, qt, kt, vt, window, sinks, blk8=False, spread=0, ks=1.0, vs=1.0,
@@ -235,3 +239,20 @@ def test_serving_run(blk8):
     step(1, fork, fork[None].cuda())
     step(1, table, bt)
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("kind,window,sinks", [("blk8", 0, 0), ("blk8", 200, 30), ("same", 200, 30), ("same", 2 ** 31 - 1, 0)])
+def test_units_of_every_kind_in_turn(kind, window, sinks):
+    # several hundred units, so that each CTA has some of one query tile and one key tile, of
+    # one query tile and several key tiles (which two groups of warps share) and of two query tiles
+    rng = np.random.default_rng(7)
+    new = [int(x) for x in rng.choice([1, 15, 16, 17, 31, 33, 40, 70], 50)]
+    prior = [int(x) for x in rng.choice([0, 1, 60, 130, 280, 400], 50)]
+    blk8 = kind == "blk8"
+    for qt in ("f16", "bf16"):
+        kt = "fp8" if blk8 else qt
+        P, q, scale, ref, tol, new = _case(11, prior, new, 64, 8, 16, qt, kt, kt, window, sinks, blk8=blk8,
+                                           spread=3 if blk8 else 0, sharp=4.0)
+        out, err = _run(P, q, scale, new, window, sinks)
+        assert err == 0
+        check(out, ref, tol, qt)

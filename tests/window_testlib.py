@@ -7,7 +7,7 @@ Attention tolerances. With fp32 output the kernels differ from the exact result 
    s itself, covered by doubling the steps), and a score error e moves a weighted
    average of values by at most 2 e max|v|;
  * the weights: two 16-bit parts hold at least 16 bits (2^-16 relative), ex2 2^-22
-   (prefill over 8-bit V: one f16 part, half a step is 2^-12: w = 2^-12 + 2^-15);
+   (prefill over 8-bit V: one f16 part, half a step is 2^-11: w = 2^-11 + 2^-15);
  * the sums over N keys: at most N roundings of 2^-24 each;
 so tol = max|v| (2 e_s + w + (N + 64) 2^-24), w = 2^-15 unless said, plus half a step of the output type.
 """
