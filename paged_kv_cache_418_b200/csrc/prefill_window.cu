@@ -28,17 +28,21 @@
 // enter as one f16 part: their 2^-11 is far below the 2^-4 of the codes they multiply, and
 // no more than half a step of either 16-bit output.
 //
-// Measured (8192-token prompt, 32 query heads over 8, 550 GFLOP): block-scaled cache 628
-// us, 875 TFLOP/s; bf16 pools 667 us; windowed bf16 chunks 270 us. Units of one query tile
-// whose rows two threads share took 762, 925 and 298 us there, and with the codes widened
-// by the softmax warps 2110. A pair of tiles takes ~5000 cycles: a softmax warp ~2100 for
-// each half (some 1100 of them its 64 exponentials, beside the other query tile's) without
-// ever waiting for scores; the tensor cores are busy for 2048 of them, shared memory for
-// ~3000 (operands of S are read once per 64 keys), the special-function units for 2048.
-// What mattered besides the layout: elect.sync for the issuing threads (a product's issue
-// took 110 cycles without it, 25 with it), an issuing warp per query tile (a step of the
-// issue, waits and commits included, is ~1100 cycles), packed fp32 operations, and reading
-// the block scales before the scores (shared-memory loads are slow beside the MMAs').
+// Where a unit has one query tile only, both groups take every other key tile of it, and
+// the first joins the two parts (small ragged chunks: 17.9 -> 16.2 us).
+//
+// Measured (8192-token prompt, 32 query heads over 8, 550 GFLOP): block-scaled cache 629
+// us, 875 TFLOP/s; bf16 pools 670 us; windowed bf16 chunks (8 x 512) 270 us. Units of one
+// query tile whose rows two threads share took 763, 925 and 298 us there, and with the codes
+// widened by the softmax warps 2110. A pair of tiles takes ~5000 cycles: a softmax warp
+// ~2100 for each half (some 1100 of them its 64 exponentials, beside the other query
+// tile's) without ever waiting for scores; the tensor cores are busy for 2048 of them,
+// shared memory for ~3000 (the operand of S that is the query is read once per 64 keys),
+// the special-function units for 2048. What mattered besides the layout: elect.sync for the
+// issuing threads (a product's issue took 110 cycles without it, 25 with it), an issuing
+// warp per query tile (a step of the issue, waits and commits included, is ~1100 cycles),
+// packed fp32 operations, and reading the block scales before the scores (shared-memory
+// loads are slow beside the MMAs').
 //
 // Block-scaled pools: K's power of two multiplies its keys' scores; V's enters as its
 // log2, s' = s + log2(vs), so the running maximum is that of the whole contribution,
@@ -146,10 +150,16 @@ struct Unit {
 // it (the two parts are joined at the end).
 struct Part {
   Reach reach;
-  int last;             // its last key tile
+  int sinks, from, last;  // its key tiles: k < sinks, from <= k <= last (split: every other one)
   bool on, split;
-  __device__ __forceinline__ bool takes(const Unit& x, int g, int k) const {
-    return on && (split ? (k & 1) == g : reach.needs(x.tile0(k), kTile));
+  __device__ __forceinline__ bool takes(int g, int k) const {
+    return split ? (k & 1) == g : k < sinks || (k >= from && k <= last);
+  }
+  // its first key tile, and the one behind k
+  __device__ __forceinline__ int first(int g) const { return split ? g : sinks > 0 ? 0 : from; }
+  __device__ __forceinline__ int next(int k) const {
+    k += split ? 2 : 1;
+    return k >= sinks && k < from ? from : k;
   }
 };
 __device__ __forceinline__ Part part_of(const Args& a, const Unit& x, int g) {
@@ -158,6 +168,11 @@ __device__ __forceinline__ Part part_of(const Args& a, const Unit& x, int g) {
   p.on = g == 0 || x.two() || p.split;
   p.reach = x.two() ? reach_of(a, x.pos(g), x.tokens(g)) : x.all;
   p.last = x.two() ? (p.reach.t1 - 1) / kTile - x.w0 + x.n0 : x.ntiles - 1 - (p.split && ((x.ntiles - 1 - g) & 1));
+  p.sinks = (p.reach.sk + kTile - 1) / kTile;
+  if (p.sinks > x.n0) p.sinks = x.n0 + max(0, p.sinks - x.w0);
+  p.from = p.reach.lo / kTile - x.w0 + x.n0;
+  if (!p.on) p.sinks = 0, p.last = -1;
+  if (p.split) p.from = 0;
   return p;
 }
 
@@ -555,7 +570,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         for (int k = 0; k <= x.ntiles && ok; ++k) {
           const bool was = pend, more = k < x.ntiles;
           const int seq = 2 * (tc_ + k), s = seq % kNST, sv = (seq - 1) % kNST;
-          pend = more && mine.takes(x, g, k);
+          pend = more && mine.takes(g, k);
           const uint32_t kst = sbase + OFF_KV + s * kOp, vst = sbase + OFF_KV + sv * kOp;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -692,9 +707,16 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
       float m = -FLT_MAX, l = 0.f;
       float f0 = a.scale_log2;                   // score factor of the row
+      if constexpr (QC) {
+        // (The first scores say that the query tile was converted. To wait for that itself
+        // would not do: a part that sat out units may be phases ahead of it.)
+        if (!mbar_wait(bar(B_SFULL + 2 * qt), tiles & 1, abort_flag)) failed = true;
+        f0 *= __uint_as_float((uint32_t)(127 - rowe[q % kNQ * 128 + r]) << 23);
+        mbar_arrive(bar(B_QEMPTY + q % kNQ));
+        if (!part.split) mbar_arrive(bar(B_QEMPTY + q % kNQ));
+      }
       bool first = true;
-      for (int k = 0; k < x.ntiles; ++k) {
-        if (!part.takes(x, qt, k)) continue;
+      for (int k = part.first(qt); k <= part.last; k = part.next(k)) {
         const int ts = x.tile0(k);
         const int n = tiles++;
         // blocks that were not loaded: the producer's word (8-bit pools), else the table's
@@ -706,13 +728,6 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           if (!mbar_wait(bar(B_SFULL + 2 * qt + h), n & 1, abort_flag)) failed = true;
           __syncwarp();
           tc_fence_after();
-          if (QC && first) {
-            // (the scores say that the query tile was converted. Waiting for that instead would
-            // not do: a part that sits out units may be phases ahead of it.)
-            f0 *= __uint_as_float((uint32_t)(127 - rowe[q % kNQ * 128 + r]) << 23);
-            mbar_arrive(bar(B_QEMPTY + q % kNQ));
-            if (!part.split) mbar_arrive(bar(B_QEMPTY + q % kNQ));
-          }
           uint32_t raw[64];
           float* s_ = reinterpret_cast<float*>(raw);
           tmem_ld32(srow + 64 * h, raw);
