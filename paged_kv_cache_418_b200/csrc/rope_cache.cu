@@ -6,7 +6,7 @@
 //   x_a' = x_a cos[p][i] - x_b sin[p][i],   x_b' = x_b cos[p][i] + x_a sin[p][i]
 // in fp32 with every product and sum rounded (no fused multiply-add): the result
 // is then a fixed sequence of roundings, which decides an 8-bit code the same
-// way for every caller and checker. Query heads are rotated to query_out, key
+// way for every caller and reader of it. Query heads are rotated to query_out, key
 // heads on their way into the pool, value heads only move.
 //
 // Both kernels move each element once: (Hq + 2 Hkv) D elements read and written
