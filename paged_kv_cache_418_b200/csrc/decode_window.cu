@@ -34,6 +34,12 @@
 //   O[16 x 8 dims] += P . V : rows 0-7 the weights, rows 8-15 what their rounding
 //     to 16 bits lost, so the MMA rows that 8 heads leave empty carry the second
 //     half of the precision and the two halves are added at the end.
+// Over f16 and 8-bit V the weights are f16, whose grid ends at 2^-24. One key that takes most of
+// the weight (the first tokens that a window keeps are there for that) would leave every other
+// weight on that grid's last steps, and their second parts with them. So the reference lies 2^7
+// under the maximum, which puts the largest weight into [2^7, 2^15], and the second parts are
+// stored 2^11 times larger (rows 8-15 have sums of their own): a weight is held to 2^-22 of itself
+// and 2^-43 of the row's largest. bf16 has fp32's range and needs neither.
 // 8-bit codes are widened to f16 (exactly) between shared memory and the MMA. The
 // 8 keys of a score product are tokens 0 4 2 6 5 1 7 3 of their tile: in that order
 // both the K reads (4 chunks of 2 rows) and the V reads (2 chunks of 4 rows) of
@@ -108,6 +114,10 @@ struct Core {
   static constexpr int RUN = K8 ? 16 : 8;       // dims of a lane's run of a K row
   static constexpr int EPV = V8 && D == 128 ? 16 : 8;   // dims of a lane's run of a V row
   static constexpr int NS = 2 * NT;             // output values per lane: slot e * NT + j
+  // The reference is set 2^kLow under a maximum and moves when passed by 2^kMove: f16
+  // weights reach 2^15, and the second part of one, at most 2^4, times kUp too.
+  static constexpr float kLow = VBF ? 0.f : 7.f, kMove = VBF ? 8.f : 15.f;
+  static constexpr float kUp = VBF ? 1.f : 2048.f;
   static_assert(NST >= 3 && kRing % STAGE == 0, "ring");
 
   uint32_t qa[KS][4];
@@ -248,7 +258,7 @@ struct Core {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     if (__any_sync(0xffffffffu, mx > m + kMove)) {
-      const float mn = mx > m + kMove ? mx : m;
+      const float mn = mx > m + kMove ? mx - kLow : m;
       const float alpha = ex2(m - mn);
       m = mn;
       l *= alpha;
@@ -270,8 +280,8 @@ struct Core {
       if (BSC) l = fmaf(sum, __uint_as_float((uint32_t)(127 - lvs[w]) << 23), l);
       else l += sum;
       uint32_t pw[4];
-      split2<VBF>(p[0][0], p[0][1], pw[0], pw[1]);
-      split2<VBF>(p[1][0], p[1][1], pw[2], pw[3]);
+      split2<VBF>(p[0][0], p[0][1], pw[0], pw[1], kUp);
+      split2<VBF>(p[1][0], p[1][1], pw[2], pw[3], kUp);
       // ---- O += P . V: the lane's tokens are those of keys 2 t, 2 t + 1 and 8 + them
       if (t0[w] < 0) continue;                  // what lies in the stage may be anything
       uint32_t keep = 15u;                      // which of the four to take: V rows that are not
@@ -333,7 +343,7 @@ struct Core {
   }
   __device__ __forceinline__ float value(int s) const {
     const int e = s / NT, j = s % NT;
-    return o[j][e] + o[j][e + 2];
+    return fmaf(o[j][e + 2], 1.f / kUp, o[j][e]);
   }
 };
 

@@ -14,8 +14,6 @@ namespace pa {
 namespace {
 
 constexpr int kTok = 16;                        // tokens per tile
-constexpr float kMove = 8.f;                    // the reference maximum moves when passed by 2^8:
-                                                // weights stay under 2^8, far inside f16
 // Work split: cost of a step of a unit, of a unit's start and end (about a step: its query,
 // and its output or piece), and the least share worth a CTA (a unit's start and two steps:
 // below that the merge costs more than the CTA saves).
@@ -80,19 +78,19 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// x0, x1 as packed 16-bit values and what their rounding lost, the same way.
+// x0, x1 as packed 16-bit values and what their rounding lost (times up), the same way.
 template <bool BF>
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo, float up = 1.f) {
   if (BF) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
     const float2 f = __bfloat1622float2(h);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
+    const __nv_bfloat162 r = __floats2bfloat162_rn((x0 - f.x) * up, (x1 - f.y) * up);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     lo = *reinterpret_cast<const uint32_t*>(&r);
   } else {
     const __half2 h = __floats2half2_rn(x0, x1);
     const float2 f = __half22float2(h);
-    const __half2 r = __floats2half2_rn(x0 - f.x, x1 - f.y);
+    const __half2 r = __floats2half2_rn((x0 - f.x) * up, (x1 - f.y) * up);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     lo = *reinterpret_cast<const uint32_t*>(&r);
   }
