@@ -21,12 +21,17 @@
 //
 // 16-bit pools: the products take the query's type, and the weights two 16-bit parts
 // (hi + lo, ~16 bits).
+// f16 weights (f16 and 8-bit V) end at 2^-24. One key that takes most of the weight (the first
+// tokens that a window keeps are there for that) would leave every other weight on the last
+// steps of that grid, so their reference lies 2^12 under the maximum: the largest weight of a row
+// is in [2^12, 2^15.9], and what the grid takes from a weight is 2^-37 of that. (Lower would move
+// the reference with every other tile: the scores of a random prompt rise by 2^2 to 2^3 after
+// the first 64 keys. Moves at this height: 8192-token prompt 640 -> 655 us.)
 // 8-bit pools: four converter warps widen each tile's codes to f16 (exactly, in place:
 // TMA leaves a row's 128 codes in the line of its second half) ahead of the tensor
 // cores; a bf16 query is rescaled by a power of two per row and becomes f16 too, exactly
 // (an element 2^-39 of its row's largest is rounded), once per unit. Weights over 8-bit V
-// enter as one f16 part: their 2^-11 is far below the 2^-4 of the codes they multiply, and
-// no more than half a step of either 16-bit output.
+// enter as one f16 part, each off by up to 2^-11 of itself.
 //
 // Where a unit has one query tile only, both groups take every other key tile of it, and
 // the first joins the two parts (small ragged chunks: 17.9 -> 16.2 us).
@@ -350,10 +355,10 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   constexpr bool QC = K8 && FMT == 1;           // the query becomes f16
   constexpr int FS = K8 ? 0 : FMT, FO = V8 ? 0 : FMT;     // operand types of the two products
   constexpr bool LO = !V8;                      // weights in two parts
-  // The reference maximum of a row moves when a tile passes it by 2^kMove: rarely, as
-  // that waits for the output product in flight. Weights stay under 2^kMove: inside f16,
-  // or, as bf16, with room for 2^60 of values and sums in fp32.
-  constexpr float kMove = FO == 1 ? 64.f : 14.f;
+  // The reference of a row is set 2^kLow under its maximum and moves when a half tile passes it
+  // by 2^kMove: rarely, as that waits for the output product in flight. f16 weights stay under
+  // 2^15.9 < 65504; bf16 ones leave room for 2^60 of values and sums in fp32.
+  constexpr float kLow = FO == 1 ? 0.f : 12.f, kMove = FO == 1 ? 64.f : 15.9f;
   using R = Roles<CONV>;
   constexpr int NB_T = kTile / BS;              // physical blocks per tile
   constexpr uint32_t kBlkBits = (uint32_t)((1ull << BS) - 1ull);   // one block's keys in a chunk mask
@@ -826,14 +831,14 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             tm = fmaxf(tm, fmaf(t0, f[c], e[c]));
           }
           if (first) {
-            m = fmaxf(tm, -FLT_MAX);
+            m = fmaxf(tm - kLow, -FLT_MAX);
           } else if (__any_sync(0xffffffffu, tm > m + kMove)) {
             // rescale the row of O, once every product before this half's is in it: those of
             // the last tile's second half (the scores of this tile's come after it), or that
             // of this tile's first half
             const bool resc = tm > m + kMove;
-            const float alpha = resc ? ex2(m - tm) : 1.f;
-            if (resc) m = tm;
+            const float alpha = resc ? ex2(m - (tm - kLow)) : 1.f;
+            if (resc) m = tm - kLow;
             if (!mbar_wait(bar(h == 0 ? B_SFULL + 2 * qt + 1 : B_OSTEP + qt), n & 1, abort_flag)) failed = true;
             __syncwarp();
             tc_fence_after();

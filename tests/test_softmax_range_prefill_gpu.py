@@ -1,0 +1,45 @@
+"""Windowed and block-scaled prefill of rows whose first key takes nearly all of the weight and has
+no value of its own, for every type of V pool (bounds: range_testlib)."""
+
+import pytest
+import torch
+
+from range_testlib import Cache, attend, check, prefill, sees, sink
+
+pytestmark = pytest.mark.gpu
+
+# Errors of a prefill's weights (fractions of the largest). f16 and 8-bit V pools: f16 weights of which
+# the largest is 2^12 or more, so that half a step of the last ones, 2^-25, is 2^-37 of it; of a weight,
+# two parts (f16 V) are off by 2^-21 and one (8-bit V) by 2^-11. bf16 V: two bf16 parts, 2^-17 and no
+# floor. ex2: 2^-22.
+PREFILL = {"f16": (2.0 ** -20, 2.0 ** -36), "fp8": (2.0 ** -11 + 2.0 ** -20, 2.0 ** -36), "bf16": (2.0 ** -16, 0.0)}
+
+
+def _run(q, c, n, T, window, sinks, vt):
+    out = prefill(c, q, [T], 128 ** -0.5, window, sinks)
+    for i in range(T):
+        ref, tol = attend(q[i].double(), c.k64[0], c.v64[0], sees(n, n - T + i, window, sinks), 128 ** -0.5,
+                          *PREFILL[vt])
+        check(out[i], ref, tol, f"token {i}")
+
+
+@pytest.mark.parametrize("n,share,T", [(1000, 0.99, 5), (4096, 0.999, 70)])
+@pytest.mark.parametrize("qt,kt,vt,Hq,Hkv", [("f16", "f16", "f16", 8, 1), ("f16", "f16", "f16", 2, 2), ("f16", "fp8", "f16", 4, 1),
+                                             ("bf16", "fp8", "fp8", 8, 1), ("f16", "fp8", "fp8", 2, 2),
+                                             ("f16", "f16", "fp8", 4, 1), ("bf16", "bf16", "bf16", 8, 1)])
+def test_sink_window_prefill(n, share, T, qt, kt, vt, Hq, Hkv):
+    q, k, v = sink(n + Hq, T, n, Hq, Hkv, 128, share, qt)
+    _run(q, Cache([(k, v)], 16, kt, vt), n, T, n // 2 + 3, 1, vt)
+
+
+@pytest.mark.parametrize("qt,Hq,Hkv,n,share,T", [("f16", 8, 1, 4096, 0.999, 70), ("bf16", 2, 2, 1000, 0.99, 200),
+                                                 ("bf16", 8, 1, 131072, 0.99, 3)])
+def test_sink_blk8_prefill(qt, Hq, Hkv, n, share, T):
+    q, k, v = sink(n + Hq, T, n, Hq, Hkv, 128, share, qt)
+    _run(q, Cache([(k, v)], 32, "fp8", "fp8", [torch.zeros(-(-n // 32), Hkv)]), n, T, 0, 0, "fp8")
+
+
+def test_sink_window_prefill_of_a_long_context():
+    n, T = 131072, 3
+    q, k, v = sink(3, T, n, 8, 1, 128, 0.999, "f16")
+    _run(q, Cache([(k, v)], 32, "f16", "f16"), n, T, n, 0, "f16")
