@@ -31,7 +31,9 @@
 // TMA leaves a row's 128 codes in the line of its second half) ahead of the tensor
 // cores; a bf16 query is rescaled by a power of two per row and becomes f16 too, exactly
 // (an element 2^-39 of its row's largest is rounded), once per unit. Weights over 8-bit V
-// enter as one f16 part, each off by up to 2^-11 of itself.
+// are two f16 parts for fp32 and f16 outputs. For bf16 outputs, whose own half step is 2^-8 of a
+// value, they are one, each off by up to 2^-11 of itself (8192-token prompt over the block-scaled
+// cache: 661 us with one part, 792 with two).
 //
 // Where a unit has one query tile only, both groups take every other key tile of it, and
 // the first joins the two parts (small ragged chunks: 17.9 -> 16.2 us).
@@ -238,7 +240,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// Two fp32 weights as packed 16-bit values, and (LO) what their rounding lost.
+// Two fp32 weights (not negative) as packed 16-bit values, and (LO) what their rounding lost.
+// f16 parts: hi is the weight cut to ten fraction bits, which takes no conversion back.
 template <bool BF, bool LO>
 __device__ __forceinline__ void pack2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
   if (BF) {
@@ -250,11 +253,13 @@ __device__ __forceinline__ void pack2(float p0, float p1, uint32_t& hi, uint32_t
       lo = *reinterpret_cast<const uint32_t*>(&l);
     }
   } else {
-    const __half2 h = __floats2half2_rn(p0, p1);
+    const float h0 = LO ? __uint_as_float(__float_as_uint(p0) & 0xffffe000u) : p0;
+    const float h1 = LO ? __uint_as_float(__float_as_uint(p1) & 0xffffe000u) : p1;
+    const __half2 h = __floats2half2_rn(h0, h1);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     if (LO) {
-      const float2 f = __half22float2(h);
-      const __half2 l = __floats2half2_rn(p0 - f.x, p1 - f.y);
+      const float2 f = fma2(make_float2(h0, h1), make_float2(-1.f, -1.f), make_float2(p0, p1));
+      const __half2 l = __floats2half2_rn(f.x, f.y);
       lo = *reinterpret_cast<const uint32_t*>(&l);
     }
   }
@@ -346,15 +351,14 @@ template <bool CONV> struct Roles {
 }  // namespace
 
 // FMT: the query's type (0 f16, 1 bf16). K8 / V8: that pool holds codes. BSC (K8 and
-// V8): with scales per block and KV head.
-template <int FMT, int BS, bool K8, bool V8, bool BSC>
+// V8): with scales per block and KV head. LO: weights in two parts.
+template <int FMT, int BS, bool K8, bool V8, bool BSC, bool LO>
 __global__ void __launch_bounds__((Roles<K8 || V8>::kThreads), 1)
 prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   constexpr bool CONV = K8 || V8;               // converter warps
   constexpr bool QC = K8 && FMT == 1;           // the query becomes f16
   constexpr int FS = K8 ? 0 : FMT, FO = V8 ? 0 : FMT;     // operand types of the two products
-  constexpr bool LO = !V8;                      // weights in two parts
   // The reference of a row is set 2^kLow under its maximum and moves when a half tile passes it
   // by 2^kMove: rarely, as that waits for the output product in flight. f16 weights stay under
   // 2^15.9 < 65504; bf16 ones leave room for 2^60 of values and sums in fp32.
@@ -1020,10 +1024,10 @@ bool make_maps(const PrefillLaunch& p, int G, CUtensorMap* q, CUtensorMap* k, CU
   return true;
 }
 
-template <int FMT, int BS, bool K8, bool V8, bool BSC>
+template <int FMT, int BS, bool K8, bool V8, bool BSC, bool LO>
 int launch_t(const Args& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
              cudaStream_t stream) {
-  auto kern = prefill_window_kernel<FMT, BS, K8, V8, BSC>;
+  auto kern = prefill_window_kernel<FMT, BS, K8, V8, BSC, LO>;
   // dynamic shared memory above 48 KB needs the attribute, on the current device
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return PA_ERR_CUDA;
@@ -1033,14 +1037,20 @@ int launch_t(const Args& a, const CUtensorMap& q, const CUtensorMap& k, const CU
                  cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+template <int FMT, bool K8, bool V8, bool BSC, bool LO>
+int launch_bs(const Args& a, int bs, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+              cudaStream_t stream) {
+  return bs == 16 ? launch_t<FMT, 16, K8, V8, BSC, LO>(a, q, k, v, stream)
+                  : launch_t<FMT, 32, K8, V8, BSC, LO>(a, q, k, v, stream);
+}
+
 template <bool K8, bool V8, bool BSC>
 int launch_kv(const Args& a, int dtype, int bs, const CUtensorMap& q, const CUtensorMap& k,
               const CUtensorMap& v, cudaStream_t stream) {
-  if (dtype == PA_BF16)
-    return bs == 16 ? launch_t<1, 16, K8, V8, BSC>(a, q, k, v, stream)
-                    : launch_t<1, 32, K8, V8, BSC>(a, q, k, v, stream);
-  return bs == 16 ? launch_t<0, 16, K8, V8, BSC>(a, q, k, v, stream)
-                  : launch_t<0, 32, K8, V8, BSC>(a, q, k, v, stream);
+  if (dtype != PA_BF16) return launch_bs<0, K8, V8, BSC, true>(a, bs, q, k, v, stream);
+  // one part: see the head of this file
+  if (V8 && a.out_dtype == PA_BF16) return launch_bs<1, K8, V8, BSC, !V8>(a, bs, q, k, v, stream);
+  return launch_bs<1, K8, V8, BSC, true>(a, bs, q, k, v, stream);
 }
 
 }  // namespace
