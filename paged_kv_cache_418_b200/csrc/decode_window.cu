@@ -63,8 +63,12 @@
 // tokens. V's would have to multiply the weights before they are rounded to
 // 16 bits, where a small scale would push them under f16's range; instead the
 // running maximum is taken over log2 of the whole contribution, s' = s + log2(vs)
-// (an exact integer): weights w = 2^(s' - m') are normalised to the largest
-// contribution, and the exp-sum counts w 2^-log2(vs).
+// (an exact integer): weights w = 2^(s' - m) are normalised to the largest
+// contribution. The exp-sum has a reference r of its own, over the scores alone,
+// l = sum 2^(s - r): a block of tiny V counts in it although its contribution is nothing
+// (w 2^-log2(vs) would lose it once w is under fp32's range). The row is O / l 2^(m - r); both
+// references are whole numbers, so that factor is exact. The second exponential per score
+// is 4 of a lane and box, beside the widening of 128 codes.
 //
 // Every pipeline wait is bounded (1 s): one that gives up sets PA_DEV_TIMEOUT,
 // raises the CTA's abort flag, and the producer waits for its copies in flight.
@@ -120,8 +124,11 @@ struct Core {
   static constexpr float kUp = VBF ? 1.f : 2048.f;
   static_assert(NST >= 3 && kRing % STAGE == 0, "ring");
 
+  static constexpr float kSumMove = 40.f;       // r moves when passed by 2^40: l < 2^40 tokens
+
   uint32_t qa[KS][4];
   float factor, m, l;
+  float r;                                      // BSC: the exp-sum's reference
   float o[NT][4];
   // offsets of this lane's operands in a head's box
   uint32_t kx;                                  // K: key tok_of(g), chunk t (chunk 4 + t: ^ 64)
@@ -189,7 +196,7 @@ struct Core {
       split2<KBF>(x[4 * ks], x[4 * ks + 1], qa[ks][0], qa[ks][1]);
       split2<KBF>(x[4 * ks + 2], x[4 * ks + 3], qa[ks][2], qa[ks][3]);
     }
-    m = -FLT_MAX;
+    m = r = -FLT_MAX;
     l = 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -235,7 +242,7 @@ struct Core {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           s[w][nt][e] = (c[nt][e] + c[nt][e + 2]) * f;
-          if (BSC) s[w][nt][e] += (float)lvs[w];
+          if (BSC) s[w][nt][e] += (float)lvs[w];      // s'
         }
     }
     bool whole[TW];
@@ -251,34 +258,44 @@ struct Core {
       }
     }
     // ---- online softmax
-    float mx = -CUDART_INF_F;
+    float mx = -CUDART_INF_F, mr = -CUDART_INF_F;
 #pragma unroll
-    for (int w = 0; w < TW; ++w)
-      mx = fmaxf(mx, fmaxf(fmaxf(s[w][0][0], s[w][0][1]), fmaxf(s[w][1][0], s[w][1][1])));
+    for (int w = 0; w < TW; ++w) {
+      const float most = fmaxf(fmaxf(s[w][0][0], s[w][0][1]), fmaxf(s[w][1][0], s[w][1][1]));
+      mx = fmaxf(mx, most);
+      if (BSC) mr = fmaxf(mr, most - (float)lvs[w]);
+    }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (__any_sync(0xffffffffu, mx > m + kMove)) {
-      const float mn = mx > m + kMove ? mx - kLow : m;
+    if (__any_sync(0xffffffffu, mx > m + kMove || (BSC && mr > r + kSumMove))) {
+      const float mn = mx > m + kMove ? floorf(mx) - kLow : m;
       const float alpha = ex2(m - mn);
       m = mn;
-      l *= alpha;
+      if (!BSC) l *= alpha;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         o[j][0] *= alpha; o[j][1] *= alpha; o[j][2] *= alpha; o[j][3] *= alpha;
+      }
+      if (BSC) {
+        mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, 1));
+        mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, 2));
+        const float rn = mr > r + kSumMove ? floorf(mr) : r;
+        l *= ex2(r - rn);
+        r = rn;
       }
     }
 #pragma unroll
     for (int w = 0; w < TW; ++w) {
       float p[2][2], sum = 0.f;
+      const float back = (float)lvs[w] + r;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           p[nt][e] = ex2(s[w][nt][e] - m);
-          sum += p[nt][e];
+          sum += BSC ? ex2(s[w][nt][e] - back) : p[nt][e];
         }
-      if (BSC) l = fmaf(sum, __uint_as_float((uint32_t)(127 - lvs[w]) << 23), l);
-      else l += sum;
+      l += sum;
       uint32_t pw[4];
       split2<VBF>(p[0][0], p[0][1], pw[0], pw[1], kUp);
       split2<VBF>(p[1][0], p[1][1], pw[2], pw[3], kUp);
@@ -347,6 +364,34 @@ struct Core {
   }
 };
 
+// A row's sums as the output wants them: O * f[0] * f[1] is O / l * 2^(m - r) * scale (two
+// factors, as 2^(m - r) alone may leave fp32's range).
+struct Norm {
+  float f[2];
+  __device__ __forceinline__ float operator()(float o) const { return o * f[0] * f[1]; }
+};
+template <bool BSC> __device__ __forceinline__ Norm norm_of(float m, float r, float l, float scale) {
+  Norm n = {{l == 0.f ? 0.f : scale / l, 1.f}};
+  if (BSC) {
+    const float h = truncf((m - r) * 0.5f);
+    n.f[0] *= ex2(h);
+    n.f[1] = ex2(m - r - h);
+  }
+  return n;
+}
+
+// A piece of a cut unit holds normalised rows, and of each the exp-sum as l * 2^ref with l in
+// [1, 2) (0: nothing attended; scores in the 10^5s: l as it is).
+__device__ __forceinline__ void put_sum(float* ws_m, float* ws_l, size_t i, float ref, float l) {
+  const uint32_t b = __float_as_uint(l);
+  if (l > 0.f && l <= FLT_MAX && fabsf(ref) < 65536.f) {    // (ref + exponent is exact there)
+    ref += (float)((int)(b >> 23) - 127);
+    l = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
+  }
+  ws_m[i] = ref;
+  ws_l[i] = l;
+}
+
 // n consecutive values to out[i ..]: 8 to a 16-bit output or 4 to an fp32 one at once.
 __device__ __forceinline__ void store8_out(void* out, size_t i, const float* f, int dt) {
   if (dt == PA_F32) {
@@ -394,7 +439,7 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
   auto full = [&](int s) { return bars + 16u * (uint32_t)s; };
   auto empty = [&](int s) { return bars + 16u * (uint32_t)s + 8u; };
   __shared__ uint32_t sm_abort;
-  __shared__ float sm_m[kCons][kHeads], sm_l[kCons][kHeads];
+  __shared__ float sm_m[kCons][kHeads], sm_l[kCons][kHeads], sm_r[BSC ? kCons : 1][kHeads];
   volatile uint32_t* abort_flag = &sm_abort;
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -585,12 +630,12 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
       const size_t slot = 2 * (size_t)cta + (cta == first ? 1 : 0);
       const size_t prow = slot * (hg * kHeads) + hd * kHeads;          // of the pieces
       if (nsub == 1) {
-        const float inv = !whole ? 1.f : core.l == 0.f ? 0.f : a.v_scale / core.l;
+        const Norm norm = norm_of<BSC>(core.m, core.r, core.l, a.v_scale);
 #pragma unroll
         for (int s = 0; s < C::NS; s += 8) {
           float f[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = core.value(s + k) * inv;
+          for (int k = 0; k < 8; ++k) f[k] = norm(core.value(s + k));
           const int d = C::dim_of(s, lane);
           if (whole) {
             if (g < gc) store8_out(a.out, (row0 + g) * D + d, f, a.out_dtype);
@@ -598,26 +643,31 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
             store8_out(a.ws_acc, (prow + g) * D + d, f, PA_F32);
           }
         }
-        if (!whole && (lane & 3) == 0) {
-          a.ws_m[prow + g] = core.m;
-          a.ws_l[prow + g] = core.l;
-        }
+        if (!whole && (lane & 3) == 0)
+          put_sum(a.ws_m, a.ws_l, prow + g, BSC ? core.r : core.m, core.l);
       } else {
         // the sub-tiles' warps of a head join their sums, each a part of the values
         cons_sync();                            // the last unit's sums have been read
-        if ((lane & 3) == 0) { sm_m[warp][g] = core.m; sm_l[warp][g] = core.l; }
+        if ((lane & 3) == 0) {
+          sm_m[warp][g] = core.m;
+          sm_l[warp][g] = core.l;
+          if (BSC) sm_r[warp][g] = core.r;
+        }
 #pragma unroll
         for (int s = 0; s < C::NS; ++s) sm_join[(warp * C::NS + s) * 32 + lane] = core.value(s);
         cons_sync();
-        float M = -FLT_MAX, L = 0.f;
-        for (int x = 0; x < nsub; ++x) M = fmaxf(M, sm_m[x * hg + hd][g]);
+        float M = -FLT_MAX, R = -FLT_MAX, L = 0.f;
+        for (int x = 0; x < nsub; ++x) {
+          M = fmaxf(M, sm_m[x * hg + hd][g]);
+          if (BSC) R = fmaxf(R, sm_r[x * hg + hd][g]);
+        }
         float cf[kCons];
 #pragma unroll
         for (int x = 0; x < kCons; ++x) {
           cf[x] = x < nsub ? ex2(sm_m[x * hg + hd][g] - M) : 0.f;
-          if (x < nsub) L = fmaf(sm_l[x * hg + hd][g], cf[x], L);
+          if (x < nsub) L = fmaf(sm_l[x * hg + hd][g], BSC ? ex2(sm_r[x * hg + hd][g] - R) : cf[x], L);
         }
-        const float inv = !whole ? 1.f : L == 0.f ? 0.f : a.v_scale / L;
+        const Norm norm = norm_of<BSC>(M, R, L, a.v_scale);
         for (int s = sub * (C::NS / nsub); s < (sub + 1) * (C::NS / nsub); ++s) {
           float O = 0.f;
 #pragma unroll
@@ -625,22 +675,22 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
             if (x < nsub) O = fmaf(sm_join[((x * hg + hd) * C::NS + s) * 32 + lane], cf[x], O);
           const int d = C::dim_of(s, lane);
           if (whole) {
-            if (g < gc) store_out(a.out, (row0 + g) * D + d, O * inv, a.out_dtype);
+            if (g < gc) store_out(a.out, (row0 + g) * D + d, norm(O), a.out_dtype);
           } else {
-            a.ws_acc[(prow + g) * D + d] = O;
+            a.ws_acc[(prow + g) * D + d] = norm(O);
           }
         }
-        if (!whole && sub == 0 && (lane & 3) == 0) {
-          a.ws_m[prow + g] = M;
-          a.ws_l[prow + g] = L;
-        }
+        if (!whole && sub == 0 && (lane & 3) == 0)
+          put_sum(a.ws_m, a.ws_l, prow + g, BSC ? R : M, L);
       }
     }
   }
 }
 
 // Units cut between CTAs: NW warps per (sequence, query head) join its pieces,
-// every NW-th each, four pieces' loads in flight at a time.
+// every NW-th each, four pieces' loads in flight at a time. A piece is a normalised row and its
+// exp-sum l 2^m: the row is the pieces' mean by those. (The weights are kept under 2^-8, so that the
+// largest values do not leave fp32 before the division.)
 template <int D, int NW>
 __global__ void __launch_bounds__(NW < 4 ? 128 : NW * 32) decode_window_merge_kernel(const WinArgs a) {
   constexpr int PER = D / 32, RPB = NW < 4 ? 4 / NW : 1;         // rows per block
@@ -693,8 +743,8 @@ __global__ void __launch_bounds__(NW < 4 ? 128 : NW * 32) decode_window_merge_ke
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (c0 + k * NW > cut.y) continue;
-      const float f = ex2(m[k] - M);
-      L = fmaf(l[k], f, L);
+      const float f = l[k] * ex2(m[k] - M - 9.f);
+      L += f;
 #pragma unroll
       for (int e = 0; e < PER; ++e) O[e] = fmaf(v[k][e], f, O[e]);
     }
@@ -719,7 +769,7 @@ __global__ void __launch_bounds__(NW < 4 ? 128 : NW * 32) decode_window_merge_ke
       for (int e = 0; e < PER; ++e) O[e] = fmaf(sm_o[x][lane * PER + e], f, O[e]);
     }
   }
-  const float inv = L == 0.f ? 0.f : a.v_scale / L;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
   for (int e = 0; e < PER; ++e)
     store_out(a.out, (size_t)row * D + lane * PER + e, O[e] * inv, a.out_dtype);

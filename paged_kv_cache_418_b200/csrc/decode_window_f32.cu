@@ -223,7 +223,7 @@ decode_window_f32_kernel(const WinArgs a) {
         if (first == last) {
           if (g < gc) store_out(a.out, row0 * D + x, L == 0.f ? 0.f : O / L, a.out_dtype);
         } else {
-          a.ws_acc[slot * (HEADS * D) + x] = O;
+          a.ws_acc[slot * (HEADS * D) + x] = L == 0.f ? 0.f : O / L;   // (pieces are normalised)
           if (x % D == 0) {
             a.ws_m[slot * HEADS + g] = M;
             a.ws_l[slot * HEADS + g] = L;

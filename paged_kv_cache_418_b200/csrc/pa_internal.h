@@ -213,8 +213,8 @@ struct WinArgs {
   int max_context_len;
   int hg, heads;                // a unit of work: hg KV heads, up to `heads` query heads of each
   int grid;                     // CTAs
-  float* ws_acc;                // [2 * grid] pieces [hg * heads][D]
-  float* ws_m;                  // [2 * grid][hg * heads]
+  float* ws_acc;                // [2 * grid] pieces [hg * heads][D], normalised rows
+  float* ws_m;                  // [2 * grid][hg * heads]: exp-sums ws_l * 2^ws_m
   float* ws_l;
   int2* cuts;                   // per unit: the CTAs that hold its first and last step
   unsigned long long wait_ns;   // limit of every pipeline wait
