@@ -364,22 +364,6 @@ struct Core {
   }
 };
 
-// A row's sums as the output wants them: O * f[0] * f[1] is O / l * 2^(m - r) * scale (two
-// factors, as 2^(m - r) alone may leave fp32's range).
-struct Norm {
-  float f[2];
-  __device__ __forceinline__ float operator()(float o) const { return o * f[0] * f[1]; }
-};
-template <bool BSC> __device__ __forceinline__ Norm norm_of(float m, float r, float l, float scale) {
-  Norm n = {{l == 0.f ? 0.f : scale / l, 1.f}};
-  if (BSC) {
-    const float h = truncf((m - r) * 0.5f);
-    n.f[0] *= ex2(h);
-    n.f[1] = ex2(m - r - h);
-  }
-  return n;
-}
-
 // A piece of a cut unit holds normalised rows, and of each the exp-sum as l * 2^ref with l in
 // [1, 2) (0: nothing attended; scores in the 10^5s: l as it is).
 __device__ __forceinline__ void put_sum(float* ws_m, float* ws_l, size_t i, float ref, float l) {

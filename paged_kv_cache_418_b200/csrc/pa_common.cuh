@@ -143,6 +143,30 @@ __device__ __forceinline__ int block_scale_log2(float s) {
   return (int)(__float_as_uint(s) >> 23) - 127;
 }
 
+// 2^x to 2 units in the last place; results under fp32's normal range are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A row's sums as the output wants them: O * f[0] * f[1] is O / l * 2^(m - r) * scale, with m
+// the reference of O and (BSC: block scales) r a whole number of powers of two away that of l
+// (two factors, as 2^(m - r) alone may leave fp32's range).
+struct Norm {
+  float f[2];
+  __device__ __forceinline__ float operator()(float o) const { return o * f[0] * f[1]; }
+};
+template <bool BSC> __device__ __forceinline__ Norm norm_of(float m, float r, float l, float scale) {
+  Norm n = {{l == 0.f ? 0.f : scale / l, 1.f}};
+  if (BSC) {
+    const float h = truncf((m - r) * 0.5f);
+    n.f[0] *= ex2(h);
+    n.f[1] = ex2(m - r - h);
+  }
+  return n;
+}
+
 // Programmatic dependent launch. Every kernel of the library lets the next
 // kernel in its stream be scheduled as soon as all of its own CTAs are running
 // (pdl_trigger), and touches global memory only after the previous kernel has

@@ -144,12 +144,6 @@ __device__ __forceinline__ long long fa_unit_of_cta(long long k, int cta, int gr
   return k * grid + ((k & 1) ? grid - 1 - cta : cta);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two fp32 weights -> packed 16-bit hi parts and lo parts (element 0 in the low half).
 template <int FMT>
 __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {

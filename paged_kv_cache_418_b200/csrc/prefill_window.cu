@@ -52,9 +52,16 @@
 // loads are slow beside the MMAs').
 //
 // Block-scaled pools: K's power of two multiplies its keys' scores; V's enters as its
-// log2, s' = s + log2(vs), so the running maximum is that of the whole contribution,
-// the weights 2^(s' - m) are normalised to the largest one, and the row sum counts each
-// over its V scale. The producer leaves a tile's scales and the mask of its missing
+// log2, s' = s + log2(vs), so the running maximum is that of the whole contribution and
+// the weights 2^(s' - m) are normalised to the largest one. The row sum has a reference r of
+// its own, over the scores alone, l = sum 2^(s - r): a block of tiny V counts in it although
+// its contribution is nothing. 16 keys of one block share the factor 2^(m - log2(vs) - r)
+// between the two; only where their contributions are all under 2^-96 of the reference (and
+// fp32 is about to lose them) but a score over 2^-45 of r's are their exponentials taken a
+// second time. A tile can hold such keys only if its least log2(vs) is under m - r - 51.
+// The row is O / l 2^(m - r), exactly, as both references are whole numbers. (8192-token
+// prompt: 650 us with the row sum taken from the weights, 677 so; all of this in the loop over
+// the scores, unrolled, 778.) The producer leaves a tile's scales and the mask of its missing
 // blocks in a ring of shared-memory slots.
 //
 // CTA, persistent over rounds of units in alternating directions: warps 0-7 softmax,
@@ -98,7 +105,8 @@ constexpr int OFF_SLOT = (OFF_MISC + 8 + 15) / 16 * 16;
 struct Slot {                                   // of a tile: what the producer knows of its blocks
   float ks[8], lvs[8];                          // K scale, log2 of the V scale
   uint32_t missing;                             // blocks that were not loaded
-  uint32_t pad[3];
+  float lvmin;                                  // the least of lvs
+  uint32_t pad[2];
 };
 constexpr int OFF_ROWE = OFF_SLOT + kSlots * (int)sizeof(Slot);  // [kNQ][128] exponents of rescaled rows
 constexpr int OFF_XCH = OFF_ROWE + kNQ * 128;                    // [2][128] maxima and sums of a second part
@@ -218,12 +226,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -272,6 +274,19 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t* r) {
       ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// 2^n of a whole number n, 0 under 2^-126 (n <= 127): without the special-function unit.
+__device__ __forceinline__ float pow2_of(float n) {
+  return __uint_as_float(__float_as_uint(fmaxf(n + 8388735.f, 8388608.f)) << 23);    // (2^23 + 127)
+}
+
+// One column of this thread's TMEM lane.
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r) : "r"(taddr) : "memory");
+  return __uint_as_float(r);
 }
 
 // Widen row `row` of a stage's codes (its line of the second half) to f16, in place;
@@ -341,6 +356,26 @@ __device__ __forceinline__ void tmem_wait_ld64(uint32_t* r) {
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])::"memory");
 }
 
+// The row sum l 2^r of a part in one word, r given as a whole number of powers of two from the
+// part's m (kMove, kSumMove and the V scales keep it within +-256 with l's own exponent): nine bits of
+// exponent over l's fraction, 0 for no sum, 511 for one that is not finite.
+__device__ __forceinline__ float pack_sum(float l, float r) {
+  const uint32_t b = __float_as_uint(l);
+  uint32_t w = 0;
+  if (!(l <= FLT_MAX)) w = 511u << 23;
+  else if (l > 0.f)
+    w = (uint32_t)max(1, min(510, (int)(b >> 23) - 127 + (int)r + 256)) << 23 | (b & 0x7fffffu);
+  return __uint_as_float(w);
+}
+// Its l, in [1, 2), and reference (r: the part's m).
+__device__ __forceinline__ float unpack_sum(float word, float& r) {
+  const uint32_t w = __float_as_uint(word);
+  if (w == 0) return 0.f;
+  if (w >> 23 == 511u) return CUDART_NAN_F;
+  r += (float)((int)(w >> 23) - 256);
+  return __uint_as_float((w & 0x7fffffu) | 0x3f800000u);
+}
+
 // Warps of the CTA and their registers, moved between warpgroups: without converters
 // 384 threads are launched with 168 each: 256 * 208 + 128 * 88 = 64,512; with them 512
 // with 128: 256 * 184 + 128 * 80 + 128 * 64 = 65,536.
@@ -363,6 +398,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   // by 2^kMove: rarely, as that waits for the output product in flight. f16 weights stay under
   // 2^15.9 < 65504; bf16 ones leave room for 2^60 of values and sums in fp32.
   constexpr float kLow = FO == 1 ? 0.f : 12.f, kMove = FO == 1 ? 64.f : 15.9f;
+  constexpr float kSumMove = 8.f;               // BSC: r moves when passed by 2^8
   using R = Roles<CONV>;
   constexpr int NB_T = kTile / BS;              // physical blocks per tile
   constexpr uint32_t kBlkBits = (uint32_t)((1ull << BS) - 1ull);   // one block's keys in a chunk mask
@@ -499,6 +535,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             phys = -1;
           }
           const uint32_t here = __ballot_sync(0xffffffffu, phys >= 0);
+          const int lvmin = BSC ? __reduce_min_sync(0xffffffffu, phys >= 0 ? block_scale_log2(vs) : 0x7fffffff) : 0;
           // per 128-byte line of rows of the blocks that are loaded
           const uint32_t bytes = (uint32_t)__popc(here) * (BS * 128u);
           for (int kv = 0; kv < 2; ++kv) {
@@ -513,7 +550,10 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
                 slot.ks[lane] = phys >= 0 ? ks : 1.f;
                 slot.lvs[lane] = phys >= 0 ? (float)block_scale_log2(vs) : 0.f;
               }
-              if (lane == 0) slot.missing = ~here;
+              if (lane == 0) {
+                slot.missing = ~here;
+                if (BSC) slot.lvmin = (float)lvmin;
+              }
               __syncwarp();
             }
             if (lane == 0) mbar_expect_tx(bar(B_FULL + s), codes ? bytes : 2u * bytes);
@@ -715,6 +755,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       const int last_lo = a.window > 0 ? max(0, part.reach.t1 - a.window) : 0;
       const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
       float m = -FLT_MAX, l = 0.f;
+      float rs = -FLT_MAX, back_m = 0.f;         // BSC: the row sum's reference, m - it
       float f0 = a.scale_log2;                   // score factor of the row
       if constexpr (QC) {
         // (The first scores say that the query tile was converted. To wait for that itself
@@ -776,13 +817,13 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           // Scores in the log2 domain, s' = s + log2(V scale) with block scales, are
           // raw f + e with f and e per 16 keys; where some are masked they are formed and
           // masked first, and f = 1, e = 0 from then on.
-          float f[4], e[4], back[4];             // back: what a weight counts in the row sum
+          float f[4], e[4], lv[4];               // lv: log2 of the V scale
+          const float lvmin = BSC ? slot.lvmin : 0.f;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int blk = (64 * h + 16 * c) / BS;
             f[c] = BSC ? f0 * slot.ks[blk] : f0;
-            e[c] = BSC ? slot.lvs[blk] : 0.f;
-            back[c] = __uint_as_float((uint32_t)(127 - (int)e[c]) << 23);
+            e[c] = lv[c] = BSC ? slot.lvs[blk] : 0.f;
           }
           tmem_wait_ld64(raw);
           if (!open) {
@@ -812,7 +853,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
               e[c] = 0.f;
             }
           }
-          float tm = -CUDART_INF_F;
+          float tm = -CUDART_INF_F, tc[4];       // the half's maximum, and those of 16 keys
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             // (f has one sign in all of a launch, but for the masked tiles' f = 1)
@@ -832,32 +873,67 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
               }
               t0 = fminf(t0, t1);
             }
-            tm = fmaxf(tm, fmaf(t0, f[c], e[c]));
+            tc[c] = fmaf(t0, f[c], e[c]);
+            tm = fmaxf(tm, tc[c]);
           }
-          if (first) {
-            m = fmaxf(tm - kLow, -FLT_MAX);
-          } else if (__any_sync(0xffffffffu, tm > m + kMove)) {
-            // rescale the row of O, once every product before this half's is in it: those of
-            // the last tile's second half (the scores of this tile's come after it), or that
-            // of this tile's first half
-            const bool resc = tm > m + kMove;
-            const float alpha = resc ? ex2(m - (tm - kLow)) : 1.f;
-            if (resc) m = tm - kLow;
-            if (!mbar_wait(bar(h == 0 ? B_SFULL + 2 * qt + 1 : B_OSTEP + qt), n & 1, abort_flag)) failed = true;
-            __syncwarp();
-            tc_fence_after();
+          // the references, in one vote: all of this is rare, but for masked halves
+          bool move = tm > m + kMove;
+          if constexpr (BSC) move = move || tm - lvmin > rs + kSumMove || lvmin < back_m - 51.f;
+          if (first || __any_sync(0xffffffffu, move)) {
+            const float mn = floorf(tm) - kLow;
+            if (first) {
+              m = fmaxf(mn, -FLT_MAX);
+            } else if (__any_sync(0xffffffffu, tm > m + kMove)) {
+              // rescale the row of O, once every product before this half's is in it: those of
+              // the last tile's second half (the scores of this tile's come after it), or that
+              // of this tile's first half
+              const bool resc = tm > m + kMove;
+              const float alpha = resc ? ex2(m - mn) : 1.f;
+              if (resc) m = mn;
+              if (!mbar_wait(bar(h == 0 ? B_SFULL + 2 * qt + 1 : B_OSTEP + qt), n & 1, abort_flag)) failed = true;
+              __syncwarp();
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kD; c += 16) {
-              float o[16];
-              tmem_ld16(orow_t + c, o);
-              uint32_t w[16];
+              for (int c = 0; c < kD; c += 16) {
+                float o[16];
+                tmem_ld16(orow_t + c, o);
+                uint32_t w[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-              tmem_put16(orow_t + c, w);
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                tmem_put16(orow_t + c, w);
+              }
+              if (!BSC) l *= alpha;
             }
-            l *= alpha;
+            first = false;
+            if constexpr (BSC) {
+              const float top = fmaxf(fmaxf(tc[0] - lv[0], tc[1] - lv[1]), fmaxf(tc[2] - lv[2], tc[3] - lv[3]));
+              if (top > rs + kSumMove) {
+                const float rn = floorf(top);
+                l *= ex2(rs - rn);
+                rs = rn;
+              }
+              back_m = m - rs;
+              uint32_t far = 0;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if (tc[c] < m - 96.f) {
+                  if (tc[c] - lv[c] > rs - 45.f) far |= 1u << c;
+                  lv[c] = CUDART_INF_F;          // counted below, or nothing to count
+                }
+              }
+              // (a loop over the scores in tensor memory: unrolled over the registers it
+              // slowed the prompt, which hardly comes here, by 9%)
+              if (__any_sync(0xffffffffu, far != 0)) {
+#pragma unroll 1
+                for (int j = 64 * h; j < 64 * h + 64; ++j) {
+                  const float x = tmem_ld1(srow + j);
+                  const int t = ts + j;
+                  const bool sees = row_ok && t <= pos && (t >= wlo || t < a.sinks) && !((missing >> (j / BS)) & 1u);
+                  if (((far >> ((j >> 4) & 3)) & 1u) && sees) l += ex2(fmaf(x, f0 * slot.ks[j / BS], -rs));
+                }
+              }
+            }
           }
-          first = false;
           // weights and the row sum; a 32-key chunk's weights go over its scores, hi parts in
           // its first 16 columns, lo parts in the next 16
 #pragma unroll
@@ -878,7 +954,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
                 sum = add2(sum, p);
                 pack2<FO == 1, LO>(p.x, p.y, hi[8 * q + j], lo[8 * q + j]);
               }
-              l = BSC ? fmaf(sum.x + sum.y, back[2 * c + q], l) : l + (sum.x + sum.y);
+              l = BSC ? fmaf(sum.x + sum.y, pow2_of(back_m - lv[2 * c + q]), l) : l + (sum.x + sum.y);
             }
             tmem_put16(srow + 64 * h + 32 * c, hi);
             if (LO) tmem_put16(srow + 64 * h + 32 * c + 16, lo);
@@ -895,25 +971,27 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       if (part.split && qt == 1) {
         // the second part: its maximum and sum to the first, which reads its O
         xch[r] = m;
-        xch[128 + r] = l;
+        xch[128 + r] = BSC ? pack_sum(l, rs - m) : l;
         tc_fence_before();
         mbar_arrive(bar(B_XCH));
         failed = __any_sync(0xffffffffu, failed);
         continue;
       }
-      float wa = 1.f, wb = 0.f;
+      Norm na, nb;                               // of this part's O and of the second's
       if (part.split) {
         if (!mbar_wait(bar(B_XCH), splits & 1, abort_flag)) failed = true;
         __syncwarp();
         tc_fence_after();
-        const float m2 = xch[r], top = fmaxf(m, m2);
-        wa = ex2(m - top);
-        wb = ex2(m2 - top);
-        l = fmaf(l, wa, xch[128 + r] * wb);
+        const float m2 = xch[r];
+        float l2 = xch[128 + r], r1 = BSC ? rs : m, r2 = m2;
+        if (BSC) l2 = unpack_sum(l2, r2);
+        const float top = fmaxf(r1, r2);
+        l = fmaf(l, ex2(r1 - top), l2 * ex2(r2 - top));
+        na = norm_of<true>(m, top, l, a.v_scale);
+        nb = norm_of<true>(m2, top, l, a.v_scale);
+      } else {
+        na = norm_of<BSC>(m, rs, l, a.v_scale);
       }
-      const float inv = l == 0.f ? 0.f : a.v_scale / l;
-      wa *= inv;
-      wb *= inv;
       const size_t orow = ((size_t)(x.qrow0 + qs * x.tpt + tl) * a.Hq + (size_t)x.h * G + hg) * kD;
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
@@ -921,14 +999,14 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         tmem_ld32(orow_t + c, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * wa);
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(na(__uint_as_float(o[e])));
         if (part.split) {
           uint32_t o2[32];
           tmem_ld32(orow_t + kD + c, o2);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            o[e] = __float_as_uint(fmaf(__uint_as_float(o2[e]), wb, __uint_as_float(o[e])));
+            o[e] = __float_as_uint(nb(__uint_as_float(o2[e])) + __uint_as_float(o[e]));
         }
         if (row_ok && !failed) {
           if (a.out_dtype == PA_F32) {

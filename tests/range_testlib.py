@@ -153,3 +153,28 @@ def sink(seed, T, n, Hq, Hkv, D, share, qt):
     k[0, :, 0] = float(np.log(share / (1 - share) * n * 1.65) * D ** 0.5 / 8)
     v[0] = 0
     return q.to(DT[qt]), k, v
+
+
+def spread(seed, lens, Hkv, D, kind, qt, new=None, G=4):
+    """Sequences over the block-scaled cache (blocks of 16): "zeros20" / "zeros100": every other block has
+    no value at all (scale 2^-100, as the append leaves it) beside values near 2^20 / 2^100, its scores 4
+    higher; "low": 1000 such tokens whose scores are 7 lower; "any": scales 2^-100 .. 2^120 at random."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(sum(new) if new else len(lens), G * Hkv, D, generator=g).to(DT[qt])
+    q[..., 0] = 4
+    seqs, exps = [], []
+    for n in lens:
+        nb = -(-n // 16)
+        k, v = torch.randn(n, Hkv, D, generator=g), torch.randn(n, Hkv, D, generator=g)
+        block = torch.arange(n) // 16
+        if kind == "any":
+            e = torch.randint(-100, 121, (nb, Hkv), generator=g)
+            k[..., 0] = 0
+        else:
+            none = torch.arange(nb) % 2 == 0 if kind != "low" else torch.arange(nb) >= 4
+            e = torch.where(none, -100, int(kind[5:]) if kind != "low" else 20)[:, None].expand(nb, Hkv).contiguous()
+            v[none[block]] = 0
+            k[..., 0] = torch.where(none[block], -7.0 if kind == "low" else 4.0, 0.0)[:, None] * D ** 0.5 / 4
+        seqs.append((k, v * torch.exp2(e.float())[block][..., None]))
+        exps.append(e)
+    return q, Cache(seqs, 16, "fp8", "fp8", exps)

@@ -5,7 +5,7 @@ no value of its own, for every type of V pool."""
 import pytest
 import torch
 
-from range_testlib import DT, Cache, attend, check, decode, sees, sink
+from range_testlib import Cache, attend, check, decode, sees, sink, spread
 
 pytestmark = pytest.mark.gpu
 
@@ -43,37 +43,12 @@ def test_sink_window_decode_of_a_long_context():
     check(decode(c, q, 128 ** -0.5, n, 0)[0], ref, tol)
 
 
-def _spread(seed, lens, Hkv, D, kind, qt):
-    """Sequences over the block-scaled cache (blocks of 16): "zeros20" / "zeros100": every other block has
-    no value at all (scale 2^-100, as the append leaves it) beside values near 2^20 / 2^100, its scores 4
-    higher; "low": 1000 such tokens whose scores are 7 lower; "any": scales 2^-100 .. 2^120 at random."""
-    g = torch.Generator().manual_seed(seed)
-    q = torch.randn(len(lens), 4 * Hkv, D, generator=g).to(DT[qt])
-    q[..., 0] = 4
-    seqs, exps = [], []
-    for n in lens:
-        nb = -(-n // 16)
-        k, v = torch.randn(n, Hkv, D, generator=g), torch.randn(n, Hkv, D, generator=g)
-        block = torch.arange(n) // 16
-        if kind == "any":
-            e = torch.randint(-100, 121, (nb, Hkv), generator=g)
-            k[..., 0] = 0
-        else:
-            none = torch.arange(nb) % 2 == 0 if kind != "low" else torch.arange(nb) >= 4
-            e = torch.where(none, -100, int(kind[5:]) if kind != "low" else 20)[:, None].expand(nb, Hkv).contiguous()
-            v[none[block]] = 0
-            k[..., 0] = torch.where(none[block], -7.0 if kind == "low" else 4.0, 0.0)[:, None] * D ** 0.5 / 4
-        seqs.append((k, v * torch.exp2(e.float())[block][..., None]))
-        exps.append(e)
-    return q, Cache(seqs, 16, "fp8", "fp8", exps)
-
-
 @pytest.mark.parametrize("kind", ["zeros20", "zeros100", "low", "any"])
 @pytest.mark.parametrize("lens,Hkv,D,qt", [([64], 1, 128, "bf16"), ([1070], 8, 128, "f16"), ([3000], 2, 64, "f32"),
                                            ([17, 900, 33, 1] * 60, 3, 64, "bf16"), ([1100, 64] * 90, 8, 128, "bf16")])
 def test_blk8_decode_of_scales_far_apart(kind, lens, Hkv, D, qt):
     """Blocks whose contribution is nothing beside others' count in the exp-sum all the same."""
-    q, c = _spread(len(lens) + D, lens, Hkv, D, kind, qt)
+    q, c = spread(len(lens) + D, lens, Hkv, D, kind, qt)
     out = decode(c, q, D ** -0.5)
     for b in sorted(set(range(min(len(lens), 4))) | {len(lens) - 1}):
         ref, tol = attend(q[b].double(), c.k64[b], c.v64[b], sees(lens[b], lens[b] - 1, 0, 0), D ** -0.5,

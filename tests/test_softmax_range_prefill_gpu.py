@@ -4,7 +4,7 @@ no value of its own, for every type of V pool (bounds: range_testlib)."""
 import pytest
 import torch
 
-from range_testlib import DT, Cache, attend, check, prefill, sees, sink
+from range_testlib import DT, Cache, attend, check, prefill, sees, sink, spread
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,19 @@ def test_two_parts_over_8_bit_values(odt, qt, kt, Hq, Hkv, n, share, T, blk8):
     c = Cache([(k, v)], 16, kt, "fp8", [torch.zeros(-(-n // 16), Hkv)] if blk8 else None)
     window, sinks = (0, 0) if blk8 else (n // 2 + 3, 1)
     _run(q, c, n, T, window, sinks, "fp8", odt)
+
+
+@pytest.mark.parametrize("kind", ["zeros20", "zeros100", "low", "any"])
+@pytest.mark.parametrize("lens,new,Hkv,G,qt", [([70], [5], 2, 4, "f16"), ([1070, 300, 1200, 33], [3, 200, 120, 33], 1, 8, "bf16"),
+                                               ([1100] * 3, [150, 1, 64], 2, 2, "f16"), ([1100, 64], [300, 64], 3, 1, "bf16")])
+def test_blk8_prefill_of_scales_far_apart(kind, lens, new, Hkv, G, qt):
+    """Blocks whose contribution is nothing beside others' count in the row sum all the same."""
+    q, c = spread(len(lens) + G, lens, Hkv, 128, kind, qt, new, G)
+    out = prefill(c, q, new, 128 ** -0.5)
+    at = 0
+    for b, (n, m) in enumerate(zip(lens, new)):
+        for i in list(range(0, m, 7)) + [m - 1]:
+            ref, tol = attend(q[at + i].double(), c.k64[b], c.v64[b], sees(n, n - m + i, 0, 0), 128 ** -0.5,
+                              *PREFILL["fp8"], vs=c.vs[b])
+            check(out[at + i], ref, tol, f"sequence {b}, token {i}")
+        at += m
