@@ -502,6 +502,7 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
           bool room = true;
           if (lane == 0) room = mbar_wait(empty(st), ((seq / NST) & 1) ^ 1, abort_flag, a.wait_ns);
           if (!__shfl_sync(0xffffffffu, room, 0)) { stop = true; break; }
+          if (a.test_withhold && seq == 0) continue;
           // the copies first: the step's barrier cannot complete before lane 0 arrives
           // with the expected bytes, once the scales are here and written
           if (ok) {
@@ -531,7 +532,7 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
         flag_error(a.err_flag, PA_DEV_TIMEOUT);
       }
       // never leave with copies in flight
-      for (int q = max(0, seq - NST); q < seq; ++q) {
+      for (int q = max(a.test_withhold ? 1 : 0, seq - NST); q < seq; ++q) {
         const uint64_t b0 = globaltimer();
         while (!mbar_try(full(q % NST), (q / NST) & 1) && globaltimer() - b0 < kWaitNs) {}
       }
@@ -577,10 +578,11 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll 1
       for (int k = s0; k < s1; ++k, ++seq) {
         const int st = seq % NST;
-        if (!failed && !mbar_wait(full(st), (seq / NST) & 1, abort_flag, a.wait_ns)) {
+        // the warp gives up as one: what follows takes all of its lanes
+        if (!failed && __any_sync(0xffffffffu, !mbar_wait(full(st), (seq / NST) & 1, abort_flag, a.wait_ns))) {
           failed = true;
           *abort_flag = 1u;
-          flag_error(a.err_flag, PA_DEV_TIMEOUT);
+          if (lane == 0) flag_error(a.err_flag, PA_DEV_TIMEOUT);
         }
         if (failed) continue;
         int t0[TW], lvs[TW];

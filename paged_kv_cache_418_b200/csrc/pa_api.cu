@@ -37,13 +37,6 @@ int kernel_override() {
   return 0;
 }
 
-// The timeout-path test's hook (PA_TC_TEST_WITHHOLD_Q=1): the tensor-core
-// kernel leaves the first unit's query unloaded, so the wait for it runs out.
-int tc_test_withhold_q() {
-  const char* s = std::getenv("PA_TC_TEST_WITHHOLD_Q");
-  return s && s[0] == '1' ? 1 : 0;
-}
-
 // Cost of a pair's start and end in the tensor-core kernel's work split, in
 // 1/16 of a tile. Per-CTA timers on the Llama-3-70B-shaped batch put a unit's
 // query load, first-tile reduction and epilogue at 1.2-1.5 tiles' time; a
@@ -76,6 +69,14 @@ unsigned long long tc_wait_ns() {
   char* end = nullptr;
   const unsigned long long v = std::strtoull(s, &end, 10);
   return (end && *end == 0 && v <= 1000000000ull) ? v : 1000000000ull;
+}
+
+// The timeout-path tests' hook (PA_TC_TEST_WITHHOLD_Q=1): the tensor-core kernels leave
+// a CTA's first load (the query's, or the windowed decode's first tiles) out, so the wait
+// for it runs out.
+int tc_test_withhold_q() {
+  const char* s = std::getenv("PA_TC_TEST_WITHHOLD_Q");
+  return s && s[0] == '1' ? 1 : 0;
 }
 
 // SM count of the current device (148 on B200; also the fallback with no device).

@@ -88,6 +88,7 @@ int decode_window_impl(void* out, int out_dtype, const void* query, int q_dtype,
     return PA_ERR_WORKSPACE;
   carve_window(a, static_cast<char*>(workspace));
   a.wait_ns = tc_wait_ns();
+  a.test_withhold = tc_test_withhold_q();
   return launch_decode_window(a, static_cast<cudaStream_t>(stream));
 }
 

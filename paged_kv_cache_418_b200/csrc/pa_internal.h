@@ -218,6 +218,7 @@ struct WinArgs {
   float* ws_l;
   int2* cuts;                   // per unit: the CTAs that hold its first and last step
   unsigned long long wait_ns;   // limit of every pipeline wait
+  int test_withhold;
   uint32_t* err_flag;
 };
 // Grid of a windowed decode; its scratch and the carve-up of it.
@@ -227,6 +228,8 @@ void carve_window(WinArgs& a, char* workspace);
 int launch_decode_window_f32(const WinArgs& a, cudaStream_t stream);
 // Limit of every pipeline wait of the tensor-core kernels, in ns.
 unsigned long long tc_wait_ns();
+// Tests of the timeout path: leave a CTA's first load out.
+int tc_test_withhold_q();
 int launch_decode_window(const WinArgs& a, cudaStream_t stream);
 
 int launch_swap_blocks(void* dst_key, void* dst_value, const void* src_key,

@@ -22,7 +22,7 @@ from . import _build
 PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2, 3
 PA_OK = 0
 PA_DEV_BAD_BLOCK_ID, PA_DEV_BAD_CTX, PA_DEV_BAD_SLOT, PA_DEV_BAD_PAIR = 1, 2, 4, 8
-PA_DEV_BAD_POS, PA_DEV_BAD_SCALE = 32, 64
+PA_DEV_TIMEOUT, PA_DEV_BAD_POS, PA_DEV_BAD_SCALE = 16, 32, 64
 _TORCH_TO_PA = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
                 torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3}
 
