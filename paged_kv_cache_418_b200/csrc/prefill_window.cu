@@ -66,7 +66,7 @@
 //
 // CTA, persistent over rounds of units in alternating directions: warps 0-7 softmax,
 // then (8-bit pools) 8-11 converters, then the TMA producer and the two MMA issuers. Every
-// pipeline wait is bounded (1 s); one that gives up sets PA_DEV_TIMEOUT, raises the
+// pipeline wait is bounded (wait_ns, 1 s); one that gives up sets PA_DEV_TIMEOUT, raises the
 // CTA's abort flag, and every role drains its asynchronous work, frees tensor memory
 // and returns.
 #include <cuda.h>
@@ -101,7 +101,7 @@ enum { B_FULL = 0, B_EMPTY = kNST, B_CONV = 2 * kNST, B_QFULL = 3 * kNST, B_QEMP
        B_QCONV = B_QEMPTY + kNQ, B_SFULL = B_QCONV + kNQ, B_PREADY = B_SFULL + 4, B_OSTEP = B_PREADY + 4,
        B_OFULL = B_OSTEP + 2, B_ODONE = B_OFULL + 2, B_DONE = B_ODONE + 2, B_XCH = B_DONE + 2, B_COUNT = B_XCH + 1 };
 constexpr int OFF_MISC = OFF_BAR + 8 * B_COUNT;
-constexpr int OFF_SLOT = (OFF_MISC + 8 + 15) / 16 * 16;
+constexpr int OFF_SLOT = (OFF_MISC + 12 + 15) / 16 * 16;  // (tensor memory, abort flag, wait limit)
 struct Slot {                                   // of a tile: what the producer knows of its blocks
   float ks[8], lvs[8];                          // K scale, log2 of the V scale
   uint32_t missing;                             // blocks that were not loaded
@@ -128,6 +128,8 @@ struct Args {
   int window, sinks;
   const float* k_scales;
   const float* v_scales;
+  uint32_t wait_ns;             // limit of every pipeline wait
+  int test_withhold;            // tests: leave the CTA's first query tile out
 };
 
 // Some rows attend keys t < t1 with t >= lo or t < sk.
@@ -215,6 +217,20 @@ __device__ __forceinline__ Unit unit_of(const Args& a, int G, int bs, long long 
 // The k-th unit of CTA cta: rounds of grid units in alternating directions.
 __device__ __forceinline__ long long unit_index(long long k, int cta, int grid) {
   return k * grid + ((k & 1) ? grid - 1 - cta : cta);
+}
+
+// Bounded wait for the phase with the given parity; false = gave up. The limit lies beside the
+// abort flag: as a kernel argument it took registers of every role (windowed bf16 chunks
+// 279 -> 295 us).
+__device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try(bar, parity)) return true;
+    if (abort_flag[0] || globaltimer() - t0 > abort_flag[1]) return false;
+  }
 }
 
 // One lane of the (converged) warp. Not lane == 0: only elect.sync tells the compiler
@@ -442,7 +458,8 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       mbar_init(bar(B_OFULL + i), 1);
       mbar_init(bar(B_ODONE + i), 128);
     }
-    *abort_flag = 0u;
+    abort_flag[0] = 0u;
+    abort_flag[1] = a.wait_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == R::kMma) {
@@ -491,8 +508,8 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           const int qi = qn % kNQ;
           bool ok = true;
           if (lane == 0) {
-            ok = mbar_wait(bar(B_QEMPTY + qi), ((qn / kNQ) & 1) ^ 1, abort_flag);
-            if (ok) {
+            ok = pipe_wait(bar(B_QEMPTY + qi), ((qn / kNQ) & 1) ^ 1, abort_flag);
+            if (ok && !(a.test_withhold && qn == 0)) {
               mbar_expect_tx(bar(B_QFULL + qi), (uint32_t)kOp);
               for (int hh = 0; hh < 2; ++hh)
                 tma_load_4d(sbase + OFF_Q + qi * kOp + hh * kHalf, &tmQ, 0, hh, x.h * G, x.qrow0 + g * x.tpt,
@@ -542,7 +559,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             const int seq = 2 * tc_ + kv, s = seq % kNST;
             const bool codes = kv ? V8 : K8;
             bool room = true;
-            if (lane == 0) room = mbar_wait(bar(B_EMPTY + s), ((seq / kNST) & 1) ^ 1, abort_flag);
+            if (lane == 0) room = pipe_wait(bar(B_EMPTY + s), ((seq / kNST) & 1) ^ 1, abort_flag);
             if (!__shfl_sync(0xffffffffu, room, 0)) { stop = true; break; }
             if (kv == 0) {
               Slot& slot = slots[tc_ % kSlots];
@@ -581,7 +598,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           const uint64_t t0 = globaltimer();
           while (!mbar_try(bar(B_FULL + seq % kNST), (seq / kNST) & 1) && globaltimer() - t0 < kWaitNs) {}
         }
-        for (int q = max(0, qn - kNQ); q < qn; ++q) {
+        for (int q = max(a.test_withhold ? 1 : 0, qn - kNQ); q < qn; ++q) {
           const uint64_t t0 = globaltimer();
           while (!mbar_try(bar(B_QFULL + q % kNQ), (q / kNQ) & 1) && globaltimer() - t0 < kWaitNs) {}
         }
@@ -609,7 +626,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         const uint32_t qst = sbase + OFF_Q + qi * kOp;
         // the other part's query tile
         auto pass_q = [&](int q) -> bool {
-          if (!mbar_wait(bar((QC ? B_QCONV : B_QFULL) + q % kNQ), (q / kNQ) & 1, abort_flag)) return false;
+          if (!pipe_wait(bar((QC ? B_QCONV : B_QFULL) + q % kNQ), (q / kNQ) & 1, abort_flag)) return false;
           mbar_arrive(bar(B_QEMPTY + q % kNQ));
           return true;
         };
@@ -627,10 +644,10 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             if (was) {
               const int n = tiles - 1 - (h == 1 && pend);
               const bool first = h == 0 && done == 1;
-              ok = mbar_wait(bar(B_PREADY + 2 * g + h), n & 1, abort_flag);
+              ok = pipe_wait(bar(B_PREADY + 2 * g + h), n & 1, abort_flag);
               // O is that of the last unit until its epilogue has read it
-              if (ok && first && units > 0) ok = mbar_wait(bar(B_ODONE + g), (units - 1) & 1, abort_flag);
-              if (ok && h == 0) ok = mbar_wait(ready_bar(1, sv), ((seq - 1) / kNST) & 1, abort_flag);
+              if (ok && first && units > 0) ok = pipe_wait(bar(B_ODONE + g), (units - 1) & 1, abort_flag);
+              if (ok && h == 0) ok = pipe_wait(ready_bar(1, sv), ((seq - 1) / kNST) & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -648,7 +665,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
                 mma_commit(bar(B_OFULL + g));
                 ++units;
               }
-            } else if (k > 0 && h == 0 && !mbar_wait(ready_bar(1, sv), ((seq - 1) / kNST) & 1, abort_flag)) {
+            } else if (k > 0 && h == 0 && !pipe_wait(ready_bar(1, sv), ((seq - 1) / kNST) & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -656,8 +673,8 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             // ---- this one
             if (more && h == 0) {
               if (pend && done == 0)
-                ok = mbar_wait(bar((QC ? B_QCONV : B_QFULL) + qi), (qt / kNQ) & 1, abort_flag);
-              ok = ok && mbar_wait(ready_bar(0, s), (seq / kNST) & 1, abort_flag);
+                ok = pipe_wait(bar((QC ? B_QCONV : B_QFULL) + qi), (qt / kNQ) & 1, abort_flag);
+              ok = ok && pipe_wait(ready_bar(0, s), (seq / kNST) & 1, abort_flag);
               if (!ok) break;
               done += pend;
               tiles += pend;
@@ -694,7 +711,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       bool ok = true;
       auto convert_q = [&]() -> bool {
         const int qi = qn % kNQ;
-        if (!mbar_wait(bar(B_QFULL + qi), (qn / kNQ) & 1, abort_flag)) return false;
+        if (!pipe_wait(bar(B_QFULL + qi), (qn / kNQ) & 1, abort_flag)) return false;
         rowe[qi * 128 + r] = (int8_t)rescale_row(smem + OFF_Q + qi * kOp, r);
         fence_proxy_async();
         mbar_arrive(bar(B_QCONV + qi));
@@ -711,7 +728,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           for (int kv = 0; kv < 2; ++kv) {
             if (!(kv ? V8 : K8)) continue;
             const int seq = 2 * tc_ + kv, s = seq % kNST;
-            if (!mbar_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) { ok = false; break; }
+            if (!pipe_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) { ok = false; break; }
             const int t = x.tile0(k) + r;
             // a V row no row of the unit attends meets only zero weights: it must be finite
             const bool zero = kv && (!x.all.needs(t, 1) || ((slots[tc_ % kSlots].missing >> (r / BS)) & 1u));
@@ -760,7 +777,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       if constexpr (QC) {
         // (The first scores say that the query tile was converted. To wait for that itself
         // would not do: a part that sat out units may be phases ahead of it.)
-        if (!mbar_wait(bar(B_SFULL + 2 * qt), tiles & 1, abort_flag)) failed = true;
+        if (!pipe_wait(bar(B_SFULL + 2 * qt), tiles & 1, abort_flag)) failed = true;
         f0 *= __uint_as_float((uint32_t)(127 - rowe[q % kNQ * 128 + r]) << 23);
         mbar_arrive(bar(B_QEMPTY + q % kNQ));
         if (!part.split) mbar_arrive(bar(B_QEMPTY + q % kNQ));
@@ -775,7 +792,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         bool open = false;                       // every row sees every key of the tile
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait(bar(B_SFULL + 2 * qt + h), n & 1, abort_flag)) failed = true;
+          if (!pipe_wait(bar(B_SFULL + 2 * qt + h), n & 1, abort_flag)) failed = true;
           __syncwarp();
           tc_fence_after();
           uint32_t raw[64];
@@ -802,7 +819,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
               // (both query tiles' threads write the zeros, ahead of their own product)
               if (!x.all.needs(ts + r, 1) || ((missing >> (r / BS)) & 1u)) {
                 const int seq = 2 * (base + k) + 1, s = seq % kNST;
-                if (!mbar_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) failed = true;
+                if (!pipe_wait(bar(B_FULL + s), (seq / kNST) & 1, abort_flag)) failed = true;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                   uint4* z = reinterpret_cast<uint4*>(smem + OFF_KV + s * kOp + hh * kHalf + r * 128);
@@ -890,7 +907,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
               const bool resc = tm > m + kMove;
               const float alpha = resc ? ex2(m - mn) : 1.f;
               if (resc) m = mn;
-              if (!mbar_wait(bar(h == 0 ? B_SFULL + 2 * qt + 1 : B_OSTEP + qt), n & 1, abort_flag)) failed = true;
+              if (!pipe_wait(bar(h == 0 ? B_SFULL + 2 * qt + 1 : B_OSTEP + qt), n & 1, abort_flag)) failed = true;
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -965,7 +982,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         }
       }
       // ---- epilogue: O / l of this row to the output
-      if (!mbar_wait(bar(B_OFULL + qt), units & 1, abort_flag)) failed = true;
+      if (!pipe_wait(bar(B_OFULL + qt), units & 1, abort_flag)) failed = true;
       ++units;
       tc_fence_after();
       if (part.split && qt == 1) {
@@ -979,7 +996,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       }
       Norm na, nb;                               // of this part's O and of the second's
       if (part.split) {
-        if (!mbar_wait(bar(B_XCH), splits & 1, abort_flag)) failed = true;
+        if (!pipe_wait(bar(B_XCH), splits & 1, abort_flag)) failed = true;
         __syncwarp();
         tc_fence_after();
         const float m2 = xch[r];
@@ -1154,6 +1171,8 @@ int launch_prefill_window(const PrefillLaunch& p, cudaStream_t stream) {
   a.err_flag = p.err_flag;
   a.window = p.window; a.sinks = p.sinks;
   a.k_scales = p.k_scales; a.v_scales = p.v_scales;
+  a.wait_ns = (uint32_t)tc_wait_ns();           // at most 10^9
+  a.test_withhold = tc_test_withhold_q();
   if (p.k_scales) return launch_kv<true, true, true>(a, p.dtype, p.bs, q, k, v, stream);
   if (k8 && v8) return launch_kv<true, true, false>(a, p.dtype, p.bs, q, k, v, stream);
   if (k8) return launch_kv<true, false, false>(a, p.dtype, p.bs, q, k, v, stream);
