@@ -801,8 +801,9 @@ int launch_window_t(const WinArgs& a, cudaStream_t stream) {
   static_assert(smem_bytes<C>(1) + 1024 <= 227 * 1024, "shared memory per CTA");
   const int smem = smem_bytes<C>(a.hg);
   auto kern = decode_window_kernel<KT, VT, D, BSC>;
-  // dynamic shared memory above 48 KB needs the attribute, on the current device
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // dynamic shared memory above 48 KB needs the attribute, on the current device: always the most
+  // any call of the kernel takes, as another thread's call may set it before this one's launch
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<C>(1)) != cudaSuccess)
     return PA_ERR_CUDA;
   CUtensorMap k, v;
   if (!make_map(a, a.k_cache, KT, &k) || !make_map(a, a.v_cache, VT, &v)) return PA_ERR_CUDA;
