@@ -19,7 +19,10 @@
 //                           16-bit parts, as in the per-sequence kernel)
 // A softmax thread owns one token row of S^T. The reference max of a query
 // column is set on the unit's first tile (an exact column max) and moves only
-// when a score passes it by 2^64 (then O's columns are rescaled in TMEM), so a
+// when a score passes it by far (then O's columns are rescaled in TMEM): by 2^64
+// with bf16 weights. f16 weights end at 2^16 above and at 2^-24 below: their
+// reference lies 2^12 under the maximum (so that small weights beside a dominating
+// one keep their bits) and moves when passed by 2^15.9. So a
 // tile needs no reduction across threads; the column sums l are per-thread
 // partial sums reduced once per unit. A score enters as one FMA against its
 // column's reference (s * scale - m, log2 units); a 16-bit mask per token row
@@ -67,7 +70,6 @@ constexpr int kSoft = 128 * kSplit;             // softmax threads
 constexpr int kHalfCols = kNQ / kSplit;         // query columns per softmax thread
 constexpr int kSoftWarps = kSoft / 32;
 constexpr int kThreads = kSoft + 64;            // + TMA producer warp + MMA warp
-constexpr float kRescaleLog2 = 64.f;
 
 constexpr int OFF_Q = kNST * kStage;            // Q: 2 d-halves x kNQ rows x 128 B
 constexpr int kQBytes = 2 * kNQ * 128;
@@ -198,6 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 multi_query_tc_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
   constexpr int NB_T = kTile / BS;              // physical blocks per tile
+  // a reference lies 2^kLow under its maximum and moves when passed by 2^kMove
+  constexpr float kLow = FMT == 1 ? 0.f : 12.f, kMove = FMT == 1 ? 64.f : 15.9f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -399,7 +403,7 @@ multi_query_tc_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tm
     // column maxima of s[] (this thread's columns c0 + i) over the 128 rows -> dst[q],
     // floored at -FLT_MAX: a column with no visible key keeps a finite reference, so
     // score - reference is -inf exactly where the score is masked
-    auto col_max = [&](const float* s, float* dst) {
+    auto col_max = [&](const float* s, float* dst, float low) {
 #pragma unroll
       for (int i = 0; i < kHalfCols; ++i) {
         float v = s[i];
@@ -409,7 +413,7 @@ multi_query_tc_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tm
       }
       sm_sync();
       if (st < kNQ)
-        dst[st] = fmaxf(fmaxf(fmaxf(red[st], red[kNQ + st]), fmaxf(red[2 * kNQ + st], red[3 * kNQ + st])),
+        dst[st] = fmaxf(fmaxf(fmaxf(red[st], red[kNQ + st]), fmaxf(red[2 * kNQ + st], red[3 * kNQ + st])) - low,
                         -FLT_MAX);
       sm_sync();
     };
@@ -499,7 +503,7 @@ multi_query_tc_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tm
 #pragma unroll
           for (int i = 0; i < kHalfCols; ++i)
             s[i] = ((mk >> i) & 1u) ? s[i] * a.scale_log2 : -CUDART_INF_F;
-          col_max(s, mref);
+          col_max(s, mref, kLow);
 #pragma unroll
           for (int i = 0; i < kHalfCols; ++i) s[i] -= mref[c0 + i];
         } else {
@@ -520,12 +524,12 @@ multi_query_tc_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tm
           float mx = s[0];
 #pragma unroll
           for (int i = 1; i < kHalfCols; ++i) mx = fmaxf(mx, s[i]);
-          if (sm_vote(mx > kRescaleLog2)) {
-            // rare: some column passed its reference by more than 2^64. Its reference
-            // moves up by the tile's maximum d of that column (relative to it), and its
+          if (sm_vote(mx > kMove)) {
+            // rare: some column passed its reference by more than 2^kMove. Its reference
+            // moves up by d, to 2^kLow under the tile's maximum of that column, and its
             // O (all earlier products included) and l are scaled by 2^-d
-            col_max(s, mnew);
-            if (st < kNQ) mold[st] = mnew[st] > kRescaleLog2 ? mnew[st] : 0.f;
+            col_max(s, mnew, 0.f);
+            if (st < kNQ) mold[st] = mnew[st] > kMove ? mnew[st] - kLow : 0.f;
             sm_sync();
             wait_pv(tc_ - 1);
             tc_fence_after();

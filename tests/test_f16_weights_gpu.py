@@ -1,0 +1,87 @@
+"""The plain tensor-core kernels whose softmax weights are f16 (fp16 queries; FP8 pools in the decode):
+scores that rise by far more than 2^16 along a sequence, and a first key that takes nearly all of the
+weight and has no value of its own. 64-bit references, bounds that follow each weight (range_testlib)."""
+
+import pytest
+import torch
+
+from paged_kv_cache_418_b200 import ops
+from range_testlib import DT, Cache, attend, check, sees, sink
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+
+
+def _rising(seed, T, n, Hq, Hkv, qt, span):
+    """Scores that rise by `span` (natural units) from the first key to the last."""
+    g = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.randn(*s, D, generator=g) for s in ((T, Hq), (n, Hkv), (n, Hkv)))
+    q[..., 0] = 8
+    k[..., 0] = (torch.arange(n) * (span * D ** 0.5 / 8 / n))[:, None]
+    return q.to(DT[qt]), k, v
+
+
+def _inputs(kind, *args):
+    return _rising(*args, 60.0) if kind == "rising" else sink(args[0], args[1], args[2], args[3], args[4], D, 0.99, args[5])
+
+
+@pytest.mark.parametrize("kernel", ["mq"])
+@pytest.mark.parametrize("kind", ["rising", "sink"])
+@pytest.mark.parametrize("qt,kt,vt,Hq,Hkv,bs", [("f16", "f16", "f16", 8, 2, 16), ("f16", "f16", "f16", 16, 1, 32),
+                                                ("f16", "fp8", "f16", 4, 2, 16), ("f16", "f16", "fp8", 2, 2, 32),
+                                                ("bf16", "bf16", "bf16", 8, 2, 16)])
+def test_prefill(monkeypatch, kernel, kind, qt, kt, vt, Hq, Hkv, bs):
+    monkeypatch.setenv("PA_PREFILL_KERNEL", kernel) if kernel else monkeypatch.delenv("PA_PREFILL_KERNEL", raising=False)
+    T, n = 70, 1500
+    q, k, v = _inputs(kind, bs + Hq, T, n, Hq, Hkv, qt)
+    c = Cache([(k, v)], bs, kt, vt)
+    qs = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if "fp8" in (kt, vt):
+        ops.pa_prefill_kv(out, q.cuda(), c.k, c.v, 1.0, 1.0, c.bt, c.cl, qs, T, D ** -0.5, n, err)
+    else:
+        ops.pa_prefill(out, q.cuda(), c.k, c.v, c.bt, c.cl, qs, T, D ** -0.5, n, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    # f16: half a step of the last ones, 2^-25 and twice for the two parts, over the largest weight, 2^12 or more
+    rel, floor = (2.0 ** -20, 2.0 ** -36) if qt == "f16" else (2.0 ** -16, 0.0)
+    for i in range(T):
+        ref, tol = attend(q[i].double(), c.k64[0], c.v64[0], sees(n, n - T + i, 0, 0), D ** -0.5, rel, floor)
+        check(out[i], ref, tol, f"token {i}")
+
+
+@pytest.mark.parametrize("kind", ["rising", "sink"])
+@pytest.mark.parametrize("qt,kt,vt,Hq,Hkv", [("f16", "f16", "f16", 8, 2), ("f16", "fp8", "f16", 16, 2), ("f16", "fp8", "fp8", 32, 4),
+                                             ("bf16", "bf16", "bf16", 8, 2)])
+def test_shared_prefix_decode(kind, qt, kt, vt, Hq, Hkv):
+    """40 groups of three over the same blocks: so many that one CTA walks the whole prefix."""
+    bs, pre, tails, groups = 16, 1024, [3, 40, 700], 40
+    n0 = pre + max(tails)
+    _, k, v = _inputs(kind, Hq, 1, n0, Hq, Hkv, qt)
+    q = torch.cat([_inputs(kind, Hq + b, 1, n0, Hq, Hkv, qt)[0] for b in range(3)])
+    c = Cache([(k[:pre + t], v[:pre + t]) for t in tails], bs, kt, vt)
+    c.bt[:, :pre // bs] = c.bt[:1, :pre // bs].clone()
+    dev = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()
+    B = 3 * groups
+    bt, cl, qd = c.bt.repeat(groups, 1), c.cl.repeat(groups), q.cuda().repeat(groups, 1, 1)
+    shared, offsets, members = dev([pre // bs] * B), dev(range(0, B + 1, 3)), dev(range(B))
+    out = torch.full(qd.shape, float("nan"), device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mc = max(c.ctx)
+    ws = ops.shared_prefix_workspace_for(qd, c.k, mc, pre // bs)
+    if "fp8" in (kt, vt):
+        ops.pa_decode_shared_prefix_kv(out, qd, c.k, c.v, 1.0, 1.0, bt, cl, shared, offsets, members, 3, pre // bs,
+                                       D ** -0.5, mc, 0, ws, err)
+    else:
+        ops.pa_decode_shared_prefix(out, qd, c.k, c.v, bt, cl, shared, offsets, members, 3, pre // bs, D ** -0.5, mc,
+                                    0, ws, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    rel, floor = (2.0 ** -20, 2.0 ** -36) if qt == "f16" else (2.0 ** -16, 0.0)
+    for b in range(3):
+        n = c.ctx[b]
+        ref, tol = attend(q[b].double(), c.k64[b], c.v64[b], sees(n, n - 1, 0, 0), D ** -0.5, rel, floor)
+        for g in (0, groups // 2, groups - 1):
+            check(out[3 * g + b], ref, tol, f"sequence {b} of group {g}")
