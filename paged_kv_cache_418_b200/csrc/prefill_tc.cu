@@ -33,8 +33,11 @@
 // more than the rest of the tile's softmax: the mask is one bit per key of a
 // 32-key chunk, and whole chunks take a loop without it.) The reference
 // maximum of a row is its first tile's maximum
-// and moves only when a later tile exceeds it by 2^64 (then the row's O is
-// rescaled in tensor memory, each half by its thread); references are
+// and moves only when a later tile exceeds it by far (then the row's O is
+// rescaled in tensor memory, each half by its thread): by 2^64 with bf16 weights.
+// f16 weights end at 2^16 above and at 2^-24 below: their reference lies 2^12
+// under the maximum (so that small weights beside a dominating one keep their
+// bits) and moves when a tile passes it by 2^15.9. References are
 // floored at -FLT_MAX so masked scores (-inf) give weight 0 without a guard.
 // Keys past a row's position are masked; the V rows of keys that no row of
 // the unit attends (past its last position, or in a block with a bad id) are
@@ -78,7 +81,6 @@ constexpr int kOp = 2 * kHalf;                  // one 128 x 128 16-bit operand:
 constexpr int kNST = 5;                         // K / V ring stages (odd: a stage serves K and V in turn)
 constexpr int kThreads = 320;                   // two softmax groups, producer, MMA
 constexpr int kProdWarp = 8, kMmaWarp = 9;
-constexpr float kRescaleLog2 = 64.f;
 
 constexpr int OFF_Q = 0;                        // [2 units][32 KB]
 constexpr int OFF_KV = 2 * kOp;                 // [kNST][32 KB]
@@ -176,6 +178,8 @@ prefill_fa_kernel(const FaArgs a, const __grid_constant__ CUtensorMap tmQ,
   constexpr uint32_t kBlkBits = (uint32_t)((1ull << BS) - 1ull);   // one block's keys in a chunk mask
   constexpr uint32_t IDESC_S = make_idesc(FMT, 0, 0, kTile, kM);
   constexpr uint32_t IDESC_O = make_idesc(FMT, 0, 1, kD, kM);
+  // a reference lies 2^kLow under its maximum and moves when passed by 2^kMove
+  constexpr float kLow = FMT == 1 ? 0.f : 12.f, kMove = FMT == 1 ? 64.f : 15.9f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -519,11 +523,11 @@ prefill_fa_kernel(const FaArgs a, const __grid_constant__ CUtensorMap tmQ,
         float alpha = 1.f;
         bool resc = false;
         if (k == 0) {
-          m = fmaxf(tm, -FLT_MAX);
-        } else if (tm > m + kRescaleLog2) {
+          m = fmaxf(tm - kLow, -FLT_MAX);
+        } else if (tm > m + kMove) {
           resc = true;
-          alpha = ex2(m - tm);
-          m = tm;
+          alpha = ex2(m - (tm - kLow));
+          m = tm - kLow;
         }
         if (__any_sync(0xffffffffu, resc)) {
           // rare: this warp's rows move their reference; O holds the products of

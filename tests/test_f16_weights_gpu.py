@@ -26,7 +26,7 @@ def _inputs(kind, *args):
     return _rising(*args, 60.0) if kind == "rising" else sink(args[0], args[1], args[2], args[3], args[4], D, 0.99, args[5])
 
 
-@pytest.mark.parametrize("kernel", ["mq"])
+@pytest.mark.parametrize("kernel", ["", "mq"])
 @pytest.mark.parametrize("kind", ["rising", "sink"])
 @pytest.mark.parametrize("qt,kt,vt,Hq,Hkv,bs", [("f16", "f16", "f16", 8, 2, 16), ("f16", "f16", "f16", 16, 1, 32),
                                                 ("f16", "fp8", "f16", 4, 2, 16), ("f16", "f16", "fp8", 2, 2, 32),
