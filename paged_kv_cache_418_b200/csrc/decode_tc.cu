@@ -45,9 +45,13 @@
 // hi = RN(p), lo = RN(p - hi), so the products keep ~16 significant bits
 // instead of 8 (bf16); O accumulates in fp32 in TMEM for the whole unit.
 // The online softmax rescales O lazily: a query head's reference max moves
-// only when a tile's max exceeds it by more than 2^64 (weights up to 2^64 are
-// far from fp32 overflow in l and O, and relative precision does not depend
-// on scale), which after the first tile is rare; then the affected TMEM
+// only when a tile's max exceeds it by far, which after the first tile is rare:
+// by 2^64 with bf16 weights (far from fp32 overflow in l and O, and their relative
+// precision does not depend on scale). f16 weights (f16 and FP8 pools) end at 2^16
+// above and at 2^-24 below: their reference lies 2^7 under the maximum and moves
+// when passed by 2^15, and their lo parts, which have columns of their own in O, are
+// stored 2^11 times larger, so that small weights beside a dominating one keep
+// their bits. When a reference moves, the affected TMEM
 // columns are read, scaled and written back. Exact in real arithmetic: O and
 // l always share the same reference.
 //
@@ -94,8 +98,6 @@ constexpr int kHG = 4;                          // KV heads per unit
 constexpr int kRt = kRows / kHG;                // tokens per head per tile (32)
 constexpr int kThreads = 320;
 constexpr int kScanChunk = 1024;                // sequences per pass of the first prologue scan
-constexpr float kRescaleLog2 = 64.f;            // lazy rescale threshold (log2 units): p <= 2^64,
-                                                // far from fp32 overflow in l and O
 constexpr int kEpochShift = 24;                 // ticket word: epoch << 24 | pieces arrived
 constexpr unsigned long long kCountMask = (1ull << kEpochShift) - 1;
 
@@ -553,6 +555,10 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
   // The output product runs on f16 operands whatever the query type: E4M3 ->
   // f16 is one conversion per pair of codes (bf16 would take several).
   constexpr int CF = KV8 ? 0 : FMT;             // element type of the output product
+  // a reference lies 2^kLow under its maximum and moves when passed by 2^kMove; lo parts
+  // are stored times kUp (at most 2^4 * 2^11)
+  constexpr float kLow = CF == 1 ? 0.f : 7.f, kMove = CF == 1 ? 64.f : 15.f;
+  constexpr float kUp = CF == 1 ? 1.f : 2048.f;
   constexpr bool QCNV = KV8;                    // the query becomes E4M3 pieces
   constexpr int NPU = FMT == 1 ? 2 : 3;         // pieces the score product uses
   constexpr uint32_t IDESC_S = make_idesc(CF, 0, 0, KV8 ? NPU * NS : NS, 128);
@@ -1010,11 +1016,11 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
         for (int g = 0; g < G; ++g) {
           const float raw = (RB < 32 && second) ? sv[(RB < 32 ? G : 0) + g] : sv[g];
           s[g] = valid ? raw * (QCNV ? qcs[g] : a.scale_log2) : -CUDART_INF_F;
-          exceed |= s[g] > mo[g] + kRescaleLog2;
+          exceed |= s[g] > mo[g] + kMove;
         }
         // The references (uniform per query head over the group): the unit's first
         // tile sets them to its maxima, a reduction over the group; a later tile
-        // only votes on whether some score passed its reference by 2^64, and
+        // only votes on whether some score passed its reference by 2^kMove, and
         // reduces (then rescales) only in that rare case.
         const bool reduce = wg_vote_or(failed || first || exceed, grp);
         if (reduce && wg_vote_or(failed, grp)) { stop = true; break; }
@@ -1034,7 +1040,7 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
           for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int q = 0; q < NQ; ++q) tm[g] = fmaxf(tm[g], rb[(q * kHG + rh) * S::GP + g]);
-            if (first) mo[g] = tm[g];
+            if (first) mo[g] = tm[g] - kLow;
           }
         }
         if (!first && reduce) {
@@ -1044,7 +1050,7 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               mold[rh * G + g] = mo[g];
-              mnew[rh * G + g] = tm[g] > mo[g] + kRescaleLog2 ? tm[g] : mo[g];
+              mnew[rh * G + g] = tm[g] > mo[g] + kMove ? tm[g] - kLow : mo[g];
             }
           }
           wg_sync(grp);
@@ -1070,9 +1076,9 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
           tc_fence_before();
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            if (tm[g] > mo[g] + kRescaleLog2) {
-              ao[g] = mo[g] == -CUDART_INF_F ? 1.f : exp2f(mo[g] - tm[g]);
-              mo[g] = tm[g];
+            if (tm[g] > mo[g] + kMove) {
+              ao[g] = mo[g] == -CUDART_INF_F ? 1.f : exp2f(mo[g] - (tm[g] - kLow));
+              mo[g] = tm[g] - kLow;
             }
           }
           wg_sync(grp);                           // mold / mnew may be rewritten next tile
@@ -1087,7 +1093,7 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
           const float p = valid ? exp2f(s[g] - mo[g]) : 0.f;
           l[g] = fmaf(l[g], ao[g], p);
           uint16_t hi, lo;
-          split_16<CF>(p, hi, lo);
+          split_16<CF>(p, hi, lo, kUp);
           *reinterpret_cast<uint16_t*>(prow + g * 128 + ((pchunk ^ (g & 7)) << 4) + pbyte) = hi;
           *reinterpret_cast<uint16_t*>(prow + (G + g) * 128 + ((pchunk ^ ((G + g) & 7)) << 4) + pbyte) = lo;
         }
@@ -1220,8 +1226,8 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             const int n = h * G + g;
-            float v = (own[g] + own[G + g]) * w[g];
-            if (has_p) v = fmaf(part[g] + part[G + g], wp[g], v);   // no partner: its TMEM is stale
+            float v = fmaf(own[G + g], 1.f / kUp, own[g]) * w[g];
+            if (has_p) v = fmaf(fmaf(part[G + g], 1.f / kUp, part[g]), wp[g], v);   // no partner: its TMEM is stale
             if (final_out) store_out(stg, (size_t)n * kD + row, v, a.out_dtype);
             else reinterpret_cast<float*>(stg)[n * kD + row] = v;
           }

@@ -169,15 +169,17 @@ __device__ __forceinline__ bool wg_vote_or(bool x, int group) {
   return r != 0;
 }
 
-template <int FMT> __device__ __forceinline__ void split_16(float p, uint16_t& hi, uint16_t& lo) {
+// p as a 16-bit value and what its rounding lost (times up), the same way.
+template <int FMT>
+__device__ __forceinline__ void split_16(float p, uint16_t& hi, uint16_t& lo, float up = 1.f) {
   if (FMT == 1) {
     __nv_bfloat16 h = __float2bfloat16_rn(p);
-    __nv_bfloat16 l = __float2bfloat16_rn(p - __bfloat162float(h));
+    __nv_bfloat16 l = __float2bfloat16_rn((p - __bfloat162float(h)) * up);
     hi = __bfloat16_as_ushort(h);
     lo = __bfloat16_as_ushort(l);
   } else {
     __half h = __float2half_rn(p);
-    __half l = __float2half_rn(p - __half2float(h));
+    __half l = __float2half_rn((p - __half2float(h)) * up);
     hi = __half_as_ushort(h);
     lo = __half_as_ushort(l);
   }

@@ -53,6 +53,33 @@ def test_prefill(monkeypatch, kernel, kind, qt, kt, vt, Hq, Hkv, bs):
 
 
 @pytest.mark.parametrize("kind", ["rising", "sink"])
+@pytest.mark.parametrize("qt,kvt,Hq,Hkv,bs", [("f16", "f16", 32, 4, 16), ("f16", "f16", 16, 4, 32), ("bf16", "fp8", 64, 8, 16),
+                                              ("f16", "fp8", 32, 8, 32), ("bf16", "bf16", 32, 4, 16)])
+def test_tensor_core_decode(monkeypatch, kind, qt, kvt, Hq, Hkv, bs):
+    monkeypatch.setenv("PA_DECODE_KERNEL", "tc")
+    # (rising: enough sequences that a CTA's share holds most of one)
+    lens = [1500, 40, 4096] if kind == "sink" else [900 + i for i in range(200)]
+    data = [_inputs(kind, b + Hq, 1, n, Hq, Hkv, qt) for b, n in enumerate(lens)]
+    q = torch.cat([x[0] for x in data])
+    c = Cache([(k, v) for _, k, v in data], bs, kvt, kvt)
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qd, mc = q.cuda(), max(lens)
+    ws = ops.workspace_for(qd, c.k, mc)
+    if kvt == "fp8":
+        ops.pa_decode_fp8(out, qd, c.k, c.v, 1.0, 1.0, c.bt, c.cl, D ** -0.5, mc, 0, ws, err)
+    else:
+        ops.pa_decode(out, qd, c.k, c.v, c.bt, c.cl, D ** -0.5, mc, 0, ws, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    # f16: lo parts 2^11 up, the largest weight 2^7 or more
+    rel, floor = (2.0 ** -16, 0.0) if kvt == "bf16" else (2.0 ** -20, 2.0 ** -43)
+    for b, n in list(enumerate(lens))[::23 if kind == "rising" else 1]:
+        ref, tol = attend(q[b].double(), c.k64[b], c.v64[b], sees(n, n - 1, 0, 0), D ** -0.5, rel, floor)
+        check(out[b], ref, tol, f"sequence {b}")
+
+
+@pytest.mark.parametrize("kind", ["rising", "sink"])
 @pytest.mark.parametrize("qt,kt,vt,Hq,Hkv", [("f16", "f16", "f16", 8, 2), ("f16", "fp8", "f16", 16, 2), ("f16", "fp8", "fp8", 32, 4),
                                              ("bf16", "bf16", "bf16", 8, 2)])
 def test_shared_prefix_decode(kind, qt, kt, vt, Hq, Hkv):
