@@ -498,6 +498,13 @@ def _check(fn: str, dense, index, indices) -> None:
             raise PAError(fn, 2)
 
 
+def _on_gpu(fn: str, device: int) -> int:
+    """The device of the first tensor, -1 for host memory: a kernel cannot read that."""
+    if device < 0:
+        raise PAError(fn, 2)
+    return device
+
+
 def _check_scales(fn: str, cache: torch.Tensor, *scales) -> None:
     shape, device = (cache.shape[0], cache.shape[2]), cache.get_device()
     for t in scales:
@@ -568,7 +575,8 @@ def pa_rope_and_cache_kv(query_out: Optional[torch.Tensor], query: Optional[torc
     T, Hq, max_positions, rot_dim = _append_sizes(query, query_out, slot_mapping, positions, cos_sin, fn)
     if value_cache.shape != shape:
         raise PAError(fn, 2)
-    qs, kvs, dtype, device = (T, Hq, D), (T, Hkv, D), key.dtype, key_cache.get_device()
+    qs, kvs, dtype = (T, Hq, D), (T, Hkv, D), key.dtype
+    device = _on_gpu(fn, key_cache.get_device())
     with _on_device_of(key_cache):
         rc = LIB.pa_rope_and_cache_kv(
             _ptr(query_out), _token_stride(query_out, qs, dtype, device, fn) if Hq else 0,
@@ -604,7 +612,8 @@ def pa_rope_and_cache_blk8(query_out: Optional[torch.Tensor], query: Optional[to
     if DEBUG:
         check_slot_mapping(slot_mapping, fn)
         check_block_runs(slot_mapping, block_size, fn)
-    qs, kvs, dtype, device = (T, Hq, D), (T, Hkv, D), key.dtype, key_cache.get_device()
+    qs, kvs, dtype = (T, Hq, D), (T, Hkv, D), key.dtype
+    device = _on_gpu(fn, key_cache.get_device())
     with _on_device_of(key_cache):
         rc = LIB.pa_rope_and_cache_blk8(
             _ptr(query_out), _token_stride(query_out, qs, dtype, device, fn) if Hq else 0,
@@ -628,16 +637,20 @@ def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
         check_block_mapping(block_mapping, "pa_copy_scales",
                             same_pool=dst_k_scales.data_ptr() == src_k_scales.data_ptr())
     fn = "pa_copy_scales"
-    _check(fn, (block_mapping, err_flag), torch.int64, (block_mapping,))
-    for t in (src_k_scales, src_v_scales, dst_k_scales, dst_v_scales):
-        if t.dtype != torch.float32 or not t.is_contiguous() or \
-                (t.get_device() != block_mapping.get_device() and not t.is_pinned()):
+    arrays = (dst_k_scales, dst_v_scales, src_k_scales, src_v_scales)
+    if block_mapping.dtype != torch.int64 or any(t.dtype != torch.float32 for t in arrays):
+        raise PAError(fn, 2)
+    # each in the memory of one device, or in page-locked host memory, which it reads as well
+    tensors = [t for t in (*arrays, block_mapping, err_flag) if t is not None]
+    device = max(t.get_device() for t in tensors)
+    for t in tensors:
+        if not t.is_contiguous() or (t.get_device() != device if t.get_device() >= 0 else not t.is_pinned()):
             raise PAError(fn, 2)
     if src_k_scales.shape != src_v_scales.shape or dst_k_scales.shape != dst_v_scales.shape or \
             src_k_scales.shape[1] != dst_k_scales.shape[1]:
         raise PAError(fn, 2)
     src_blocks, Hkv = src_k_scales.shape
-    with _on_device_of(dst_k_scales, src_k_scales):
+    with _on_device_of(*tensors):
         rc = LIB.pa_copy_scales(_ptr(dst_k_scales), _ptr(dst_v_scales), _ptr(src_k_scales),
                                 _ptr(src_v_scales), _ptr(block_mapping), block_mapping.shape[0],
                                 Hkv, src_blocks, dst_k_scales.shape[0], _ptr(err_flag),
@@ -675,6 +688,7 @@ def pa_decode_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torch
     if value_cache.shape != pool or out.shape != shape or head_size != D or rows != B or \
             context_lens.shape != (B,):
         raise PAError("pa_decode_window_kv", 2)
+    _on_gpu("pa_decode_window_kv", query.get_device())
     with _on_device_of(query):
         rc = LIB.pa_decode_window_kv(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
@@ -708,6 +722,7 @@ def pa_decode_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tens
     if value_cache.shape != pool or out.shape != shape or head_size != D or rows != B or \
             context_lens.shape != (B,):
         raise PAError("pa_decode_blk8", 2)
+    _on_gpu("pa_decode_blk8", query.get_device())
     with _on_device_of(query):
         rc = LIB.pa_decode_blk8(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
@@ -736,6 +751,7 @@ def pa_prefill_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torc
     if value_cache.shape != pool or out.shape != shape or head_size != D or \
             context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_window_kv", 2)
+    _on_gpu("pa_prefill_window_kv", query.get_device())
     with _on_device_of(query):
         rc = LIB.pa_prefill_window_kv(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
@@ -767,6 +783,7 @@ def pa_prefill_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Ten
     if value_cache.shape != pool or out.shape != shape or head_size != D or \
             context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_blk8", 2)
+    _on_gpu("pa_prefill_blk8", query.get_device())
     with _on_device_of(query):
         rc = LIB.pa_prefill_blk8(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),

@@ -1,0 +1,86 @@
+"""What the binding of the rotary append, the windowed attention and the block-scaled cache refuses
+before the library is called. CPU only."""
+
+import pytest
+import torch
+
+from paged_kv_cache_418_b200 import ops
+
+BF, I64, I32 = torch.bfloat16, torch.int64, torch.int32
+
+
+class Recorder:
+    """In place of the library: counts the calls that reach it and takes no pointer."""
+
+    def __init__(self, real):
+        self.calls = []
+        self.pa_status_string = real.pa_status_string
+
+    def __getattr__(self, name):
+        def f(*args):
+            self.calls.append((name, args))
+            return 0
+        return f
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it lies on device 0 (nothing reads it: the library is a Recorder)."""
+
+    def get_device(self):
+        return 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = Recorder(ops.LIB)
+    monkeypatch.setattr(ops, "LIB", lib)
+    monkeypatch.setattr(ops, "_stream", lambda stream: 0)
+    return lib
+
+
+def _calls():
+    """Every entry point with arguments it takes."""
+    kc = torch.zeros(4, 16, 2, 128, dtype=BF)
+    c8, sc = torch.zeros(4, 16, 2, 128, dtype=torch.uint8), torch.ones(4, 2)
+    q, k = torch.zeros(3, 8, 128, dtype=BF), torch.zeros(3, 2, 128, dtype=BF)
+    p, cs = torch.zeros(3, dtype=I64), torch.zeros(8, 128)
+    bt, cl, qs = torch.zeros(3, 4, dtype=I32), torch.zeros(3, dtype=I32), torch.zeros(4, dtype=I32)
+    ws, err, pairs = torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1, dtype=I32), torch.zeros(1, 2, dtype=I64)
+    return {"pa_rope_and_cache_kv": [q, q, k, k, p, cs, kc, kc, 1.0, 1.0, p, False, err],
+            "pa_rope_and_cache_blk8": [q, q, k, k, p, cs, c8, c8, sc, sc, p, False, err],
+            "pa_copy_scales": [sc, sc, sc, sc, pairs, err],
+            "pa_decode_window_kv": [q, q, kc, kc, 1.0, 1.0, bt, cl, 0.1, 5, 0, 64, ws, err],
+            "pa_decode_blk8": [q, q, c8, c8, sc, sc, bt, cl, 0.1, 64, 0, 0, ws, err],
+            "pa_prefill_window_kv": [q, q, kc, kc, 1.0, 1.0, bt, cl, qs, 1, 0.1, 5, 0, 64, err],
+            "pa_prefill_blk8": [q, q, c8, c8, sc, sc, bt, cl, qs, 1, 0.1, 64, 0, 0, err]}
+
+
+NAMES = sorted(_calls())
+
+
+def _gpu(args):
+    return [x.as_subclass(OnGpu) if isinstance(x, torch.Tensor) else x for x in args]
+
+
+def _refused(lib, name, args, status=2):
+    with pytest.raises(ops.PAError) as e:
+        getattr(ops, name)(*args)
+    assert e.value.status == status and not lib.calls
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_taken_on_a_device(lib, name):
+    getattr(ops, name)(*_gpu(_calls()[name]))
+    assert [c[0] for c in lib.calls] == [name]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_host_tensors_are_refused(lib, name):
+    """All of them on the host, and each alone beside device tensors."""
+    args = _calls()[name]
+    _refused(lib, name, args)
+    for i, x in enumerate(args):
+        if isinstance(x, torch.Tensor):
+            one = _gpu(args)
+            one[i] = x
+            _refused(lib, name, one)
