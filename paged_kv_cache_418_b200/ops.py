@@ -638,7 +638,8 @@ def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
                             same_pool=dst_k_scales.data_ptr() == src_k_scales.data_ptr())
     fn = "pa_copy_scales"
     arrays = (dst_k_scales, dst_v_scales, src_k_scales, src_v_scales)
-    if block_mapping.dtype != torch.int64 or any(t.dtype != torch.float32 for t in arrays):
+    if block_mapping.dtype != torch.int64 or block_mapping.dim() != 2 or block_mapping.shape[1] != 2 or \
+            any(t.dtype != torch.float32 or t.dim() != 2 for t in arrays):
         raise PAError(fn, 2)
     # each in the memory of one device, or in page-locked host memory, which it reads as well
     tensors = [t for t in (*arrays, block_mapping, err_flag) if t is not None]

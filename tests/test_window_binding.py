@@ -84,3 +84,16 @@ def test_host_tensors_are_refused(lib, name):
             one = _gpu(args)
             one[i] = x
             _refused(lib, name, one)
+
+
+def test_copy_scales_refuses_what_is_no_list_of_pairs(lib):
+    args = _gpu(_calls()["pa_copy_scales"])
+    for bad in (torch.zeros(3, dtype=I64), torch.zeros(3, 1, dtype=I64), torch.zeros(3, 3, dtype=I64),
+                torch.zeros(1, 3, 2, dtype=I64)):
+        _refused(lib, "pa_copy_scales", args[:4] + _gpu([bad]))
+    for i in range(4):
+        one = list(args)
+        one[i] = torch.ones(4).as_subclass(OnGpu)
+        _refused(lib, "pa_copy_scales", one)
+    ops.pa_copy_scales(*args[:4], torch.zeros(0, 2, dtype=I64).as_subclass(OnGpu))
+    assert lib.calls[0][1][5] == 0                 # no pairs
