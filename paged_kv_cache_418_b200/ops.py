@@ -505,6 +505,15 @@ def _on_gpu(fn: str, device: int) -> int:
     return device
 
 
+def _ints(fn: str, *lengths) -> list:
+    """Lengths as the library's ints; ctypes would cut a larger one to its last 32 bits."""
+    lengths = [int(x) for x in lengths]
+    for x in lengths:
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise PAError(fn, 2)
+    return lengths
+
+
 def _check_scales(fn: str, cache: torch.Tensor, *scales) -> None:
     shape, device = (cache.shape[0], cache.shape[2]), cache.get_device()
     for t in scales:
@@ -662,7 +671,8 @@ def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
 
 def pa_window_workspace_size(B: int, Hq: int, Hkv: int, D: int, max_context_len: int,
                              window: int = 0, num_sinks: int = 0) -> int:
-    return int(LIB.pa_window_workspace_size(B, Hq, Hkv, D, max_context_len, window, num_sinks))
+    lengths = _ints("pa_window_workspace_size", max_context_len, window, num_sinks)
+    return int(LIB.pa_window_workspace_size(B, Hq, Hkv, D, *lengths))
 
 
 def window_workspace_for(query: torch.Tensor, key_cache: torch.Tensor, max_context_len: int,
@@ -690,13 +700,14 @@ def pa_decode_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torch
             context_lens.shape != (B,):
         raise PAError("pa_decode_window_kv", 2)
     _on_gpu("pa_decode_window_kv", query.get_device())
+    window, num_sinks, max_context_len = _ints("pa_decode_window_kv", window, num_sinks, max_context_len)
     with _on_device_of(query):
         rc = LIB.pa_decode_window_kv(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
             pa_dtype(key_cache), float(k_scale), value_cache.data_ptr(), pa_dtype(value_cache),
             float(v_scale), block_tables.data_ptr(), max_blocks, context_lens.data_ptr(), B, Hq,
-            Hkv, D, block_size, num_blocks, float(scale), int(window), int(num_sinks),
-            int(max_context_len), _ptr(workspace),
+            Hkv, D, block_size, num_blocks, float(scale), window, num_sinks,
+            max_context_len, _ptr(workspace),
             0 if workspace is None else workspace.nbytes,
             _ptr(err_flag), _stream(stream))
     if rc:
@@ -724,14 +735,14 @@ def pa_decode_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tens
             context_lens.shape != (B,):
         raise PAError("pa_decode_blk8", 2)
     _on_gpu("pa_decode_blk8", query.get_device())
+    window, num_sinks, max_context_len = _ints("pa_decode_blk8", window, num_sinks, max_context_len)
     with _on_device_of(query):
         rc = LIB.pa_decode_blk8(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
             value_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
             max_blocks, context_lens.data_ptr(), B, Hq, Hkv, D, block_size, num_blocks,
-            float(scale), int(window), int(num_sinks), int(max_context_len), _ptr(workspace),
-            0 if workspace is None else workspace.nbytes,
-            _ptr(err_flag), _stream(stream))
+            float(scale), window, num_sinks, max_context_len, _ptr(workspace),
+            0 if workspace is None else workspace.nbytes, _ptr(err_flag), _stream(stream))
     if rc:
         raise PAError("pa_decode_blk8", rc)
 
@@ -753,13 +764,14 @@ def pa_prefill_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torc
             context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_window_kv", 2)
     _on_gpu("pa_prefill_window_kv", query.get_device())
+    window, num_sinks, max_context_len, max_query_len = _ints("pa_prefill_window_kv", window, num_sinks, max_context_len, max_query_len)
     with _on_device_of(query):
         rc = LIB.pa_prefill_window_kv(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
             pa_dtype(key_cache), float(k_scale), value_cache.data_ptr(), pa_dtype(value_cache),
             float(v_scale), block_tables.data_ptr(), max_blocks, context_lens.data_ptr(),
-            query_start.data_ptr(), B, T, int(max_query_len), Hq, Hkv, D, block_size, num_blocks,
-            float(scale), int(window), int(num_sinks), int(max_context_len), _ptr(err_flag),
+            query_start.data_ptr(), B, T, max_query_len, Hq, Hkv, D, block_size, num_blocks,
+            float(scale), window, num_sinks, max_context_len, _ptr(err_flag),
             _stream(stream))
     if rc:
         raise PAError("pa_prefill_window_kv", rc)
@@ -785,12 +797,13 @@ def pa_prefill_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Ten
             context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_blk8", 2)
     _on_gpu("pa_prefill_blk8", query.get_device())
+    window, num_sinks, max_context_len, max_query_len = _ints("pa_prefill_blk8", window, num_sinks, max_context_len, max_query_len)
     with _on_device_of(query):
         rc = LIB.pa_prefill_blk8(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
             value_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
             max_blocks, context_lens.data_ptr(), query_start.data_ptr(), B, T,
-            int(max_query_len), Hq, Hkv, D, block_size, num_blocks, float(scale), int(window),
-            int(num_sinks), int(max_context_len), _ptr(err_flag), _stream(stream))
+            max_query_len, Hq, Hkv, D, block_size, num_blocks, float(scale), window,
+            num_sinks, max_context_len, _ptr(err_flag), _stream(stream))
     if rc:
         raise PAError("pa_prefill_blk8", rc)

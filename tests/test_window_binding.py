@@ -97,3 +97,25 @@ def test_copy_scales_refuses_what_is_no_list_of_pairs(lib):
         _refused(lib, "pa_copy_scales", one)
     ops.pa_copy_scales(*args[:4], torch.zeros(0, 2, dtype=I64).as_subclass(OnGpu))
     assert lib.calls[0][1][5] == 0                 # no pairs
+
+
+@pytest.mark.parametrize("name,places", [("pa_decode_window_kv", (9, 10, 11)), ("pa_decode_blk8", (9, 10, 11)),
+                                         ("pa_prefill_window_kv", (9, 11, 12, 13)), ("pa_prefill_blk8", (9, 11, 12, 13))])
+def test_lengths_past_32_bits_are_refused(lib, name, places):
+    """(2^32 + 5 would be read as 5, 2^32 as 0: every token.)"""
+    args = _gpu(_calls()[name])
+    for i in places:
+        for x in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1):
+            one = list(args)
+            one[i] = x
+            _refused(lib, name, one)
+        one = list(args)
+        one[i] = 2 ** 31 - 1
+        getattr(ops, name)(*one)
+        assert 2 ** 31 - 1 in lib.calls.pop()[1]
+
+
+def test_workspace_of_lengths_past_32_bits_is_refused():
+    for args in ((2 ** 32 + 5, 0, 0), (64, 2 ** 32, 0), (64, 5, 2 ** 31)):
+        with pytest.raises(ops.PAError):
+            ops.pa_window_workspace_size(1, 8, 2, 128, *args)
