@@ -533,7 +533,7 @@ def _token_stride(t: torch.Tensor, shape: tuple, dtype, device: int, fn: str) ->
     T, H, D = shape
     if sd != 1 or (H > 1 and sh != D):
         raise PAError(fn, 2)
-    return st if T > 1 else max(st, H * D)
+    return st if T > 1 else H * D                # (of one token any stride would do)
 
 
 def _append_sizes(query, query_out, slot_mapping, positions, cos_sin, fn: str):
@@ -764,7 +764,8 @@ def pa_prefill_window_kv(out: torch.Tensor, query: torch.Tensor, key_cache: torc
             context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_window_kv", 2)
     _on_gpu("pa_prefill_window_kv", query.get_device())
-    window, num_sinks, max_context_len, max_query_len = _ints("pa_prefill_window_kv", window, num_sinks, max_context_len, max_query_len)
+    window, num_sinks, max_context_len, max_query_len = \
+        _ints("pa_prefill_window_kv", window, num_sinks, max_context_len, max_query_len)
     with _on_device_of(query):
         rc = LIB.pa_prefill_window_kv(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),
@@ -797,7 +798,8 @@ def pa_prefill_blk8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Ten
             context_lens.shape != (B,) or query_start.shape != (B + 1,):
         raise PAError("pa_prefill_blk8", 2)
     _on_gpu("pa_prefill_blk8", query.get_device())
-    window, num_sinks, max_context_len, max_query_len = _ints("pa_prefill_blk8", window, num_sinks, max_context_len, max_query_len)
+    window, num_sinks, max_context_len, max_query_len = \
+        _ints("pa_prefill_blk8", window, num_sinks, max_context_len, max_query_len)
     with _on_device_of(query):
         rc = LIB.pa_prefill_blk8(
             out.data_ptr(), pa_dtype(out), query.data_ptr(), pa_dtype(query), key_cache.data_ptr(),

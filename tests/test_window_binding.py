@@ -119,3 +119,17 @@ def test_workspace_of_lengths_past_32_bits_is_refused():
     for args in ((2 ** 32 + 5, 0, 0), (64, 2 ** 32, 0), (64, 5, 2 ** 31)):
         with pytest.raises(ops.PAError):
             ops.pa_window_workspace_size(1, 8, 2, 128, *args)
+
+
+@pytest.mark.parametrize("name", ["pa_rope_and_cache_kv", "pa_rope_and_cache_blk8"])
+def test_one_token_of_an_odd_buffer(lib, name):
+    """A single token has no next one: its stride does not count, whatever the buffer behind it is."""
+    args = _gpu(_calls()[name])
+    rows = torch.zeros(2, 12 * 128 + 3, dtype=BF)            # 1539 elements: no multiple of 16 bytes
+    q, k = rows[:, :8 * 128].view(2, 8, 128)[:1], rows[:, 8 * 128:10 * 128].view(2, 2, 128)[:1]
+    assert q.stride(0) == 1539
+    args[:4] = _gpu([q, q, k, k])
+    args[4], args[10] = args[4][:1], args[10][:1]
+    getattr(ops, name)(*args)
+    strides = lib.calls[0][1][1:8:2]
+    assert all(s * 2 % 16 == 0 for s in strides), strides
