@@ -488,8 +488,11 @@ def workspace_for(query: torch.Tensor, key_cache: torch.Tensor, max_context_len:
 def _check(fn: str, dense, index, indices) -> None:
     """The sizes and addresses of the entry points below are read off these tensors, so a
     wrong one would be read past its end: no gaps in `dense` and `indices`, the integer type
-    `index` for `indices`, and all of them on the device of the first of `dense`."""
+    `index` for `indices`, and all of them on the device of the first of `dense`, the last of
+    which is the error flag: 32 bits of it are written."""
     device = dense[0].get_device()
+    if dense[-1] is not None and dense[-1].nbytes < 4:
+        raise PAError(fn, 2)
     for t in dense:
         if t is not None and (not t.is_contiguous() or t.get_device() != device):
             raise PAError(fn, 2)
@@ -648,7 +651,8 @@ def pa_copy_scales(dst_k_scales: torch.Tensor, dst_v_scales: torch.Tensor,
     fn = "pa_copy_scales"
     arrays = (dst_k_scales, dst_v_scales, src_k_scales, src_v_scales)
     if block_mapping.dtype != torch.int64 or block_mapping.dim() != 2 or block_mapping.shape[1] != 2 or \
-            any(t.dtype != torch.float32 or t.dim() != 2 for t in arrays):
+            any(t.dtype != torch.float32 or t.dim() != 2 for t in arrays) or \
+            (err_flag is not None and err_flag.nbytes < 4):
         raise PAError(fn, 2)
     # each in the memory of one device, or in page-locked host memory, which it reads as well
     tensors = [t for t in (*arrays, block_mapping, err_flag) if t is not None]

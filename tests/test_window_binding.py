@@ -133,3 +133,12 @@ def test_one_token_of_an_odd_buffer(lib, name):
     getattr(ops, name)(*args)
     strides = lib.calls[0][1][1:8:2]
     assert all(s * 2 % 16 == 0 for s in strides), strides
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_an_error_flag_holds_32_bits(lib, name):
+    args = _gpu(_calls()[name])
+    for bad in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.bool), torch.zeros(1, dtype=torch.int16),
+                torch.zeros(0, dtype=I32)):
+        _refused(lib, name, args[:-1] + _gpu([bad]))
+    getattr(ops, name)(*args[:-1], None)
