@@ -456,8 +456,8 @@ int pa_decode_plan(int dtype, int B, int Hq, int Hkv, int D, int block_size,
  * sum rounded to nearest (no fused multiply-add). Rotated query heads go to
  * query_out, rotated key heads and the value heads to the pools.
  * query, query_out  [T, Hq, D] of src_dtype (PA_F32, PA_F16 or PA_BF16);
- *               query_out may be query itself (rotated in place), otherwise
- *               the two do not overlap. Hq = 0 with NULL: keys only;
+ *               query_out may be query itself (rotated in place, with query's
+ *               stride), otherwise the two do not overlap. Hq = 0 with NULL: keys only;
  * key, value    [T, Hkv, D] of src_dtype;
  * *_stride      elements from one token to the next (>= heads * D, a multiple
  *               of 16 bytes; a token's heads are dense), so the arrays may be

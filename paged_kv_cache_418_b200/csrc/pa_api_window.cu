@@ -30,6 +30,8 @@ int rope_impl(RopeArgs a, int src_dtype, bool blk8, void* stream) {
   };
   if (!stride_ok(a.k_stride, a.Hkv) || !stride_ok(a.v_stride, a.Hkv)) return PA_ERR_SHAPE;
   if (a.Hq > 0 && (!stride_ok(a.q_stride, a.Hq) || !stride_ok(a.qo_stride, a.Hq))) return PA_ERR_SHAPE;
+  // in place means row by row: with two strides one token's result would land on another's input
+  if (a.Hq > 0 && a.T > 1 && a.query && a.query == a.query_out && a.q_stride != a.qo_stride) return PA_ERR_SHAPE;
   if (a.T == 0) return PA_OK;
   if (!a.key || !a.value || !a.key_cache || !a.value_cache || !a.slot_mapping) return PA_ERR_NULL;
   if (a.Hq > 0 && (!a.query || !a.query_out)) return PA_ERR_NULL;

@@ -142,3 +142,15 @@ def test_an_error_flag_holds_32_bits(lib, name):
                 torch.zeros(0, dtype=I32)):
         _refused(lib, name, args[:-1] + _gpu([bad]))
     getattr(ops, name)(*args[:-1], None)
+
+
+def test_in_place_rotation_takes_one_stride():
+    """Rotated in place with another output stride, one token's result would land on another's input."""
+    import test_window_abi as abi
+    for fn, base in (("pa_rope_and_cache_kv", abi.ROPE), ("pa_rope_and_cache_blk8", abi.BLK)):
+        kw = dict(T=2, q=32, qo=32, qs=1024, qos=2048, nb=0)
+        assert abi.call(fn, base, **kw) == 2
+        assert abi.call(fn, base, **dict(kw, pos=None)) == 2
+        assert abi.call(fn, base, **dict(kw, pos=None, qo=64)) == 1          # (what is refused next)
+        assert abi.call(fn, base, **dict(kw, pos=None, qos=1024)) == 1
+        assert abi.call(fn, base, **dict(kw, pos=None, T=1)) == 1
