@@ -206,7 +206,7 @@ int pa_copy_scales(float* dst_k_scales, float* dst_v_scales, const float* src_k_
 
 size_t pa_window_workspace_size(int B, int Hq, int Hkv, int D, int max_context_len, int window,
                                 int num_sinks) {
-  if (B <= 0 || max_context_len <= 0 || window < 0 || num_sinks < 0 || B > 65535 || Hq > 65535 ||
+  if (B <= 0 || max_context_len < 0 || window < 0 || num_sinks < 0 || B > 65535 || Hq > 65535 ||
       !supported_shape(Hq, Hkv, D, 16))
     return 0;
   WinArgs a{};

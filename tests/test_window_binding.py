@@ -154,3 +154,10 @@ def test_in_place_rotation_takes_one_stride():
         assert abi.call(fn, base, **dict(kw, pos=None, qo=64)) == 1          # (what is refused next)
         assert abi.call(fn, base, **dict(kw, pos=None, qos=1024)) == 1
         assert abi.call(fn, base, **dict(kw, pos=None, T=1)) == 1
+
+
+def test_workspace_of_a_batch_of_empty_sequences():
+    """A bound of 0 tokens is a batch whose rows are all zeros; the decode wants its scratch all the same."""
+    n = ops.pa_window_workspace_size
+    assert n(3, 8, 2, 128, 0) == n(3, 8, 2, 128, 1) > 0 and n(3, 8, 2, 128, 0, 5, 1) > 0
+    assert n(3, 8, 2, 128, -1) == 0 and n(0, 8, 2, 128, 0) == 0
