@@ -130,7 +130,8 @@ int prefill_window_impl(void* out, int out_dtype, const void* query, int q_dtype
   p.v_scale = v8 && !blk8 ? v_scale : 1.f;
   p.block_tables = block_tables; p.max_blocks = max_blocks_per_seq;
   p.context_lens = context_lens; p.query_start = query_start;
-  p.B = B; p.T = T; p.max_query_len = max_query_len; p.Hq = Hq; p.Hkv = Hkv; p.bs = block_size;
+  // (a bound past all the tokens would only add chunks that hold none, each walked by every CTA)
+  p.B = B; p.T = T; p.max_query_len = max_query_len < T ? max_query_len : T; p.Hq = Hq; p.Hkv = Hkv; p.bs = block_size;
   p.num_blocks = num_blocks;
   p.scale_log2 = scale * kLog2e * (k8 && !blk8 ? k_scale : 1.f);
   p.max_context_len = max_context_len;
