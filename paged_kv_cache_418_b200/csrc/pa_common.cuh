@@ -150,21 +150,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A row's sums as the output wants them: O * f[0] * f[1] is O / l * 2^(m - r) * scale, with m
-// the reference of O and (BSC: block scales) r a whole number of powers of two away that of l
-// (two factors, as 2^(m - r) alone may leave fp32's range).
+// A row's sums as the output wants them: O * f[0] * f[1] is O / l * 2^n * scale, with n (FAR) the
+// distance of O's reference over l's (two factors, as 2^n alone may leave fp32's range; exact
+// where n is a whole number).
 struct Norm {
   float f[2];
   __device__ __forceinline__ float operator()(float o) const { return o * f[0] * f[1]; }
 };
-template <bool BSC> __device__ __forceinline__ Norm norm_of(float m, float r, float l, float scale) {
-  Norm n = {{l == 0.f ? 0.f : scale / l, 1.f}};
-  if (BSC) {
-    const float h = truncf((m - r) * 0.5f);
-    n.f[0] *= ex2(h);
-    n.f[1] = ex2(m - r - h);
+template <bool FAR> __device__ __forceinline__ Norm norm_of(float n, float l, float scale) {
+  Norm x = {{l == 0.f ? 0.f : scale / l, 1.f}};
+  if (FAR) {
+    const float h = truncf(n * 0.5f);
+    x.f[0] *= ex2(h);
+    x.f[1] = ex2(n - h);
   }
-  return n;
+  return x;
 }
 
 // Programmatic dependent launch. Every kernel of the library lets the next

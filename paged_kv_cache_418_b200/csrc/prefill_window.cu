@@ -59,9 +59,10 @@
 // between the two; only where their contributions are all under 2^-96 of the reference (and
 // fp32 is about to lose them) but a score over 2^-45 of r's are their exponentials taken a
 // second time. A tile can hold such keys only if its least log2(vs) is under m - r - 51.
-// The row is O / l 2^(m - r), exactly, as both references are whole numbers. (8192-token
-// prompt: 650 us with the row sum taken from the weights, 677 so; all of this in the loop over
-// the scores, unrolled, 778.) The producer leaves a tile's scales and the mask of its missing
+// The row is O / l 2^(m - r), exactly, as m - r is a whole number. (8192-token prompt: 650 us
+// with the row sum taken from the weights, 677 so; all of this in the loop over the scores,
+// unrolled, 778.) m itself is no whole number: 2^kLow under the maximum, not under its floor,
+// the weight of a key that outweighs the rest is a power of two, which loses nothing to f16. The producer leaves a tile's scales and the mask of its missing
 // blocks in a ring of shared-memory slots.
 //
 // CTA, persistent over rounds of units in alternating directions: warps 0-7 softmax,
@@ -772,7 +773,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       const int last_lo = a.window > 0 ? max(0, part.reach.t1 - a.window) : 0;
       const int32_t* table = a.block_tables + (size_t)x.b * a.max_blocks;
       float m = -FLT_MAX, l = 0.f;
-      float rs = -FLT_MAX, back_m = 0.f;         // BSC: the row sum's reference, m - it
+      float back_m = 0.f;                        // BSC: the row sum's reference r as m - r
       float f0 = a.scale_log2;                   // score factor of the row
       if constexpr (QC) {
         // (The first scores say that the query tile was converted. To wait for that itself
@@ -895,9 +896,9 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
           }
           // the references, in one vote: all of this is rare, but for masked halves
           bool move = tm > m + kMove;
-          if constexpr (BSC) move = move || tm - lvmin > rs + kSumMove || lvmin < back_m - 51.f;
+          if constexpr (BSC) move = move || tm - lvmin > m - back_m + kSumMove || lvmin < back_m - 51.f;
           if (first || __any_sync(0xffffffffu, move)) {
-            const float mn = floorf(tm) - kLow;
+            const float mn = tm - kLow, mo = m;
             if (first) {
               m = fmaxf(mn, -FLT_MAX);
             } else if (__any_sync(0xffffffffu, tm > m + kMove)) {
@@ -924,12 +925,12 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             first = false;
             if constexpr (BSC) {
               const float top = fmaxf(fmaxf(tc[0] - lv[0], tc[1] - lv[1]), fmaxf(tc[2] - lv[2], tc[3] - lv[3]));
-              if (top > rs + kSumMove) {
-                const float rn = floorf(top);
-                l *= ex2(rs - rn);
-                rs = rn;
-              }
-              back_m = m - rs;
+              // r stays a whole number of powers of two away from m
+              const float ro = mo - back_m, bo = back_m;
+              if (top > ro + kSumMove) back_m = rintf(m - top);
+              else if (m != mo) back_m = rintf(m - ro);
+              l *= ex2(mo - m - (bo - back_m));
+              const float rs = m - back_m;
               uint32_t far = 0;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -988,7 +989,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
       if (part.split && qt == 1) {
         // the second part: its maximum and sum to the first, which reads its O
         xch[r] = m;
-        xch[128 + r] = BSC ? pack_sum(l, rs - m) : l;
+        xch[128 + r] = BSC ? pack_sum(l, -back_m) : l;
         tc_fence_before();
         mbar_arrive(bar(B_XCH));
         failed = __any_sync(0xffffffffu, failed);
@@ -1000,14 +1001,14 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         __syncwarp();
         tc_fence_after();
         const float m2 = xch[r];
-        float l2 = xch[128 + r], r1 = BSC ? rs : m, r2 = m2;
+        float l2 = xch[128 + r], r1 = BSC ? m - back_m : m, r2 = m2;
         if (BSC) l2 = unpack_sum(l2, r2);
         const float top = fmaxf(r1, r2);
         l = fmaf(l, ex2(r1 - top), l2 * ex2(r2 - top));
-        na = norm_of<true>(m, top, l, a.v_scale);
-        nb = norm_of<true>(m2, top, l, a.v_scale);
+        na = norm_of<true>(m - top, l, a.v_scale);
+        nb = norm_of<true>(m2 - top, l, a.v_scale);
       } else {
-        na = norm_of<BSC>(m, rs, l, a.v_scale);
+        na = norm_of<BSC>(back_m, l, a.v_scale);
       }
       const size_t orow = ((size_t)(x.qrow0 + qs * x.tpt + tl) * a.Hq + (size_t)x.h * G + hg) * kD;
 #pragma unroll 1
