@@ -1016,7 +1016,7 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
         for (int g = 0; g < G; ++g) {
           const float raw = (RB < 32 && second) ? sv[(RB < 32 ? G : 0) + g] : sv[g];
           s[g] = valid ? raw * (QCNV ? qcs[g] : a.scale_log2) : -CUDART_INF_F;
-          exceed |= s[g] > mo[g] + kMove;
+          exceed |= s[g] - mo[g] > kMove;
         }
         // The references (uniform per query head over the group): the unit's first
         // tile sets them to its maxima, a reduction over the group; a later tile
@@ -1050,7 +1050,7 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               mold[rh * G + g] = mo[g];
-              mnew[rh * G + g] = tm[g] > mo[g] + kMove ? tm[g] - kLow : mo[g];
+              mnew[rh * G + g] = tm[g] - mo[g] > kMove ? tm[g] - kLow : mo[g];
             }
           }
           wg_sync(grp);
@@ -1076,7 +1076,7 @@ decode_tc_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmK,
           tc_fence_before();
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            if (tm[g] > mo[g] + kMove) {
+            if (tm[g] - mo[g] > kMove) {
               ao[g] = mo[g] == -CUDART_INF_F ? 1.f : exp2f(mo[g] - (tm[g] - kLow));
               mo[g] = tm[g] - kLow;
             }

@@ -267,8 +267,8 @@ struct Core {
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (__any_sync(0xffffffffu, mx > m + kMove || (BSC && mr > r + kSumMove))) {
-      const float mn = mx > m + kMove ? floorf(mx) - kLow : m;
+    if (__any_sync(0xffffffffu, mx - m > kMove || (BSC && mr > r + kSumMove))) {
+      const float mn = mx - m > kMove ? floorf(mx) - kLow : m;
       const float alpha = ex2(m - mn);
       m = mn;
       if (!BSC) l *= alpha;

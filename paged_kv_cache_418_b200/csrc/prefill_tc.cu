@@ -37,7 +37,7 @@
 // rescaled in tensor memory, each half by its thread): by 2^64 with bf16 weights.
 // f16 weights end at 2^16 above and at 2^-24 below: their reference lies 2^12
 // under the maximum (so that small weights beside a dominating one keep their
-// bits) and moves when a tile passes it by 2^15.9. References are
+// bits) and moves when a tile passes it by 2^15.5. References are
 // floored at -FLT_MAX so masked scores (-inf) give weight 0 without a guard.
 // Keys past a row's position are masked; the V rows of keys that no row of
 // the unit attends (past its last position, or in a block with a bad id) are
@@ -179,7 +179,7 @@ prefill_fa_kernel(const FaArgs a, const __grid_constant__ CUtensorMap tmQ,
   constexpr uint32_t IDESC_S = make_idesc(FMT, 0, 0, kTile, kM);
   constexpr uint32_t IDESC_O = make_idesc(FMT, 0, 1, kD, kM);
   // a reference lies 2^kLow under its maximum and moves when passed by 2^kMove
-  constexpr float kLow = FMT == 1 ? 0.f : 12.f, kMove = FMT == 1 ? 64.f : 15.9f;
+  constexpr float kLow = FMT == 1 ? 0.f : 12.f, kMove = FMT == 1 ? 64.f : 15.5f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -524,7 +524,7 @@ prefill_fa_kernel(const FaArgs a, const __grid_constant__ CUtensorMap tmQ,
         bool resc = false;
         if (k == 0) {
           m = fmaxf(tm - kLow, -FLT_MAX);
-        } else if (tm > m + kMove) {
+        } else if (tm - m > kMove) {
           resc = true;
           alpha = ex2(m - (tm - kLow));
           m = tm - kLow;

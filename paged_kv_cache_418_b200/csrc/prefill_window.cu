@@ -24,7 +24,7 @@
 // f16 weights (f16 and 8-bit V) end at 2^-24. One key that takes most of the weight (the first
 // tokens that a window keeps are there for that) would leave every other weight on the last
 // steps of that grid, so their reference lies 2^12 under the maximum: the largest weight of a row
-// is in [2^12, 2^15.9], and what the grid takes from a weight is 2^-37 of that. (Lower would move
+// is in [2^12, 2^15.5], and what the grid takes from a weight is 2^-37 of that. (Lower would move
 // the reference with every other tile: the scores of a random prompt rise by 2^2 to 2^3 after
 // the first 64 keys. Moves at this height: 8192-token prompt 640 -> 655 us.)
 // 8-bit pools: four converter warps widen each tile's codes to f16 (exactly, in place:
@@ -413,8 +413,9 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   constexpr int FS = K8 ? 0 : FMT, FO = V8 ? 0 : FMT;     // operand types of the two products
   // The reference of a row is set 2^kLow under its maximum and moves when a half tile passes it
   // by 2^kMove: rarely, as that waits for the output product in flight. f16 weights stay under
-  // 2^15.9 < 65504; bf16 ones leave room for 2^60 of values and sums in fp32.
-  constexpr float kLow = FO == 1 ? 0.f : 12.f, kMove = FO == 1 ? 64.f : 15.9f;
+  // 65504, with half a power of two for a score whose maximum was rounded to fp32 before m was
+  // subtracted; bf16 ones leave room for 2^60 of values and sums in fp32.
+  constexpr float kLow = FO == 1 ? 0.f : 12.f, kMove = FO == 1 ? 64.f : 15.5f;
   constexpr float kSumMove = 8.f;               // BSC: r moves when passed by 2^8
   using R = Roles<CONV>;
   constexpr int NB_T = kTile / BS;              // physical blocks per tile
@@ -895,17 +896,17 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             tm = fmaxf(tm, tc[c]);
           }
           // the references, in one vote: all of this is rare, but for masked halves
-          bool move = tm > m + kMove;
+          bool move = tm - m > kMove;
           if constexpr (BSC) move = move || tm - lvmin > m - back_m + kSumMove || lvmin < back_m - 51.f;
           if (first || __any_sync(0xffffffffu, move)) {
             const float mn = tm - kLow, mo = m;
             if (first) {
               m = fmaxf(mn, -FLT_MAX);
-            } else if (__any_sync(0xffffffffu, tm > m + kMove)) {
+            } else if (__any_sync(0xffffffffu, tm - m > kMove)) {
               // rescale the row of O, once every product before this half's is in it: those of
               // the last tile's second half (the scores of this tile's come after it), or that
               // of this tile's first half
-              const bool resc = tm > m + kMove;
+              const bool resc = tm - m > kMove;
               const float alpha = resc ? ex2(m - mn) : 1.f;
               if (resc) m = mn;
               if (!pipe_wait(bar(h == 0 ? B_SFULL + 2 * qt + 1 : B_OSTEP + qt), n & 1, abort_flag)) failed = true;

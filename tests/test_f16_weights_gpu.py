@@ -112,3 +112,31 @@ def test_shared_prefix_decode(kind, qt, kt, vt, Hq, Hkv):
         ref, tol = attend(q[b].double(), c.k64[b], c.v64[b], sees(n, n - 1, 0, 0), D ** -0.5, rel, floor)
         for g in (0, groups // 2, groups - 1):
             check(out[3 * g + b], ref, tol, f"sequence {b} of group {g}")
+
+
+@pytest.mark.parametrize("call", ["prefill", "prefill mq", "decode", "window decode", "window prefill"])
+def test_scores_of_millions(monkeypatch, call):
+    """Scores near 4e6, where fp32 steps are 1/4 and more, that rise by halves: the weights stay inside f16
+    (what remains of the softmax is a matter of rounding; the rows are means of the values all the same)."""
+    n, T, Hq, Hkv = 1500, 1 if "decode" in call else 40, 16, 4
+    monkeypatch.setenv("PA_DECODE_KERNEL", "tc")
+    monkeypatch.setenv("PA_PREFILL_KERNEL", "mq") if call.endswith("mq") else monkeypatch.delenv("PA_PREFILL_KERNEL", raising=False)
+    g = torch.Generator().manual_seed(1)
+    q, k = torch.zeros(T, Hq, D), torch.zeros(n, Hkv, D)
+    q[..., 0], q[..., 1] = 1000, 1
+    k[..., 0], k[..., 1] = 4000, (torch.arange(n) * 0.5)[:, None]
+    v = torch.rand(n, Hkv, D, generator=g) + 1
+    c = Cache([(k, v)], 16, "f16", "f16")
+    qd, out = q.half().cuda(), torch.full(q.shape, float("nan"), device="cuda")
+    qs = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    if call == "window decode":
+        ops.pa_decode_window_kv(out, qd, c.k, c.v, 1.0, 1.0, c.bt, c.cl, 1.0, n, 0, n, ops.window_workspace_for(qd, c.k, n, n, 0))
+    elif call == "window prefill":
+        ops.pa_prefill_window_kv(out, qd, c.k, c.v, 1.0, 1.0, c.bt, c.cl, qs, T, 1.0, n, 0, n)
+    elif call == "decode":
+        ops.pa_decode(out, qd, c.k, c.v, c.bt, c.cl, 1.0, n, 0, ops.workspace_for(qd, c.k, n))
+    else:
+        ops.pa_prefill(out, qd, c.k, c.v, c.bt, c.cl, qs, T, 1.0, n)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out).all())
+    assert float(out.min()) >= 0.99 and float(out.max()) <= 2.01
