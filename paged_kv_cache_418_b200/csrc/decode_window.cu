@@ -763,18 +763,6 @@ __global__ void __launch_bounds__(NW < 4 ? 128 : NW * 32) decode_window_merge_ke
 
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                                     cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-  }();
-  return fn;
-}
-
 // Pool [NB][bs][Hkv][D] seen as [NB][lines of a row][Hkv][bs][line]: a box of 16
 // tokens of hg heads, every line of their rows.
 bool make_map(const WinArgs& a, const void* pool, int dt, CUtensorMap* m) {

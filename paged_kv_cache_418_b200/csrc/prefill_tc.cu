@@ -658,28 +658,13 @@ prefill_fa_kernel(const FaArgs a, const __grid_constant__ CUtensorMap tmQ,
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 fa_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 // Query [T][Hq][128] seen as [T][Hq][2 d-halves][64]: a box of TPU tokens x G
 // heads x one d-half lands as 128 rows (token-major, then head) of 128 B,
 // 128-byte swizzled. Pools [NB][bs][Hkv][128] seen as [NB][2][Hkv][bs][64]: a
 // box of one block's bs rows of one head and one d-half.
 bool make_fa_maps(const PrefillLaunch& p, int G, bool k8, bool v8, CUtensorMap* q, CUtensorMap* k,
                   CUtensorMap* v) {
-  auto enc = fa_encode_fn();
+  auto enc = encode_fn();
   if (!enc || p.num_blocks <= 0) return false;
   const CUtensorMapDataType dt =
       p.dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;

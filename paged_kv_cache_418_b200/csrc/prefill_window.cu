@@ -1070,18 +1070,6 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
 
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                                     cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-  }();
-  return fn;
-}
-
 // Query [T][Hq][128] seen as [T][Hq][2 d-halves][64]: a box of 128 / G tokens x G heads
 // x one d-half lands as 128 rows (token-major, then head) of 128 B, 128-byte swizzled.
 // 16-bit pools [NB][bs][Hkv][128] seen as [NB][2][Hkv][bs][64]: a box of one block's rows
