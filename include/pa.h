@@ -578,7 +578,7 @@ int pa_decode_blk8(void* out, int out_dtype, const void* query, int q_dtype, con
  * pa_prefill_kv (num_blocks >= 1; a sequence whose query_start passes T also sets
  * PA_DEV_BAD_CTX). Sums and softmax statistics are fp32; the weights enter the
  * output product as two 16-bit parts; for a bf16 output over an 8-bit V pool as one
- * f16 value (off by up to 2^-11 of itself). Over f16 and 8-bit V each is off by 2^-36
+ * f16 value (off by up to 2^-11 of itself). Over f16 and 8-bit V each is off by 2^-34
  * of the row's largest besides. As there, the query rows of neighbouring tokens (up to 256 / G
  * of them) meet the same key tiles: an infinite or NaN V element of a token that
  * one of them attends may reach the others' rows.

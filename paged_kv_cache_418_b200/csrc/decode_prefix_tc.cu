@@ -21,7 +21,7 @@
 // column is set on the unit's first tile (an exact column max) and moves only
 // when a score passes it by far (then O's columns are rescaled in TMEM): by 2^64
 // with bf16 weights. f16 weights end at 2^16 above and at 2^-24 below: their
-// reference lies 2^12 under the maximum (so that small weights beside a dominating
+// reference lies 2^10 under the maximum (so that small weights beside a dominating
 // one keep their bits) and moves when passed by 2^15.9. So a
 // tile needs no reduction across threads; the column sums l are per-thread
 // partial sums reduced once per unit. A score enters as one FMA against its
@@ -201,7 +201,7 @@ multi_query_tc_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap tm
                       const __grid_constant__ CUtensorMap tmV) {
   constexpr int NB_T = kTile / BS;              // physical blocks per tile
   // a reference lies 2^kLow under its maximum and moves when passed by 2^kMove
-  constexpr float kLow = FMT == 1 ? 0.f : 12.f, kMove = FMT == 1 ? 64.f : 15.9f;
+  constexpr float kLow = FMT == 1 ? 0.f : 10.f, kMove = FMT == 1 ? 64.f : 15.9f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));

@@ -35,7 +35,7 @@
 // maximum of a row is its first tile's maximum
 // and moves only when a later tile exceeds it by far (then the row's O is
 // rescaled in tensor memory, each half by its thread): by 2^64 with bf16 weights.
-// f16 weights end at 2^16 above and at 2^-24 below: their reference lies 2^12
+// f16 weights end at 2^16 above and at 2^-24 below: their reference lies 2^10
 // under the maximum (so that small weights beside a dominating one keep their
 // bits) and moves when a tile passes it by 2^15.5. References are
 // floored at -FLT_MAX so masked scores (-inf) give weight 0 without a guard.
@@ -179,7 +179,7 @@ prefill_fa_kernel(const FaArgs a, const __grid_constant__ CUtensorMap tmQ,
   constexpr uint32_t IDESC_S = make_idesc(FMT, 0, 0, kTile, kM);
   constexpr uint32_t IDESC_O = make_idesc(FMT, 0, 1, kD, kM);
   // a reference lies 2^kLow under its maximum and moves when passed by 2^kMove
-  constexpr float kLow = FMT == 1 ? 0.f : 12.f, kMove = FMT == 1 ? 64.f : 15.5f;
+  constexpr float kLow = FMT == 1 ? 0.f : 10.f, kMove = FMT == 1 ? 64.f : 15.5f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));

@@ -23,10 +23,10 @@
 // (hi + lo, ~16 bits).
 // f16 weights (f16 and 8-bit V) end at 2^-24. One key that takes most of the weight (the first
 // tokens that a window keeps are there for that) would leave every other weight on the last
-// steps of that grid, so their reference lies 2^12 under the maximum: the largest weight of a row
-// is in [2^12, 2^15.5], and what the grid takes from a weight is 2^-37 of that. (Lower would move
-// the reference with every other tile: the scores of a random prompt rise by 2^2 to 2^3 after
-// the first 64 keys. Moves at this height: 8192-token prompt 640 -> 655 us.)
+// steps of that grid, so their reference lies 2^10 under the maximum: the largest weight of a row
+// is in [2^10, 2^15.5], and half a step of the grid is 2^-35 of that. (Lower moves the reference
+// more often, as the scores of a random prompt rise by 2^2 to 2^5 after the first keys: windowed
+// f16 chunks 269 us at 2^9 and 2^10, 287 at 2^11, 304 at 2^12.)
 // 8-bit pools: four converter warps widen each tile's codes to f16 (exactly, in place:
 // TMA leaves a row's 128 codes in the line of its second half) ahead of the tensor
 // cores; a bf16 query is rescaled by a power of two per row and becomes f16 too, exactly
@@ -415,7 +415,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
   // by 2^kMove: rarely, as that waits for the output product in flight. f16 weights stay under
   // 65504, with half a power of two for a score whose maximum was rounded to fp32 before m was
   // subtracted; bf16 ones leave room for 2^60 of values and sums in fp32.
-  constexpr float kLow = FO == 1 ? 0.f : 12.f, kMove = FO == 1 ? 64.f : 15.5f;
+  constexpr float kLow = FO == 1 ? 0.f : 10.f, kMove = FO == 1 ? 64.f : 15.5f;
   constexpr float kSumMove = 8.f;               // BSC: r moves when passed by 2^8
   using R = Roles<CONV>;
   constexpr int NB_T = kTile / BS;              // physical blocks per tile

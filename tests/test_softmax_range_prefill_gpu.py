@@ -9,11 +9,11 @@ from range_testlib import DT, Cache, attend, check, prefill, sees, sink, spread
 pytestmark = pytest.mark.gpu
 
 # Errors of a prefill's weights (fractions of the largest). f16 and 8-bit V pools: f16 weights of which
-# the largest is 2^12 or more, so that half a step of the last ones, 2^-25, is 2^-37 of it; of a weight,
-# two parts are off by 2^-21 and one (8-bit V with bf16 outputs) by 2^-11. bf16 V: two bf16 parts, 2^-17 and no
+# the largest is 2^10 or more, so that half a step of the last ones, 2^-25, is 2^-35 of it, and of each
+# of two parts; of a weight, two parts are off by 2^-21 and one (8-bit V with bf16 outputs) by 2^-11. bf16 V: two bf16 parts, 2^-17 and no
 # floor. ex2: 2^-22.
-PREFILL = {"f16": (2.0 ** -20, 2.0 ** -36), "fp8": (2.0 ** -20, 2.0 ** -36), "bf16": (2.0 ** -16, 0.0)}
-ONE = (2.0 ** -11 + 2.0 ** -20, 2.0 ** -36)
+PREFILL = {"f16": (2.0 ** -20, 2.0 ** -34), "fp8": (2.0 ** -20, 2.0 ** -34), "bf16": (2.0 ** -16, 0.0)}
+ONE = (2.0 ** -11 + 2.0 ** -20, 2.0 ** -34)
 
 
 def _run(q, c, n, T, window, sinks, vt, odt="f32"):
