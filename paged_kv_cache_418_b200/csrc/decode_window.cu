@@ -616,7 +616,7 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
       const size_t slot = 2 * (size_t)cta + (cta == first ? 1 : 0);
       const size_t prow = slot * (hg * kHeads) + hd * kHeads;          // of the pieces
       if (nsub == 1) {
-        const Norm norm = norm_of<BSC>(core.m - core.r, core.l, a.v_scale);
+        const Norm<BSC> norm = norm_of<BSC>(core.m - core.r, core.l, a.v_scale);
 #pragma unroll
         for (int s = 0; s < C::NS; s += 8) {
           float f[8];
@@ -653,7 +653,7 @@ decode_window_kernel(const WinArgs a, const __grid_constant__ CUtensorMap tmK,
           cf[x] = x < nsub ? ex2(sm_m[x * hg + hd][g] - M) : 0.f;
           if (x < nsub) L = fmaf(sm_l[x * hg + hd][g], BSC ? ex2(sm_r[x * hg + hd][g] - R) : cf[x], L);
         }
-        const Norm norm = norm_of<BSC>(M - R, L, a.v_scale);
+        const Norm<BSC> norm = norm_of<BSC>(M - R, L, a.v_scale);
         for (int s = sub * (C::NS / nsub); s < (sub + 1) * (C::NS / nsub); ++s) {
           float O = 0.f;
 #pragma unroll

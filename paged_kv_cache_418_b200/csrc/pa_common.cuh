@@ -150,15 +150,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A row's sums as the output wants them: O * f[0] * f[1] is O / l * 2^n * scale, with n (FAR) the
-// distance of O's reference over l's (two factors, as 2^n alone may leave fp32's range; exact
-// where n is a whole number).
-struct Norm {
+// A row's sums as the output wants them: O / l * scale, and with FAR * 2^n besides, n the distance
+// of O's reference over l's (in two factors, as 2^n alone may leave fp32's range; exact where n is
+// a whole number).
+template <bool FAR> struct Norm {
   float f[2];
-  __device__ __forceinline__ float operator()(float o) const { return o * f[0] * f[1]; }
+  __device__ __forceinline__ float operator()(float o) const { return FAR ? o * f[0] * f[1] : o * f[0]; }
 };
-template <bool FAR> __device__ __forceinline__ Norm norm_of(float n, float l, float scale) {
-  Norm x = {{l == 0.f ? 0.f : scale / l, 1.f}};
+template <bool FAR> __device__ __forceinline__ Norm<FAR> norm_of(float n, float l, float scale) {
+  Norm<FAR> x = {{l == 0.f ? 0.f : scale / l, 1.f}};
   if (FAR) {
     const float h = truncf(n * 0.5f);
     x.f[0] *= ex2(h);

@@ -902,7 +902,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
             const float mn = tm - kLow, mo = m;
             if (first) {
               m = fmaxf(mn, -FLT_MAX);
-            } else if (__any_sync(0xffffffffu, tm - m > kMove)) {
+            } else if (!BSC || __any_sync(0xffffffffu, tm - m > kMove)) {
               // rescale the row of O, once every product before this half's is in it: those of
               // the last tile's second half (the scores of this tile's come after it), or that
               // of this tile's first half
@@ -996,7 +996,7 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         failed = __any_sync(0xffffffffu, failed);
         continue;
       }
-      Norm na, nb;                               // of this part's O and of the second's
+      Norm<BSC> na, nb;                          // of this part's O and of the second's
       if (part.split) {
         if (!pipe_wait(bar(B_XCH), splits & 1, abort_flag)) failed = true;
         __syncwarp();
@@ -1006,8 +1006,12 @@ prefill_window_kernel(const Args a, const __grid_constant__ CUtensorMap tmQ,
         if (BSC) l2 = unpack_sum(l2, r2);
         const float top = fmaxf(r1, r2);
         l = fmaf(l, ex2(r1 - top), l2 * ex2(r2 - top));
-        na = norm_of<true>(m - top, l, a.v_scale);
-        nb = norm_of<true>(m2 - top, l, a.v_scale);
+        na = norm_of<BSC>(m - top, l, a.v_scale);
+        nb = norm_of<BSC>(m2 - top, l, a.v_scale);
+        if (!BSC) {                              // (m and m2 are at most top there)
+          na.f[0] *= ex2(m - top);
+          nb.f[0] *= ex2(m2 - top);
+        }
       } else {
         na = norm_of<BSC>(back_m, l, a.v_scale);
       }
