@@ -50,14 +50,15 @@
 // weights through tensor memory and, for 8-bit V, a widened copy of the tile in
 // shared memory.)
 //
-// Measured (one B200, copy rate 6.55 TB/s): 64 fp16 MHA sequences under a window of 1000
-// (846 MB) 143 us, 5.9 TB/s; 8 long bf16 GQA sequences under a window of 4096 (137 MB) 38.5
-// us, 3.5 TB/s; block-scaled GQA (550 MB) 109 us, 5.0 TB/s, and one long sequence (205 MB)
-// 50 us, 4.1 TB/s. In steady state a CTA runs at ~95% of its part of the copy rate; ~2 us go by
-// before a CTA knows its share, as much again until its first tile is there, ~5 with the
-// merge kernel, and the SMs' speeds differ by 7% either way. A ring of cp.async copies per
-// warp instead took 323, 43, 251 and 86 us; eight consumer warps without the register split
-// (whose producer then spills) 144, 41, 122 and 51.
+// Measured (one B200, copy rate 6.55 TB/s; calls back to back): 64 fp16 MHA sequences under a
+// window of 1000 (846 MB) 143-147 us, 5.8 TB/s; 8 long bf16 GQA sequences under a window of 4096
+// (137 MB) 39 us, 3.5 TB/s; block-scaled GQA (550 MB) 118-124 us (through a graph 115), 4.5 TB/s,
+// and one long sequence (205 MB) 53 us, 3.9 TB/s. In steady state a CTA runs at ~95% of its part
+// of the copy rate; ~2 us go by before a CTA knows its share, as much again until its first tile
+// is there, ~5 with the merge kernel, and the SMs' speeds differ by 7% either way. When those
+// figures were 142, 38, 109 and 50, a ring of cp.async copies per warp instead took 323, 43, 251
+// and 86 us, and eight consumer warps without the register split (whose producer then spills)
+// 144, 41, 122 and 51.
 //
 // Block-scaled pools: K's power of two multiplies the scores of its block's
 // tokens. V's would have to multiply the weights before they are rounded to
@@ -70,7 +71,7 @@
 // references are whole numbers, so that factor is exact. The second exponential per score
 // is 4 of a lane and box, beside the widening of 128 codes.
 //
-// Every pipeline wait is bounded (1 s): one that gives up sets PA_DEV_TIMEOUT,
+// Every pipeline wait is bounded (wait_ns, 1 s): one that gives up sets PA_DEV_TIMEOUT,
 // raises the CTA's abort flag, and the producer waits for its copies in flight.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -818,8 +819,10 @@ template <int D>
 int launch_merge_d(const WinArgs& a, cudaStream_t stream) {
   const long long rows = (long long)a.B * a.Hq;
   // warps per row by the pieces to expect: with few units most CTAs hold a part of
-  // one (one long sequence: 16 warps 50 us, one 71); with many, a unit is rarely cut in
-  // more than two or three (128 sequences, 8 KV heads: one warp 109 us, 16 warps 116)
+  // one, with many a unit is rarely cut in more than two or three. The whole decode of 200,000
+  // block-scaled tokens, 64 heads over 8, with 16 / 4 / 1 warps per row: 1 sequence 100 / 111 /
+  // 145 us, 8 102 / 100 / 104, 20 107 / 100 / 101, 70 129 / 104 / 100, 128 157 / 111 / 102;
+  // 8 heads over 1: 1 sequence 37 / 43 / 59, 16 33 / 34 / 37, 70 37 / 35 / 35.
   const long long units = rows / (a.hg * a.heads) + 1;
   cudaError_t e;
   if (units <= a.grid / 8)

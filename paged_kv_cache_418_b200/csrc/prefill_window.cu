@@ -36,12 +36,16 @@
 // cache: 661 us with one part, 792 with two).
 //
 // Where a unit has one query tile only, both groups take every other key tile of it, and
-// the first joins the two parts (small ragged chunks: 17.9 -> 16.2 us).
+// the first joins the two parts (small ragged chunks: 17.9 -> 16.2 us; with two weight parts and
+// the row sum's own reference 18.7).
 //
-// Measured (8192-token prompt, 32 query heads over 8, 550 GFLOP): block-scaled cache 629
-// us, 875 TFLOP/s; bf16 pools 670 us; windowed bf16 chunks (8 x 512) 270 us. Units of one
-// query tile whose rows two threads share took 763, 925 and 298 us there, and with the codes
-// widened by the softmax warps 2110. A pair of tiles takes ~5000 cycles: a softmax warp
+// Measured (8192-token prompt, 32 query heads over 8, 550 GFLOP; calls back to back):
+// block-scaled cache with bf16 output 681 us, 807 TFLOP/s, with f16 output (two weight parts)
+// 810-860; 8-bit pools without block scales 613-669; bf16 pools 736-800. Windowed chunks (8 x
+// 512) 274 us in bf16, 261-272 in f16. (The ranges are of several boxes and of the power limit,
+// which the longer ones reach.) Units of one query tile whose rows two threads share took 763 us
+// on the prompt and 298 on the bf16 chunks when this layout took 629 and 270, and with the codes
+// widened by the softmax warps 2110. A pair of tiles took ~5000 cycles at 629 us: a softmax warp
 // ~2100 for each half (some 1100 of them its 64 exponentials, beside the other query
 // tile's) without ever waiting for scores; the tensor cores are busy for 2048 of them,
 // shared memory for ~3000 (the operand of S that is the query is read once per 64 keys),

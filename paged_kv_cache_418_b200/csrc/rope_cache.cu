@@ -186,7 +186,9 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, int t, int c, int 
 // CTA's 128 threads, and over blockIdx.y when there are few tokens. Five heads of a
 // thread in flight: one round for 64 + 8 + 8 heads of 128. (At 8 x 512 such bf16
 // tokens, 170 MB: 256 threads and two heads 34.1 us, 128 and five 29.9 us, 5.7 TB/s,
-// 87% of a plain copy.)
+// 87% of a plain copy. The same bytes with other numbers of heads, 2 / 3 / 5 / 8 in flight,
+// with a cold L2: 128 + 8 + 8 43 / 43 / 41 / 39 us, 32 + 32 + 32 41 with each, 32 + 8 + 8
+// 45 / 43 / 47 / 49, 16 + 2 + 2 61 / 61 / 74 / 76.)
 template <typename TS, bool IL>
 __global__ void __launch_bounds__(128, 4)
 rope_and_cache_kernel(const RopeArgs a) {
@@ -448,7 +450,10 @@ int launch_rope_t(const RopeArgs& a, bool blk8, cudaStream_t stream) {
   if (blk8) {
     // Tokens per CTA: one while that leaves a warp per (token, head, K or V) in two
     // waves of the GPU (a decode step: every token is a run of its own); else 16, of
-    // which a chunk's runs leave about one per CTA.
+    // which a chunk's runs leave about one per CTA. With one / 16, 64 + 8 + 8 heads: a step of
+    // 128 tokens 12 / 51 us, of 296 16 / 55, of 512 23 / 55, of 2048 61 / 78; a chunk of 512
+    // 18 / 14 us, of 2048 41 / 29 (32 + 32 + 32 heads: 80 / 37). The host cannot see which of
+    // the two a call is: past the limit a step pays for the chunks.
     const int ys = (2 * a.Hkv + 7) / 8;
     const int tb = (long long)a.T * ys <= 4 * kSMs ? 1 : 16;
     const long long kv = ((long long)a.T + tb - 1) / tb * ys;
