@@ -543,6 +543,10 @@ int pa_copy_scales(float* dst_k_scales, float* dst_v_scales, const float* src_k_
  *               256-byte aligned; its contents do not matter before or after.
  *               Calls that may run at the same time need one each.
  * num_blocks    >= 1. Other arguments, types, shapes and errors as pa_decode_kv.
+ * Sums and softmax statistics are fp32; over 16- and 8-bit V pools the weights enter
+ * the output product as two 16-bit parts: off by 2^-17 of themselves over bf16 V, by
+ * 2^-22 of themselves and 2^-43 of the row's largest over f16 and 8-bit V (of the
+ * largest weight times V scale, with block scales).
  */
 size_t pa_window_workspace_size(int B, int Hq, int Hkv, int D, int max_context_len, int window,
                                 int num_sinks);
@@ -579,9 +583,10 @@ int pa_decode_blk8(void* out, int out_dtype, const void* query, int q_dtype, con
  * PA_DEV_BAD_CTX). Sums and softmax statistics are fp32; the weights enter the
  * output product as two 16-bit parts; for a bf16 output over an 8-bit V pool as one
  * f16 value (off by up to 2^-11 of itself). Over f16 and 8-bit V each is off by 2^-34
- * of the row's largest besides. As there, the query rows of neighbouring tokens (up to 256 / G
- * of them) meet the same key tiles: an infinite or NaN V element of a token that
- * one of them attends may reach the others' rows.
+ * of the row's largest besides (of weight times V scale, with block scales). As
+ * there, the query rows of neighbouring tokens (up to 256 / G of them) meet the same
+ * key tiles: an infinite or NaN V element of a token that one of them attends may
+ * reach the others' rows.
  *
  * pa_prefill_blk8 -- the same over the block-scaled 8-bit cache (scales and
  * their errors as pa_decode_blk8); window 0: every earlier token.
